@@ -59,6 +59,15 @@ _SIGS = {
     "bsfp8_workspace_bytes_mxfp8": (_SZ, [_I64, _I64, _I64, _I64, _I]),
     "bsfp8_gemm_mxfp8": (_I, [_P, _I64, _I64, _I64, _I64, _I64, _P, _P, _I, _P, _SZ, _P, _P, _P]),
     "bsfp8_workspace_bytes_mxfp8_config": (_SZ, [_I64, _I64, _I64, _I64, _I, _I]),
+    "bsfp8_cache_write": (_I, [_P, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I64, _P, _P, _P, ctypes.c_float, _P, _I64,
+                               _I64, _P, _I, _P]),
+    "bsfp8_cache_read": (_I, [_P, _P, _I64, _P, _P, _P]),
+    "bsfp8_attention_workspace_bytes": (_SZ, [_I64] * 6),
+    "bsfp8_tree_attention": (_I, [_P, _I64, _I64, _I64, _I64, _P, _P, _I64, _P, _P, _P, ctypes.c_float, _I64, _P, _SZ,
+                                  _P, _P]),
+    "bsfp8_verify_workspace_bytes": (_SZ, [_I64] * 3),
+    "bsfp8_verify_chain": (_I, [_P, _P, _I, _I64, _I64, _I64, _P, _P, _P, _P, _P, _SZ, _P, _P, _P]),
+    "bsfp8_verify_tree": (_I, [_P, _I, _I64, _I64, _I64, _P, _P, _P, _P, _P, _SZ, _P, _P, _P, _P]),
     "bsfp8_gemm_mxfp8_config": (_I, [_P, _I64, _I64, _I64, _I64, _I64, _P, _P, _I, _I, _P, _SZ, _P, _P, _P]),
 }
 
@@ -622,3 +631,242 @@ def bsfp8_gemm_mxfp8_config(x, q, e, cfg, cps, ws=None, yq=None, ys=None):
     _check(lib().bsfp8_gemm_mxfp8_config(_ptr(x), ldx, M, G, N, K, _ptr(q), _ptr(e), cfg, cps, _ptr(ws), wsb,
                                          _ptr(yq), _ptr(ys), _stream(x)), "bsfp8_gemm_mxfp8_config")
     return yq, ys
+
+
+# ------------------------------------------------------------------------------------------------
+# the verify step: paged MXFP8 key/value cache, attention of drafted tokens, verification of drafts
+# ------------------------------------------------------------------------------------------------
+class _KVCacheStruct(ctypes.Structure):
+    _fields_ = [("kq", _P), ("ks", _P), ("vq", _P), ("vs", _P), ("pages", _I64), ("heads", _I64), ("page", _I64),
+                ("dim", _I64)]
+
+
+class KVCache:
+    """A paged key/value cache in MXFP8: codes kq, vq [pages, heads, page, dim] (uint8 or float8_e4m3fn) and scale
+    bytes ks, vs [pages, heads, page, dim/32] (uint8 or float8_e8m0fnu), contiguous, on one GPU. The tensors stay the
+    caller's; the handle keeps them alive. dim: 64, 128, 192 or 256; page: a multiple of 16."""
+
+    def __init__(self, kq, ks, vq, vs):
+        kq, vq = _codes(kq), _codes(vq)
+        ks, vs = (s.view(torch.uint8) if s.dtype == torch.float8_e8m0fnu else s for s in (ks, vs))
+        if kq.dim() != 4:
+            raise ValueError("kq must be [pages, heads, page, dim]")
+        pages, heads, page, dim = kq.shape
+        if dim not in (64, 128, 192, 256) or page < 16 or page % 16:
+            raise ValueError(f"dim must be 64, 128, 192 or 256 and page a multiple of 16, got {dim} and {page}")
+        for t, name, w in ((kq, "kq", dim), (ks, "ks", dim // 32), (vq, "vq", dim), (vs, "vs", dim // 32)):
+            _need(t, torch.uint8, name, device=kq.device)
+            if tuple(t.shape) != (pages, heads, page, w):
+                raise ValueError(f"{name} must be {(pages, heads, page, w)}, got {tuple(t.shape)}")
+        self.kq, self.ks, self.vq, self.vs = kq, ks, vq, vs
+        self.pages, self.heads, self.page, self.dim, self.device = pages, heads, page, dim, kq.device
+        self._struct = _KVCacheStruct(kq.data_ptr(), ks.data_ptr(), vq.data_ptr(), vs.data_ptr(), pages, heads, page, dim)
+        self._ref = ctypes.addressof(self._struct)
+
+    @classmethod
+    def empty(cls, pages, heads, page, dim, device="cuda"):
+        """A zeroed cache (zero codes with the smallest scale)."""
+        return cls(*(torch.zeros((pages, heads, page, w), dtype=torch.uint8, device=device)
+                     for w in (dim, dim // 32, dim, dim // 32)))
+
+
+def _cache(cache):
+    if not isinstance(cache, KVCache):
+        raise TypeError("cache must be a KVCache")
+    return cache
+
+
+def _vec(t, dtype, name, shape, device):
+    """_need, and the exact shape."""
+    _need(t, dtype, name, device=device)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _heads_view(x, name, R, heads, dim, device):
+    """bf16 rows of heads, [R, heads, dim] or [R, heads * dim] with any row stride -> (pointer, row stride)."""
+    if not isinstance(x, torch.Tensor) or x.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be a bf16 tensor")
+    if x.device != device:
+        raise ValueError(f"{name} is on {x.device}, expected {device}")
+    shape, stride = x.shape, x.stride()
+    if len(shape) == 3 and heads is None:
+        heads = shape[1]
+    elif heads is None:
+        heads = shape[1] // dim if len(shape) == 2 else -1
+    ok = (len(shape) == 3 and shape[1] == heads and shape[2] == dim and stride[2] == 1 and (heads <= 1 or stride[1] == dim)
+          or len(shape) == 2 and shape[1] == heads * dim and stride[1] == 1)
+    if not ok or shape[0] != R:
+        raise ValueError(f"{name} must be [{R}, heads, {dim}] with strides (any, {dim}, 1), got {list(shape)}, {list(stride)}")
+    return x.data_ptr(), stride[0] if R > 1 else max(heads, 1) * dim, heads
+
+
+def bsfp8_cache_write(cache, slots, k, v, q=None, q_out=None, q_weight=None, k_weight=None, eps=1e-6, cos_sin=None,
+                      positions=None, interleaved=False):
+    """Write tokens into the cache, normalising and rotating queries and keys on the way.
+
+    k, v: bf16 [R, heads, dim] (or [R, heads * dim]), any row stride; q likewise, or None. slots: int64 [R]. q_weight,
+    k_weight: bf16 [dim] norm weights or None. cos_sin: fp32 [n_positions, rot] with positions int64 [R], or None.
+    Returns q_out (bf16 [R, hq, dim], allocated when None), or None without q."""
+    c = _cache(cache)
+    dev, D = c.device, c.dim
+    R = k.shape[0]
+    ps = _vec(slots, torch.int64, "slots", (R,), dev)
+    pk, ldk, _ = _heads_view(k, "k", R, c.heads, D, dev)
+    pv, ldv, _ = _heads_view(v, "v", R, c.heads, D, dev)
+    pq = pqo = ldq = hq = 0
+    if q is not None:
+        pq, ldq, hq = _heads_view(q, "q", R, None, D, dev)
+        if q_out is None:
+            q_out = torch.empty((R, hq, D), dtype=torch.bfloat16, device=dev)
+        _need(q_out, torch.bfloat16, "q_out", device=dev)
+        if q_out.numel() != R * hq * D:
+            raise ValueError(f"q_out holds {q_out.numel()} values, expected {R * hq * D}")
+        pqo = q_out.data_ptr()
+    elif q_out is not None or q_weight is not None:
+        raise ValueError("q_out and q_weight need q")
+    pqw = _vec(q_weight, torch.bfloat16, "q_weight", (D,), dev) if q_weight is not None else 0
+    pkw = _vec(k_weight, torch.bfloat16, "k_weight", (D,), dev) if k_weight is not None else 0
+    pcs = pp = n_pos = rot = 0
+    if cos_sin is not None:
+        _need(cos_sin, torch.float32, "cos_sin", device=dev)
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be [n_positions, rot]")
+        n_pos, rot = cos_sin.shape
+        pcs, pp = cos_sin.data_ptr(), _vec(positions, torch.int64, "positions", (R,), dev)
+    st = lib().bsfp8_cache_write(c._ref, ps, R, pk, ldk, pv, ldv, pq, ldq, hq, pqo, pqw, pkw, eps, pcs, n_pos, rot, pp,
+                                 1 if interleaved else 0, _stream(k))
+    _check(st, "bsfp8_cache_write")
+    return q_out
+
+
+def bsfp8_cache_read(cache, slots, k_out=None, v_out=None):
+    """Cache rows slots int64 [R] -> (k, v) bf16 [R, heads, dim]; a slot outside the cache gives zeros."""
+    c = _cache(cache)
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
+        raise ValueError("slots must be [R]")
+    R = slots.shape[0]
+    ps = _vec(slots, torch.int64, "slots", (R,), c.device)
+    shape = (R, c.heads, c.dim)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=c.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=c.device)
+    pk = _vec(k_out, torch.bfloat16, "k_out", shape, c.device)
+    pv = _vec(v_out, torch.bfloat16, "v_out", shape, c.device)
+    _check(lib().bsfp8_cache_read(c._ref, ps, R, pk, pv, _stream(slots)), "bsfp8_cache_read")
+    return k_out, v_out
+
+
+def bsfp8_attention_workspace_bytes(B, T, hq, hkv, dim, max_len):
+    return int(lib().bsfp8_attention_workspace_bytes(B, T, hq, hkv, dim, max_len))
+
+
+def workspace_attention(B, T, hq, hkv, dim, max_len, device="cuda"):
+    """A workspace tensor for bsfp8_tree_attention with these sizes (its contents need no clearing)."""
+    return torch.empty(bsfp8_attention_workspace_bytes(B, T, hq, hkv, dim, max_len), dtype=torch.uint8, device=device)
+
+
+def bsfp8_tree_attention(q, cache, pages, lens, nodes=None, mask=None, scale=None, max_len=None, ws=None, out=None):
+    """Attention of the drafted tokens q bf16 [B, T, hq, dim] over the cache -> bf16 [B, T, hq, dim].
+
+    pages: int32 [B, W] page table; lens: int32 [B] tokens held, the drafted ones last; nodes: int32 [B] drafted tokens
+    (None: T each; rows past it are zeros); mask: int64 [B, T], bit i of a node's word = it sees node i (None: a chain,
+    node t sees 0..t). scale: dim ** -0.5 when None. max_len: a bound of lens (None: W * page). q may be a slice of a
+    wider projection: heads and values contiguous, one stride between tokens."""
+    c = _cache(cache)
+    dev = c.device
+    if not isinstance(q, torch.Tensor) or q.dtype != torch.bfloat16:
+        raise TypeError("q must be a bf16 tensor")
+    if q.device != dev:
+        raise ValueError(f"q is on {q.device}, expected {dev}")
+    if q.dim() != 4 or q.shape[3] != c.dim:
+        raise ValueError(f"q must be [B, T, hq, {c.dim}], got {list(q.shape)}")
+    B, T, hq, D = q.shape
+    if q.is_contiguous():
+        ldq = hq * D
+    else:
+        sb, stt, sh, sd = q.stride()
+        ldq = stt if T > 1 else sb if B > 1 else hq * D
+        if sd != 1 or (hq > 1 and sh != D) or (B > 1 and T > 1 and sb != T * stt):
+            raise ValueError("q must have contiguous heads and one stride between tokens")
+    if not isinstance(pages, torch.Tensor) or pages.dim() != 2:
+        raise ValueError("pages must be [B, W]")
+    W = pages.shape[1]
+    pp = _vec(pages, torch.int32, "pages", (B, W), dev)
+    pl = _vec(lens, torch.int32, "lens", (B,), dev)
+    pn = _vec(nodes, torch.int32, "nodes", (B,), dev) if nodes is not None else 0
+    pm = _vec(mask, torch.int64, "mask", (B, T), dev) if mask is not None else 0
+    max_len = W * c.page if max_len is None else max_len
+    if ws is None:
+        ws = workspace_attention(B, T, hq, c.heads, D, max_len, device=dev)
+    _need(ws, torch.uint8, "ws", device=dev)
+    if out is None:
+        out = torch.empty((B, T, hq, D), dtype=torch.bfloat16, device=dev)
+    po = _vec(out, torch.bfloat16, "out", (B, T, hq, D), dev)
+    st = lib().bsfp8_tree_attention(q.data_ptr(), ldq, B, T, hq, c._ref, pp, W, pl, pn, pm,
+                                    D ** -0.5 if scale is None else scale, max_len, ws.data_ptr(), ws.numel(), po,
+                                    _stream(q))
+    _check(st, "bsfp8_tree_attention")
+    return out
+
+
+def bsfp8_verify_workspace_bytes(B, T, V):
+    return int(lib().bsfp8_verify_workspace_bytes(B, T, V))
+
+
+def workspace_verify(B, T, V, device="cuda"):
+    """A zero-filled workspace tensor for the verification calls with these sizes."""
+    return torch.zeros(bsfp8_verify_workspace_bytes(B, T, V), dtype=torch.uint8, device=device)
+
+
+def _verify_args(logits, ws, out_tokens, n_accepted):
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("logits must be fp32 or bf16")
+    _need(logits, logits.dtype, "logits")
+    if logits.dim() != 3:
+        raise ValueError("logits must be [B, T, V]")
+    B, T, V = logits.shape
+    dev = logits.device
+    ws = workspace_verify(B, T, V, device=dev) if ws is None else ws
+    _need(ws, torch.uint8, "ws", device=dev)
+    out_tokens = torch.empty((B, T), dtype=torch.int32, device=dev) if out_tokens is None else out_tokens
+    n_accepted = torch.empty((B,), dtype=torch.int32, device=dev) if n_accepted is None else n_accepted
+    _vec(out_tokens, torch.int32, "out_tokens", (B, T), dev)
+    _vec(n_accepted, torch.int32, "n_accepted", (B,), dev)
+    return B, T, V, dev, 1 if logits.dtype == torch.float32 else 0, ws, out_tokens, n_accepted
+
+
+def bsfp8_verify_chain(logits, draft, tokens, temperature, u, u_sample, ws=None, out_tokens=None, n_accepted=None):
+    """Verify a chain of T - 1 drafted tokens a sequence: logits [B, T, V] of the target and draft [B, T-1, V] of the
+    drafter (fp32 or bf16, alike), tokens int32 [B, T-1], temperature fp32 [B] (0: greedy), u fp32 [B, T-1] and u_sample
+    fp32 [B] uniform in [0, 1). -> (out_tokens int32 [B, T]: accepted tokens, the next one, -1s; n_accepted int32 [B])."""
+    B, T, V, dev, dt, ws, out_tokens, n_accepted = _verify_args(logits, ws, out_tokens, n_accepted)
+    pd = _vec(draft, logits.dtype, "draft", (B, T - 1, V), dev)
+    pt = _vec(tokens, torch.int32, "tokens", (B, T - 1), dev)
+    pe = _vec(temperature, torch.float32, "temperature", (B,), dev)
+    pu = _vec(u, torch.float32, "u", (B, T - 1), dev)
+    ps = _vec(u_sample, torch.float32, "u_sample", (B,), dev)
+    st = lib().bsfp8_verify_chain(logits.data_ptr(), pd, dt, B, T, V, pt, pe, pu, ps, ws.data_ptr(), ws.numel(),
+                                  out_tokens.data_ptr(), n_accepted.data_ptr(), _stream(logits))
+    _check(st, "bsfp8_verify_chain")
+    return out_tokens, n_accepted
+
+
+def bsfp8_verify_tree(logits, tokens, parents, temperature, u, ws=None, out_tokens=None, path=None, n_accepted=None):
+    """Verify a tree of drafted tokens a sequence: logits [B, T, V] (fp32 or bf16), tokens and parents int32 [B, T]
+    (node 0 the root), temperature fp32 [B] (0: greedy), u fp32 [B, T] uniform in [0, 1).
+    -> (out_tokens int32 [B, T]: accepted tokens, the next one, -1s; path int32 [B, T]: the path's nodes, -1s;
+    n_accepted int32 [B])."""
+    B, T, V, dev, dt, ws, out_tokens, n_accepted = _verify_args(logits, ws, out_tokens, n_accepted)
+    path = torch.empty((B, T), dtype=torch.int32, device=dev) if path is None else path
+    pp = _vec(path, torch.int32, "path", (B, T), dev)
+    pt = _vec(tokens, torch.int32, "tokens", (B, T), dev)
+    pr = _vec(parents, torch.int32, "parents", (B, T), dev)
+    pe = _vec(temperature, torch.float32, "temperature", (B,), dev)
+    pu = _vec(u, torch.float32, "u", (B, T), dev)
+    st = lib().bsfp8_verify_tree(logits.data_ptr(), dt, B, T, V, pt, pr, pe, pu, ws.data_ptr(), ws.numel(),
+                                 out_tokens.data_ptr(), pp, n_accepted.data_ptr(), _stream(logits))
+    _check(st, "bsfp8_verify_tree")
+    return out_tokens, path, n_accepted

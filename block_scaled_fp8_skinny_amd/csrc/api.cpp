@@ -168,6 +168,53 @@ int run_gemm_mxfp8(const GemmShape& s, const GemmPlan& p, const uint16_t* x, con
                                    gemm_partials_order(p), yq, ys, stream);
 }
 
+// Sizes of the cache (BSFP8_ESHAPE), its pointers and their alignment.
+int check_cache(const bsfp8_kv_cache* c) {
+  if (!c) return BSFP8_EINVAL;
+  if ((c->dim != 64 && c->dim != 128 && c->dim != 192 && c->dim != 256) || c->page < 16 || c->page % 16) return BSFP8_ESHAPE;
+  if (c->heads < 1 || c->heads > 65536 || c->pages < 0 || c->page >= ((int64_t)1 << 31)) return BSFP8_ESHAPE;
+  if (c->pages >= ((int64_t)1 << 31) || c->pages * c->page >= ((int64_t)1 << 31)) return BSFP8_ESHAPE;
+  if (c->pages == 0) return BSFP8_OK;
+  if (!c->kq || !c->ks || !c->vq || !c->vs) return BSFP8_EINVAL;
+  if (!aligned16(c->kq) || !aligned16(c->ks) || !aligned16(c->vq) || !aligned16(c->vs)) return BSFP8_ESTRIDE;
+  return BSFP8_OK;
+}
+inline size_t cache_codes(const bsfp8_kv_cache* c) { return (size_t)c->pages * c->heads * c->page * c->dim; }
+inline size_t rows_span(int64_t rows, int64_t ld, int64_t cols) { return ((size_t)(rows - 1) * ld + cols) * 2; }
+
+int check_attention_sizes(int64_t B, int64_t T, int64_t hq, int64_t hkv, int64_t dim, int64_t max_len) {
+  if (dim != 64 && dim != 128 && dim != 192 && dim != 256) return BSFP8_ESHAPE;
+  if (B < 0 || T < 1 || hkv < 1 || hkv > 65536 || hq < hkv || hq % hkv || hq > 64 * hkv || max_len < 0) return BSFP8_ESHAPE;
+  const int64_t lim = (int64_t)1 << 31;
+  if (max_len >= lim || B >= lim || T >= lim || B * T >= lim || B * T * hq >= lim) return BSFP8_ESHAPE;
+  // units of 128 positions of a head and a block of at least 16 rows are counted in 32 bits
+  const int64_t blocks = (T * (hq / hkv) + 15) / 16, units = max_len / 128 + 1;
+  if (B > 0 && (hkv * blocks >= lim || B * hkv * blocks >= lim / units)) return BSFP8_ESHAPE;
+  return BSFP8_OK;
+}
+
+int check_verify_sizes(int64_t B, int64_t T, int64_t V) {
+  if (B < 0 || B > (1 << 24) || T < 1 || T > 64 || V < 1 || V > (1 << 24)) return BSFP8_ESHAPE;
+  return BSFP8_OK;
+}
+// What the two verification calls have in common.
+int check_verify(const VerifyArgs& a, int dtype, size_t ws_bytes) {
+  if (dtype != BSFP8_LOGITS_BF16 && dtype != BSFP8_LOGITS_F32) return BSFP8_EINVAL;
+  const int st = check_verify_sizes(a.B, a.T, a.V);
+  if (st != BSFP8_OK || a.B == 0) return st;
+  if (!a.logits || !a.temperature || !a.out_tokens || !a.n_accepted) return BSFP8_EINVAL;
+  if (!aligned16(a.logits) || !aligned16(a.draft)) return BSFP8_ESTRIDE;
+  if (!a.ws || ws_bytes < verify_ws_bytes(a.B, a.T, a.V) || !aligned16(a.ws)) return BSFP8_EWORKSPACE;
+  const size_t n = (size_t)a.B * a.T * 4, es = dtype == BSFP8_LOGITS_F32 ? 4 : 2, d = (size_t)a.B * (a.T - 1);
+  const size_t per_node = a.u_sample ? d * 4 : n;   // tokens and u of a chain have no entry for the root
+  if (outputs_alias({{a.out_tokens, n}, {a.path, n}, {a.n_accepted, (size_t)a.B * 4}, {a.ws, ws_bytes}},
+                    {{a.logits, (size_t)a.B * a.T * a.V * es}, {a.draft, d * a.V * es}, {a.tokens, per_node},
+                     {a.parents, n}, {a.temperature, (size_t)a.B * 4}, {a.u, per_node},
+                     {a.u_sample, (size_t)a.B * 4}}))
+    return BSFP8_EINVAL;
+  return BSFP8_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -565,6 +612,114 @@ int bsfp8_gemm_mxfp8_config(const uint16_t* x, int64_t ldx, int64_t M, int64_t G
   st = plan_with(s, cfg, cps, &p);
   if (st != BSFP8_OK) return st;
   return run_gemm_mxfp8(s, p, x, q, e, ws, ws_bytes, yq, ys, /*fuse=*/false, as_stream(stream));
+}
+
+int bsfp8_cache_write(const bsfp8_kv_cache* cache, const int64_t* slots, int64_t R, const uint16_t* k, int64_t ldk,
+                      const uint16_t* v, int64_t ldv, const uint16_t* q, int64_t ldq, int64_t hq, uint16_t* q_out,
+                      const uint16_t* q_weight, const uint16_t* k_weight, float eps, const float* cos_sin,
+                      int64_t n_positions, int64_t rot, const int64_t* positions, int interleaved, void* stream) {
+  int st = check_cache(cache);
+  if (st != BSFP8_OK) return st;
+  const int64_t D = cache->dim, kv = cache->heads * D;
+  if (R < 0 || R >= ((int64_t)1 << 31) || hq < 0 || hq > (1 << 20) || rot < 0 || rot > D || rot % 16) return BSFP8_ESHAPE;
+  if (n_positions < 0) return BSFP8_ESHAPE;
+  if (!(eps >= 0.f) || eps > 3.4e38f || (interleaved != 0 && interleaved != 1)) return BSFP8_EINVAL;
+  if (R == 0) return BSFP8_OK;
+  if (!slots || !k || !v || (hq > 0 && (!q || !q_out)) || (rot > 0 && (!cos_sin || !positions))) return BSFP8_EINVAL;
+  if (ldk < kv || ldv < kv || ldk % 8 || ldv % 8 || (hq > 0 && (ldq < hq * D || ldq % 8))) return BSFP8_ESTRIDE;
+  if (!aligned16(k) || !aligned16(v) || (hq > 0 && (!aligned16(q) || !aligned16(q_out)))) return BSFP8_ESTRIDE;
+  if (!aligned16(q_weight) || !aligned16(k_weight) || (rot > 0 && !aligned16(cos_sin))) return BSFP8_ESTRIDE;
+  const size_t codes = cache_codes(cache);
+  const size_t qn = hq > 0 ? rows_span(R, ldq, hq * D) : 0, w = (size_t)D * 2;
+  if (outputs_alias({{hq > 0 ? q_out : nullptr, (size_t)R * hq * D * 2}, {cache->kq, codes}, {cache->ks, codes / 32},
+                     {cache->vq, codes}, {cache->vs, codes / 32}},
+                    {{k, rows_span(R, ldk, kv)}, {v, rows_span(R, ldv, kv)}, {hq > 0 ? q : nullptr, qn}, {q_weight, w},
+                     {k_weight, w}, {rot > 0 ? cos_sin : nullptr, (size_t)n_positions * rot * 4}, {slots, (size_t)R * 8},
+                     {rot > 0 ? positions : nullptr, (size_t)R * 8}}))
+    return BSFP8_EINVAL;
+  // an empty table knows no position: the kernel reads its first row for the lanes of unknown ones
+  if (rot > 0 && n_positions == 0) return BSFP8_ESHAPE;
+  const CacheWriteArgs a{*cache, slots, R, k, v, q, ldk, ldv, ldq, hq, q_out, q_weight, k_weight, eps, cos_sin, n_positions,
+                         rot, positions, interleaved};
+  return launch_cache_write(a, as_stream(stream));
+}
+
+int bsfp8_cache_read(const bsfp8_kv_cache* cache, const int64_t* slots, int64_t R, uint16_t* k_out, uint16_t* v_out,
+                     void* stream) {
+  const int st = check_cache(cache);
+  if (st != BSFP8_OK) return st;
+  if (R < 0 || R >= ((int64_t)1 << 31) || R * cache->heads >= ((int64_t)1 << 31)) return BSFP8_ESHAPE;
+  if (R == 0) return BSFP8_OK;
+  if (!slots || !k_out || !v_out) return BSFP8_EINVAL;
+  if (!aligned16(k_out) || !aligned16(v_out)) return BSFP8_ESTRIDE;
+  const size_t codes = cache_codes(cache), n = (size_t)R * cache->heads * cache->dim * 2;
+  if (outputs_alias({{k_out, n}, {v_out, n}}, {{cache->kq, codes}, {cache->ks, codes / 32}, {cache->vq, codes},
+                                               {cache->vs, codes / 32}, {slots, (size_t)R * 8}}))
+    return BSFP8_EINVAL;
+  return launch_cache_read(*cache, slots, R, k_out, v_out, as_stream(stream));
+}
+
+size_t bsfp8_attention_workspace_bytes(int64_t B, int64_t T, int64_t hq, int64_t hkv, int64_t dim, int64_t max_len) {
+  if (check_attention_sizes(B, T, hq, hkv, dim, max_len) != BSFP8_OK || B == 0) return 0;
+  AttentionArgs a{};
+  a.B = B;
+  a.T = T;
+  a.hq = hq;
+  a.cache.heads = hkv;
+  a.cache.dim = dim;
+  a.max_len = max_len;
+  return attention_ws_bytes(a);
+}
+
+int bsfp8_tree_attention(const uint16_t* q, int64_t ldq, int64_t B, int64_t T, int64_t hq, const bsfp8_kv_cache* cache,
+                         const int32_t* pages, int64_t ld_pages, const int32_t* lens, const int32_t* nodes,
+                         const int64_t* mask, float scale, int64_t max_len, void* ws, size_t ws_bytes, uint16_t* out,
+                         void* stream) {
+  int st = check_cache(cache);
+  if (st != BSFP8_OK) return st;
+  st = check_attention_sizes(B, T, hq, cache->heads, cache->dim, max_len);
+  if (st != BSFP8_OK) return st;
+  if (ld_pages < 0 || ld_pages >= ((int64_t)1 << 31) || (mask && T > 64)) return BSFP8_ESHAPE;
+  if (B == 0) return BSFP8_OK;
+  const int64_t D = cache->dim;
+  if (!q || !out || !lens || (ld_pages > 0 && !pages)) return BSFP8_EINVAL;
+  if (ldq < hq * D || ldq % 8 || !aligned16(q) || !aligned16(out)) return BSFP8_ESTRIDE;
+  const AttentionArgs a{q, ldq, B, T, hq, *cache, pages, ld_pages, lens, nodes, mask, scale, max_len, ws, out};
+  if (!ws || ws_bytes < attention_ws_bytes(a) || !aligned16(ws)) return BSFP8_EWORKSPACE;
+  const size_t codes = cache_codes(cache);
+  if (outputs_alias({{out, (size_t)B * T * hq * D * 2}, {ws, ws_bytes}},
+                    {{q, rows_span(B * T, ldq, hq * D)}, {cache->kq, codes}, {cache->ks, codes / 32}, {cache->vq, codes},
+                     {cache->vs, codes / 32}, {pages, (size_t)B * ld_pages * 4}, {lens, (size_t)B * 4},
+                     {nodes, (size_t)B * 4}, {mask, (size_t)B * T * 8}}))
+    return BSFP8_EINVAL;
+  return launch_tree_attention(a, as_stream(stream));
+}
+
+size_t bsfp8_verify_workspace_bytes(int64_t B, int64_t T, int64_t V) {
+  return check_verify_sizes(B, T, V) == BSFP8_OK && B > 0 ? verify_ws_bytes(B, T, V) : 0;
+}
+
+int bsfp8_verify_chain(const void* logits, const void* draft, int dtype, int64_t B, int64_t T, int64_t V,
+                       const int32_t* tokens, const float* temperature, const float* u, const float* u_sample, void* ws,
+                       size_t ws_bytes, int32_t* out_tokens, int32_t* n_accepted, void* stream) {
+  if (T <= 1) draft = nullptr;
+  const VerifyArgs a{logits, draft, dtype == BSFP8_LOGITS_F32, B, T, V, tokens, nullptr, temperature, u, u_sample, ws,
+                     out_tokens, nullptr, n_accepted};
+  const int st = check_verify(a, dtype, ws_bytes);
+  if (st != BSFP8_OK || B == 0) return st;
+  if (!u_sample || (T > 1 && (!draft || !tokens || !u))) return BSFP8_EINVAL;
+  return launch_verify(a, false, as_stream(stream));
+}
+
+int bsfp8_verify_tree(const void* logits, int dtype, int64_t B, int64_t T, int64_t V, const int32_t* tokens,
+                      const int32_t* parents, const float* temperature, const float* u, void* ws, size_t ws_bytes,
+                      int32_t* out_tokens, int32_t* path, int32_t* n_accepted, void* stream) {
+  const VerifyArgs a{logits, nullptr, dtype == BSFP8_LOGITS_F32, B, T, V, tokens, parents, temperature, u, nullptr, ws,
+                     out_tokens, path, n_accepted};
+  const int st = check_verify(a, dtype, ws_bytes);
+  if (st != BSFP8_OK || B == 0) return st;
+  if (!u || !path || (T > 1 && (!tokens || !parents))) return BSFP8_EINVAL;
+  return launch_verify(a, true, as_stream(stream));
 }
 
 }  // extern "C"

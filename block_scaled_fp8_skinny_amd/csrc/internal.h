@@ -103,6 +103,55 @@ int scratch_for_stream(hipStream_t stream, void** out);
 // Zero-fills `bytes` (a multiple of 16) at p with a kernel on `stream`.
 int launch_clear(void* p, size_t bytes, hipStream_t stream);
 
+// The verify step: the paged MXFP8 key/value cache (cache.hip), attention of drafted tokens over it
+// (attention.hip) and verification of the drafts (verify.hip). Arguments are checked by the caller.
+struct CacheWriteArgs {
+  bsfp8_kv_cache cache;
+  const int64_t* slots;
+  int64_t R;
+  const uint16_t *k, *v, *q;
+  int64_t ldk, ldv, ldq, hq;
+  uint16_t* q_out;
+  const uint16_t *q_weight, *k_weight;
+  float eps;
+  const float* cos_sin;
+  int64_t n_positions, rot;
+  const int64_t* positions;
+  int interleaved;
+};
+int launch_cache_write(const CacheWriteArgs& a, hipStream_t stream);
+int launch_cache_read(const bsfp8_kv_cache& c, const int64_t* slots, int64_t R, uint16_t* k_out, uint16_t* v_out,
+                      hipStream_t stream);
+
+struct AttentionArgs {
+  const uint16_t* q;
+  int64_t ldq, B, T, hq;
+  bsfp8_kv_cache cache;
+  const int32_t* pages;
+  int64_t ld_pages;
+  const int32_t *lens, *nodes;
+  const int64_t* mask;
+  float scale;
+  int64_t max_len;
+  void* ws;
+  uint16_t* out;
+};
+// Workspace for the sizes in a (pointers, strides and the cache's page count are not read).
+size_t attention_ws_bytes(const AttentionArgs& a);
+int launch_tree_attention(const AttentionArgs& a, hipStream_t stream);
+
+struct VerifyArgs {
+  const void *logits, *draft;            // draft null: a tree
+  int f32;
+  int64_t B, T, V;
+  const int32_t *tokens, *parents;
+  const float *temperature, *u, *u_sample;
+  void* ws;
+  int32_t *out_tokens, *path, *n_accepted;
+};
+size_t verify_ws_bytes(int64_t B, int64_t T, int64_t V);
+int launch_verify(const VerifyArgs& a, bool tree, hipStream_t stream);
+
 inline int hip_status(hipError_t err) { return err == hipSuccess ? BSFP8_OK : BSFP8_EHIP; }
 
 }  // namespace bsfp8

@@ -319,6 +319,138 @@ BSFP8_API int bsfp8_gemm_mxfp8(const uint16_t* x, int64_t ldx, int64_t M, int64_
                                const uint8_t* q, const uint8_t* e, int split_k, void* ws, size_t ws_bytes,
                                uint8_t* yq, uint8_t* ys, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * The verify step of speculative decoding (per call, asynchronous, no allocation): the paged
+ * MXFP8 key/value cache, attention of drafted tokens over it, and verification of the drafts.
+ *
+ * The decode and verify projections above run on a root token and a handful of drafted tokens
+ * per sequence; these calls are what such a step does between them.
+ * ------------------------------------------------------------------------------------------ */
+
+/* A paged key/value cache in MXFP8 (the format of bsfp8_quantize_mx along the head dimension):
+ *   kq, vq : uint8_t e4m3 codes [pages][heads][page][dim] (device, 16-byte aligned);
+ *   ks, vs : uint8_t scale bytes [pages][heads][page][dim/32] (device, 16-byte aligned), 2^(byte-127).
+ * dim is 64, 128, 192 or 256; page (tokens per page) a multiple of 16; heads >= 1; pages >= 0 and
+ * pages * page < 2^31 (offsets inside the cache are 64-bit). Slot s is token s % page of page
+ * s / page. Every call below returns BSFP8_ESHAPE for sizes outside these, BSFP8_EINVAL for a
+ * missing pointer, BSFP8_ESTRIDE for a misaligned one. */
+typedef struct bsfp8_kv_cache {
+  uint8_t* kq;
+  uint8_t* ks;
+  uint8_t* vq;
+  uint8_t* vs;
+  int64_t pages, heads, page, dim;
+} bsfp8_kv_cache;
+
+/* Write R tokens into the cache, with the norms of queries and keys and the position rotation in
+ * the same pass. Per token r, in fp32 from the bf16 inputs:
+ *   queries and keys: y = x * 1/sqrt(mean(x^2) + eps) * weight over the head's dim values (skipped
+ *   where the weight is NULL), then the first `rot` values of the head are rotated by the angle of
+ *   positions[r]: (a, b) -> (a cos - b sin, b cos + a sin) for the pairs (i, i + rot/2), or
+ *   (2i, 2i + 1) when `interleaved` (skipped when rot is 0);
+ *   queries are rounded to bf16 into q_out; keys and values are quantised to MXFP8 (the rule of
+ *   bsfp8_quantize_mx, on the fp32 value: keys are not rounded to bf16 in between) into slots[r].
+ *   slots     : int64_t [R] (device). A slot outside [0, pages * page) (e.g. -1 for a padding row)
+ *               stores no key and value; its query is written all the same. Two rows of one call
+ *               with the same slot leave either row's values.
+ *   k, v      : bf16 [R][ldk], [R][ldv], head h at columns [h*dim, (h+1)*dim) (16-byte aligned; row
+ *               strides >= heads*dim, multiples of 8: slices of a fused projection).
+ *   q, q_out  : bf16 [R][ldq] with hq heads, and [R][hq][dim] contiguous; NULL with hq = 0.
+ *   q_weight, k_weight : bf16 [dim] (16-byte aligned), nullable. eps >= 0 and finite.
+ *   cos_sin   : float [n_positions][rot] (16-byte aligned): rot/2 cosines, then rot/2 sines.
+ *   rot       : 0 or a multiple of 16 up to dim (cos_sin and positions are not read when 0).
+ *   positions : int64_t [R] (device). A position outside [0, n_positions) gives NaN in the rotated
+ *               values (and so a NaN block, scale byte 255, in the cache).
+ * q_out must not overlap an input or the cache, and the cache no input (BSFP8_EINVAL). */
+BSFP8_API int bsfp8_cache_write(const bsfp8_kv_cache* cache, const int64_t* slots, int64_t R,
+                                const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
+                                const uint16_t* q, int64_t ldq, int64_t hq, uint16_t* q_out,
+                                const uint16_t* q_weight, const uint16_t* k_weight, float eps,
+                                const float* cos_sin, int64_t n_positions, int64_t rot,
+                                const int64_t* positions, int interleaved, void* stream);
+
+/* Rows of the cache as bf16: k_out, v_out [R][heads][dim] (contiguous, 16-byte aligned), each value
+ * e4m3(code) * 2^(byte-127) rounded once to bf16 (exact unless it falls below the bf16 normals;
+ * scale byte 255 and NaN codes give NaN). A slot outside the cache gives zeros. */
+BSFP8_API int bsfp8_cache_read(const bsfp8_kv_cache* cache, const int64_t* slots, int64_t R,
+                               uint16_t* k_out, uint16_t* v_out, void* stream);
+
+/* Workspace bytes of bsfp8_tree_attention for these sizes (0 for sizes it refuses). The contents
+ * need no clearing; one workspace must not be used by two calls that can run at the same time. */
+BSFP8_API size_t bsfp8_attention_workspace_bytes(int64_t B, int64_t T, int64_t hq, int64_t hkv, int64_t dim,
+                                                 int64_t max_len);
+
+/* Attention of T drafted tokens (nodes) per sequence over the cache, which already holds them:
+ *   out[b][t][h] = sum_j softmax_j(scale * q[b][t][h] . K[b][j][h / (hq/hkv)]) V[b][j][h / (hq/hkv)]
+ * over the positions j that node t of sequence b sees. Sequence b holds lens[b] tokens, position j in
+ * slot (pages[b][j / page], j % page); its last nodes[b] tokens are the nodes (node i at position
+ * lens[b] - nodes[b] + i), the ones before them its prefix, which every node sees. Without a mask
+ * node t sees nodes 0..t (a chain; T = 1 is plain decoding); with one it sees node i where bit i
+ * of mask[b][t] is set (a tree: a node's ancestors and itself).
+ *   q     : bf16 [B*T][ldq], head h at columns [h*dim, (h+1)*dim) (16-byte aligned, ldq % 8 == 0).
+ *   pages : int32_t [B][ld_pages] (device). A page outside [0, cache->pages) holds no tokens: its
+ *           positions are seen by no node.
+ *   lens  : int32_t [B] (device), the nodes included; cut to [0, min(max_len, ld_pages * page)].
+ *   nodes : int32_t [B] (device), cut to [0, T]; NULL: T everywhere. Rows t >= nodes[b] are zeros.
+ *   mask  : int64_t [B][T] (device) or NULL; with a mask T <= 64.
+ *   out   : bf16 [B][T][hq][dim] (contiguous, 16-byte aligned). A node that sees nothing gets zeros.
+ * Values of positions that a node does not see never reach it, also when they are NaN or infinite
+ * (a rejected draft's leftovers, a page never written). hq is a multiple of cache->heads, at most
+ * 64 times it; T >= 1; B * T * hq < 2^31. Scores and sums are fp32; the weights of one tile are
+ * rounded to bf16 for the product with V (rebuilt exactly from its codes, as K is). The split of
+ * the positions over workgroups depends on lens and the sizes only: results repeat bit for bit. */
+BSFP8_API int bsfp8_tree_attention(const uint16_t* q, int64_t ldq, int64_t B, int64_t T, int64_t hq,
+                                   const bsfp8_kv_cache* cache, const int32_t* pages, int64_t ld_pages,
+                                   const int32_t* lens, const int32_t* nodes, const int64_t* mask, float scale,
+                                   int64_t max_len, void* ws, size_t ws_bytes, uint16_t* out, void* stream);
+
+/* Type of the logits handed to the verification calls. */
+typedef enum bsfp8_logits {
+  BSFP8_LOGITS_BF16 = 0,
+  BSFP8_LOGITS_F32 = 1
+} bsfp8_logits;
+
+/* Workspace bytes of the verification calls (0 for sizes they refuse). ZERO-FILLED once after
+ * allocation; every call leaves its counters at zero. Not for two calls that can run at the same
+ * time. */
+BSFP8_API size_t bsfp8_verify_workspace_bytes(int64_t B, int64_t T, int64_t V);
+
+/* Verification of a chain of T - 1 drafted tokens per sequence. With p_i = softmax(logits[b][i] / t)
+ * and q_i = softmax(draft[b][i] / t), t = temperature[b]: draft token x_i = tokens[b][i] is accepted
+ * while u[b][i] * q_i(x_i) < p_i(x_i). n = the number accepted before the first refusal. The next
+ * token is the first index whose running sum of the weights passes u_sample[b] times their total,
+ * the weights being max(p_n - q_n, 0) after a refusal (p_n where that is zero everywhere) and
+ * p_{T-1} when all were accepted. With t = 0 (greedy; also t < 0 or NaN) x_i is accepted if it is
+ * the lowest index of the largest logit of row i, and the next token is that of row n.
+ *   logits : [B][T][V], draft : [B][T-1][V], of `dtype` (bsfp8_logits), contiguous, 16-byte aligned.
+ *            bf16 rows of an odd total are read to the end of their last 4-byte word.
+ *   tokens : int32_t [B][T-1]; one outside [0, V) is refused. temperature: float [B]; u: float
+ *            [B][T-1]; u_sample: float [B], uniform in [0, 1) (all device; the draft arrays may be NULL
+ *            when T = 1).
+ *   out_tokens : int32_t [B][T]: the n accepted tokens, the next one, then -1. n_accepted: int32_t [B].
+ * 1 <= T <= 64, 1 <= V <= 2^24. Probabilities and running sums are 64-bit, so that neighbouring
+ * sums are told apart. -inf logits have probability 0; a NaN logit counts as -inf; +inf ones share
+ * the row. A row of nothing but -inf or NaN gives index 0. */
+BSFP8_API int bsfp8_verify_chain(const void* logits, const void* draft, int dtype, int64_t B, int64_t T, int64_t V,
+                                 const int32_t* tokens, const float* temperature, const float* u,
+                                 const float* u_sample, void* ws, size_t ws_bytes, int32_t* out_tokens,
+                                 int32_t* n_accepted, void* stream);
+
+/* Verification of a tree of drafted tokens: node 0 is the root, node i carries tokens[b][i] and hangs
+ * from node parents[b][i] < i. Every node samples its next token from softmax(logits[b][i] / t) with
+ * u[b][i] (the rule above; the lowest index of the largest logit when t = 0); from the root, the walk
+ * goes on to the child that carries the sampled token (the lowest-numbered one of equals) until there
+ * is none.
+ *   tokens, parents : int32_t [B][T] (device; the root's entries are not read). A parent outside [0, i) cuts the node off.
+ *   out_tokens : int32_t [B][T]: the sampled token of each node of the path (the accepted drafts, then
+ *                the next token), then -1. path: int32_t [B][T]: the path's nodes from the root, then -1.
+ *   n_accepted : int32_t [B]: the drafts accepted (the path's length less one).
+ * Other arguments and limits as bsfp8_verify_chain. */
+BSFP8_API int bsfp8_verify_tree(const void* logits, int dtype, int64_t B, int64_t T, int64_t V, const int32_t* tokens,
+                                const int32_t* parents, const float* temperature, const float* u, void* ws,
+                                size_t ws_bytes, int32_t* out_tokens, int32_t* path, int32_t* n_accepted,
+                                void* stream);
+
 #ifdef __cplusplus
 }
 #endif
