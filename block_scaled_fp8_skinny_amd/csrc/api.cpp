@@ -682,7 +682,7 @@ int bsfp8_tree_attention(const uint16_t* q, int64_t ldq, int64_t B, int64_t T, i
   if (ld_pages < 0 || ld_pages >= ((int64_t)1 << 31) || (mask && T > 64)) return BSFP8_ESHAPE;
   if (B == 0) return BSFP8_OK;
   const int64_t D = cache->dim;
-  if (!q || !out || !lens || (ld_pages > 0 && !pages)) return BSFP8_EINVAL;
+  if (!q || !out || !lens || (ld_pages > 0 && !pages) || !(scale - scale == 0.f)) return BSFP8_EINVAL;
   if (ldq < hq * D || ldq % 8 || !aligned16(q) || !aligned16(out)) return BSFP8_ESTRIDE;
   const AttentionArgs a{q, ldq, B, T, hq, *cache, pages, ld_pages, lens, nodes, mask, scale, max_len, ws, out};
   if (!ws || ws_bytes < attention_ws_bytes(a) || !aligned16(ws)) return BSFP8_EWORKSPACE;

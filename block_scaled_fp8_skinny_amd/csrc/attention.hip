@@ -23,8 +23,6 @@
 // all sequences, in order, are divided into equal runs, one per workgroup, so that ragged lengths
 // leave nobody idle; a head that falls into several runs leaves partial (m, l, O) in the workspace
 // for a second kernel to join.
-#include <type_traits>
-
 #include "device.h"
 
 namespace bsfp8 {
@@ -33,7 +31,7 @@ namespace {
 constexpr int NW = 4;                               // waves per workgroup
 constexpr int TILE = 32;                            // tokens of a wave's tile
 constexpr int UNIT = NW * TILE;
-constexpr int TABLE = 1024;                         // page numbers held in LDS at a time
+constexpr int TABLE = 512;                          // page numbers held in LDS at a time
 constexpr float MOVE = 8.f;
 constexpr float M_NONE = -1e30f;                    // reference of a row that has seen nothing
 
@@ -46,7 +44,8 @@ struct AttnParams {
   float* part;                                      // [nwg][2][rows of a block][D]
   float2* stat;                                     // [nwg][2][rows of a block]: m, l
   int64_t ldq, ld_pages, n_pages;
-  float scale2;
+  float scale2;                                     // |scale| * log2 e (1 for a scale of 0)
+  uint32_t q_keep, q_flip;                          // the scale's sign, or a scale of 0, on the queries
   int B, T, hq, hkv, g, rows, mblocks, page, max_len, nwg;
   FastDiv dpage, dg;
 };
@@ -180,33 +179,33 @@ __device__ __forceinline__ int v_value(int x, int i) {
 // (the product of the flags of such values with the flags of seen tokens is positive) get NaN.
 template <int MT>
 __device__ __forceinline__ void unseen_nonfinite(bf16x8_t (&a)[4], const uint32_t (&sees)[MT], f32x4_t* o, int stride) {
-  u32x4_t flag[4];
-  bool any = false;
+  auto bad = [](uint32_t v) {                       // ones where a half is NaN or infinite
+    return ((v & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((v & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
+  };
+  uint32_t any = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) any |= bad(__builtin_bit_cast(u32x4_t, a[k])[j]);
+  if (!__any(any != 0)) return;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const u32x4_t v = __builtin_bit_cast(u32x4_t, a[k]);
-    u32x4_t keep;
+    u32x4_t v = __builtin_bit_cast(u32x4_t, a[k]), flag;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t lo = (v[j] & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u;
-      const uint32_t hi = (v[j] & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u;
-      flag[k][j] = 0x3F803F80u & (lo | hi);
-      keep[j] = v[j] & ~(lo | hi);
-      any = any || (lo | hi) != 0;
+      const uint32_t x = bad(v[j]);
+      flag[j] = 0x3F803F80u & x;
+      v[j] &= ~x;
     }
-    a[k] = __builtin_bit_cast(bf16x8_t, keep);
-  }
-  if (!__any(any)) return;
+    a[k] = __builtin_bit_cast(bf16x8_t, v);
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    u32x4_t w;
+    for (int mt = 0; mt < MT; ++mt) {
+      u32x4_t w;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      w[j] = ((sees[mt] >> (2 * j)) & 1 ? 0x3F80u : 0u) | ((sees[mt] >> (2 * j + 1)) & 1 ? 0x3F800000u : 0u);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const f32x4_t n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, flag[k]),
-                                                                __builtin_bit_cast(bf16x8_t, w), f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+      for (int j = 0; j < 4; ++j)
+        w[j] = ((sees[mt] >> (2 * j)) & 1 ? 0x3F80u : 0u) | ((sees[mt] >> (2 * j + 1)) & 1 ? 0x3F800000u : 0u);
+      const f32x4_t n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+          __builtin_bit_cast(bf16x8_t, flag), __builtin_bit_cast(bf16x8_t, w), f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
 #pragma unroll
       for (int r = 0; r < 4; ++r)
         if (n[r] > 0.f) o[mt * stride + k][r] = __uint_as_float(0x7FC00000u);
@@ -214,16 +213,64 @@ __device__ __forceinline__ void unseen_nonfinite(bf16x8_t (&a)[4], const uint32_
   }
 }
 
+// Scale factors (2^(byte - 127), in the exponent field; the conversions read nothing else of the operand,
+// so the byte only has to be rotated there) of one 16-token group.
+template <int D>
+struct Scales {
+  static constexpr int TB = D / 32;                 // bytes per token
+  static __device__ __forceinline__ float rotated(uint32_t w, int byte) {
+    return __uint_as_float(__builtin_amdgcn_alignbit(w, w, 8 * byte + 9));
+  }
+  // K: token r16, blocks 2j + half (j = 0 .. D/64 - 1)
+  static __device__ __forceinline__ void k(const uint8_t* s, int r16, int half, float (&f)[D / 64]) {
+    if constexpr (D == 256) {
+      const uint2 w = *reinterpret_cast<const uint2*>(s + r16 * 8);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = rotated(j < 2 ? w.x : w.y, 2 * (j & 1) + half);
+    } else if constexpr (D == 128) {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(s + r16 * 4);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) f[j] = rotated(w, 2 * j + half);
+    } else {
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j) f[j] = rotated(*reinterpret_cast<const uint16_t*>(s + r16 * TB + 2 * j), half);
+    }
+  }
+  // V: tokens q4 * 4 + 0..3, the block of the lane's values of operand tiles 4c .. 4c + 3
+  static __device__ __forceinline__ void v(const uint8_t* s, int r16, int q4, int c, float* f) {
+    if constexpr (D == 128) {
+      const uint4 w = *reinterpret_cast<const uint4*>(s + q4 * 16);
+      const uint32_t t[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = rotated(t[j], r16 >> 2);
+    } else if constexpr (D == 64) {
+      const uint2 w = *reinterpret_cast<const uint2*>(s + q4 * 8);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = rotated(j < 2 ? w.x : w.y, 2 * (j & 1) + (r16 >> 3));
+    } else if constexpr (D == 256) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        f[j] = rotated(*reinterpret_cast<const uint32_t*>(s + (q4 * 4 + j) * 8 + (r16 >> 3) * 4), (r16 >> 1) & 3);
+    } else {
+      const int block = c < 2 ? r16 >> 2 : 4 + (r16 >> 3);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = block_scale(s[(q4 * 4 + j) * TB + block]);
+    }
+  }
+};
+
 template <int D, int MT, int NS>
-__global__ void __launch_bounds__(64 * NW, MT * D <= 384 ? 2 : 1) attention_kernel(AttnParams p) {
+__global__ void __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) attention_kernel(AttnParams p) {
   using G = Geo<D>;
   constexpr int ND = D / 16, NK = D / 32, BR = MT * 16;
   constexpr int RING = NW * NS * G::STAGE, JOIN = 2 * MT * ND * 1024;
   constexpr int BYTES = RING > JOIN ? RING : JOIN;
   static_assert((NS - 1) * G::PER_TILE <= 63, "vector memory counter range");
+  static_assert(NW * BR * 8 <= TABLE * 4, "the statistics take the table's place");
   __shared__ __align__(16) uint8_t ring[BYTES];
-  __shared__ int32_t table[TABLE];
-  __shared__ float2 stats[NW][BR];
+  __shared__ __align__(16) uint4 queries[MT * NK * 64];   // B operands: row mt*16 + r16, values of K's operand order
+  __shared__ __align__(16) int32_t table[TABLE];
+  float2* const stats = reinterpret_cast<float2*>(table);
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, q4 = lane >> 4;
@@ -255,21 +302,20 @@ __global__ void __launch_bounds__(64 * NW, MT * D <= 384 ? 2 : 1) attention_kern
     const int here = p.nodes ? max(0, min(p.nodes[b], p.T)) : p.T;
     const int prefix = len - here;
 
-    // the rows' queries: B operands, row mt*16 + r16, k = the values of K's operand order
-    bf16x8_t qf[MT][NK];
-    int node[MT];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const int m = mb * BR + mt * 16 + r16;
-      node[mt] = m < p.rows ? fdiv(m, p.dg) : p.T;
-      const int hd = m - node[mt] * p.g;
-      const uint16_t* src = p.q + ((int64_t)b * p.T + node[mt]) * p.ldq + ((int64_t)h * p.g + hd) * D;
-#pragma unroll
-      for (int j = 0; j < NK; ++j) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (node[mt] < here) v = *reinterpret_cast<const uint4*>(src + (j >> 1) * 64 + q4 * 16 + (j & 1) * 8);
-        qf[mt][j] = __builtin_bit_cast(bf16x8_t, v);
+    __syncthreads();                                // the last run's ring, queries and statistics are done with
+    for (int i = threadIdx.x; i < MT * NK * 64; i += 64 * NW) {
+      const int l = i & 63, j = (i >> 6) % NK, m = mb * BR + (i >> 6) / NK * 16 + (l & 15);
+      const int nd = fdiv(min(m, p.rows - 1), p.dg), hd = m - nd * p.g;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (m < p.rows && nd < here) {
+        v = *reinterpret_cast<const uint4*>(p.q + ((int64_t)b * p.T + nd) * p.ldq + ((int64_t)h * p.g + hd) * D +
+                                            (j >> 1) * 64 + (l >> 4) * 16 + (j & 1) * 8);
+        v.x = (v.x & p.q_keep) ^ p.q_flip;
+        v.y = (v.y & p.q_keep) ^ p.q_flip;
+        v.z = (v.z & p.q_keep) ^ p.q_flip;
+        v.w = (v.w & p.q_keep) ^ p.q_flip;
       }
+      queries[i] = v;
     }
     f32x4_t o[MT][ND];
     float mref[MT], l[MT];
@@ -285,7 +331,7 @@ __global__ void __launch_bounds__(64 * NW, MT * D <= 384 ? 2 : 1) attention_kern
       const int p0 = fdiv(uc * UNIT, p.dpage);
       const int uz = (int)min((int64_t)ub, ((int64_t)p0 + TABLE) * p.page / UNIT);
       const int np = fdiv(min(uz * UNIT, len) - 1, p.dpage) + 1 - p0;
-      __syncthreads();                              // the ring and table are free
+      if (uc != ua) __syncthreads();                // the table is free
       for (int i = threadIdx.x; i < np; i += 64 * NW) {
         const int pg = p.pages[(int64_t)b * p.ld_pages + p0 + i];
         table[i] = pg >= 0 && pg < p.n_pages ? pg : -1;
@@ -299,80 +345,91 @@ __global__ void __launch_bounds__(64 * NW, MT * D <= 384 ? 2 : 1) attention_kern
       };
       auto issue = [&](int i) {
         uint8_t* st = my_ring + (i % NS) * G::STAGE;
-        const uint8_t* sc[4];
+        int64_t at[2];                              // the groups' first rows; absent tokens: some page, not used
 #pragma unroll
         for (int gr = 0; gr < 2; ++gr) {
           const int t = t0 + i * UNIT + gr * 16;
-          const int pg = max(page_of(t), 0);        // absent tokens: some page, not used
+          const int pg = max(page_of(t), 0);
           const int off = t < len ? t - fdiv(t, p.dpage) * p.page : 0;
-          const int64_t at = ((int64_t)pg * p.hkv + h) * p.page + off;
-          const uint8_t *kb = p.kq + at * D, *vb = p.vq + at * D;
-          sc[gr] = p.ks + at * (D / 32);
-          sc[2 + gr] = p.vs + at * (D / 32);
+          at[gr] = ((int64_t)pg * p.hkv + h) * p.page + off;
 #pragma unroll
           for (int n = 0; n < G::LOADS; ++n) {
-            gload_lds16(kb, ksrc[n], lds_addr(st + gr * G::CODES + n * 1024));
-            gload_lds16(vb, vsrc[n], lds_addr(st + (2 + gr) * G::CODES + n * 1024));
+            gload_lds16(p.kq + at[gr] * D, ksrc[n], lds_addr(st + gr * G::CODES + n * 1024));
+            gload_lds16(p.vq + at[gr] * D, vsrc[n], lds_addr(st + (2 + gr) * G::CODES + n * 1024));
           }
         }
         constexpr int Q = D / 8;                    // dwords of one group's scales
 #pragma unroll
         for (int n = 0; n < G::SLOADS; ++n) {
           const int e = n * 64 + lane, quarter = e / Q;
-          const uint8_t* a = quarter == 0 ? sc[0] : quarter == 1 ? sc[1] : quarter == 2 ? sc[2] : sc[3];
+          const uint8_t* a = (quarter & 2 ? p.vs : p.ks) + (quarter & 1 ? at[1] : at[0]) * (D / 32);
           if (e < 4 * Q) gload_lds4(a + (e - quarter * Q) * 4, lds_addr(st + 4 * G::CODES + n * 256));
         }
       };
-      // SPECIAL: a tile that some row does not see whole (nodes, the sequence's end, an absent page)
-      auto compute = [&](int i, int pg0, int pg1, auto SPECIAL) {
-        constexpr bool special = decltype(SPECIAL)::value;
+      auto compute = [&](int i) {
         const uint8_t* st = my_ring + (i % NS) * G::STAGE;
         const uint8_t* scales = st + 4 * G::CODES;
-        const int t = t0 + i * UNIT;
+        const int t = t0 + i * UNIT, pg0 = page_of(t), pg1 = page_of(t + 16);
+        // a tile that some row does not see whole: nodes, the sequence's end, an absent page (uniform)
+        const bool special = t + TILE > prefix || t + TILE > len || pg0 < 0 || pg1 < 0;
         f32x4_t s[2][MT];
+        float kf[2][D / 64];
 #pragma unroll
         for (int gr = 0; gr < 2; ++gr) {
+          Scales<D>::k(scales + gr * G::SCALES, r16, q4 >> 1, kf[gr]);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) s[gr][mt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-          const uint8_t* kr = st + gr * G::CODES + r16 * D;
-          const uint8_t* kscale = scales + gr * G::SCALES + r16 * (D / 32) + (q4 >> 1);
+        }
 #pragma unroll
-          for (int j = 0; j < D / 64; ++j) {
-            const uint4 a = *reinterpret_cast<const uint4*>(kr + (((4 * j + q4) ^ G::swizzle(r16)) * 16));
-            const float f = block_scale(kscale[2 * j]);
-            const bf16x8_t a0 = dequant8(a.x, a.y, f), a1 = dequant8(a.z, a.w, f);
+        for (int j = 0; j < D / 64; ++j) {
+          bf16x8_t a[2][2];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              s[gr][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, qf[mt][2 * j], s[gr][mt], 0, 0, 0);
-              s[gr][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, qf[mt][2 * j + 1], s[gr][mt], 0, 0, 0);
-            }
+          for (int gr = 0; gr < 2; ++gr) {
+            const uint4 w = *reinterpret_cast<const uint4*>(st + gr * G::CODES + r16 * D +
+                                                            (((4 * j + q4) ^ G::swizzle(r16)) * 16));
+            a[gr][0] = dequant8(w.x, w.y, kf[gr][j]);
+            a[gr][1] = dequant8(w.z, w.w, kf[gr][j]);
           }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const bf16x8_t qf = __builtin_bit_cast(bf16x8_t, queries[(mt * NK + 2 * j + e) * 64 + lane]);
+#pragma unroll
+              for (int gr = 0; gr < 2; ++gr)
+                s[gr][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[gr][e], qf, s[gr][mt], 0, 0, 0);
+            }
         }
         // tokens of the lane: t + (e / 4) * 16 + q4 * 4 + e % 4, e = 0..7
         bf16x8_t pf[MT];
-        uint32_t sees[MT];                          // SPECIAL: bit e = the row sees token e
+        uint32_t sees[MT];                          // bit e: the row sees token e (special tiles)
+        if (special) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          float x[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = s[e >> 2][mt][e & 3] * p.scale2;
-          if constexpr (special) {
-            sees[mt] = 0;
-            const int nd = node[mt];
-            int64_t bits = 0;
-            if (p.mask && nd < here) bits = p.mask[(int64_t)b * p.T + nd];
+          for (int mt = 0; mt < MT; ++mt) {
+            const int m = mb * BR + mt * 16 + r16, nd = m < p.rows ? fdiv(m, p.dg) : here;
+            uint64_t bits = 0;
+            if (p.mask && nd < here) bits = (uint64_t)p.mask[(int64_t)b * p.T + nd];
+            uint32_t see = 0;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const int tok = t + (e >> 2) * 16 + q4 * 4 + (e & 3), rel = tok - prefix;
               bool seen = tok < len && (e < 4 ? pg0 : pg1) >= 0 && nd < here;
               if (rel >= 0) seen = seen && (p.mask ? (bits >> (rel & 63) & 1) != 0 : rel <= nd);
-              x[e] = seen ? x[e] : -__builtin_inff();
-              sees[mt] |= seen ? 1u << e : 0u;
+              s[e >> 2][mt][e & 3] = seen ? s[e >> 2][mt][e & 3] : -__builtin_inff();
+              see |= seen ? 1u << e : 0u;
             }
+            sees[mt] = see;
           }
-          float top = x[0];
+        } else {
 #pragma unroll
-          for (int e = 1; e < 8; ++e) top = fmaxf(top, x[e]);
+          for (int mt = 0; mt < MT; ++mt) sees[mt] = 0xFF;
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = s[e >> 2][mt][e & 3];
+          float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]))) * p.scale2;
           if (__any(top > mref[mt] + MOVE)) {
             top = fmaxf(top, __shfl_xor(top, 16));
             top = fmaxf(top, __shfl_xor(top, 32));
@@ -384,26 +441,30 @@ __global__ void __launch_bounds__(64 * NW, MT * D <= 384 ? 2 : 1) attention_kern
           }
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            x[e] = __builtin_amdgcn_exp2f(x[e] - mref[mt]);
+            x[e] = __builtin_amdgcn_exp2f(fmaf(x[e], p.scale2, -mref[mt]));
             l[mt] += x[e];
           }
           const u32x4_t w = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
                              pack_bf16x2(x[6], x[7])};
           pf[mt] = __builtin_bit_cast(bf16x8_t, w);
         }
-        // V: dword c of the lane's values of each token; its block is the same for all four
+        // V: dword c of the lane's values of each token; their block is the same for all four
 #pragma unroll
         for (int c = 0; c < ND / 4; ++c) {
+          // the scheduler would hoist every chunk's reads, and spill; spilled registers are reloaded through
+          // the counter that the ring's loads use, so a wait for one would drain the ring
+          __builtin_amdgcn_sched_barrier(0);
           uint32_t raw[8];
           float f[8];
           const int d = v_value<D>(r16, 4 * c);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int gr = e >> 2, j = e & 3;
-            raw[e] = *reinterpret_cast<const uint32_t*>(st + (2 + gr) * G::CODES + (j * 4 + q4) * D + d);
-            f[e] = block_scale(scales[(2 + gr) * G::SCALES + (q4 * 4 + j) * (D / 32) + d / 32]);
+          for (int gr = 0; gr < 2; ++gr) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              raw[gr * 4 + j] = *reinterpret_cast<const uint32_t*>(st + (2 + gr) * G::CODES + (j * 4 + q4) * D + d);
+            Scales<D>::v(scales + (2 + gr) * G::SCALES, r16, q4, c, f + gr * 4);
           }
-          if constexpr (special) {
+          if (special) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               if (t + (e >> 2) * 16 + q4 * 4 + (e & 3) >= len || (e < 4 ? pg0 : pg1) < 0) {
@@ -413,7 +474,7 @@ __global__ void __launch_bounds__(64 * NW, MT * D <= 384 ? 2 : 1) attention_kern
           }
           bf16x8_t a[4];
           v_operands(raw, f, a);
-          if constexpr (special) unseen_nonfinite<MT>(a, sees, &o[0][0] + 4 * c, ND);
+          if (special) unseen_nonfinite<MT>(a, sees, &o[0][0] + 4 * c, ND);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -422,20 +483,16 @@ __global__ void __launch_bounds__(64 * NW, MT * D <= 384 ? 2 : 1) attention_kern
         }
       };
 
-#pragma unroll
-      for (int i = 0; i < NS; ++i)
-        if (i < nt) issue(i);
+#pragma unroll 1
+      for (int i = 0; i < NS && i < nt; ++i) issue(i);
+#pragma unroll 1
       for (int i = 0; i < nt; ++i) {
         const int ahead = min(NS - 1, nt - 1 - i);  // tiles in flight beyond this one
         if (ahead >= 3) wait_vmcnt_le<(NS > 3 ? 3 * G::PER_TILE : 0)>();
         else if (ahead == 2) wait_vmcnt_le<(NS > 2 ? 2 * G::PER_TILE : 0)>();
         else if (ahead == 1) wait_vmcnt_le<G::PER_TILE>();
         else wait_vmcnt_le<0>();
-        const int t = t0 + i * UNIT, pg0 = page_of(t), pg1 = page_of(t + 16);
-        if (t + TILE > prefix || t + TILE > len || pg0 < 0 || pg1 < 0)   // uniform
-          compute(i, pg0, pg1, std::true_type{});
-        else
-          compute(i, pg0, pg1, std::false_type{});
+        compute(i);
         if (i + NS < nt) {
           asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // this tile's reads, before it is refilled
           issue(i + NS);
@@ -445,11 +502,12 @@ __global__ void __launch_bounds__(64 * NW, MT * D <= 384 ? 2 : 1) attention_kern
     }
 
     // join the waves: common reference, then the sums by a fixed tree (2, 3 into 0, 1; 1 into 0)
+    __syncthreads();                                // the table's page numbers are done with
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       l[mt] += __shfl_xor(l[mt], 16);
       l[mt] += __shfl_xor(l[mt], 32);
-      if (q4 == 0) stats[wave][mt * 16 + r16] = make_float2(mref[mt], l[mt]);
+      if (q4 == 0) stats[wave * BR + mt * 16 + r16] = make_float2(mref[mt], l[mt]);
     }
     __syncthreads();
 #pragma unroll
@@ -458,7 +516,7 @@ __global__ void __launch_bounds__(64 * NW, MT * D <= 384 ? 2 : 1) attention_kern
       float m = M_NONE;
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
-        st[w] = stats[w][mt * 16 + r16];
+        st[w] = stats[w * BR + mt * 16 + r16];
         m = fmaxf(m, st[w].x);
       }
       float sum = 0.f;
@@ -495,13 +553,13 @@ __global__ void __launch_bounds__(64 * NW, MT * D <= 384 ? 2 : 1) attention_kern
       const int64_t slot = (int64_t)blockIdx.x * 2 + (u == first_u ? 0 : 1);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        const int row = mt * 16 + r16;
-        if (node[mt] >= p.T) continue;
-        const int hd = mb * BR + row - node[mt] * p.g;
+        const int row = mt * 16 + r16, m = mb * BR + row;
+        if (m >= p.rows) continue;
         if (whole) {
-          const bool live = node[mt] < here && l[mt] != 0.f;   // NaN passes
+          const int nd = fdiv(m, p.dg);
+          const bool live = nd < here && l[mt] != 0.f;   // NaN passes
           const float f = 1.f / l[mt];
-          uint16_t* dst = p.out + (((int64_t)b * p.T + node[mt]) * p.hq + (int64_t)h * p.g + hd) * D;
+          uint16_t* dst = p.out + (((int64_t)b * p.T + nd) * p.hq + (int64_t)h * p.g + (m - nd * p.g)) * D;
 #pragma unroll
           for (int c = 0; c < ND / 4; ++c)
 #pragma unroll
@@ -530,61 +588,100 @@ __global__ void __launch_bounds__(64 * NW, MT * D <= 384 ? 2 : 1) attention_kern
   }
 }
 
-// Join the partial results of the heads that several workgroups shared, and zero the rows of empty
-// sequences. One workgroup per row: D/4 lanes hold four values each, the 256 / (D/4) slices of the
-// workgroup take every so-many-th partial result.
+// Join the partial results of the heads that several workgroups shared, and zero the rows that nobody
+// wrote (empty sequences). A workgroup takes `jr` rows of a head and row block, so that there are about
+// JOIN_BLOCKS of them: the search for the runs' owners comes before the first row. D/4 lanes hold
+// four values of a row each; the workgroup's 256 / (D/4) slices take rows side by side, or, when a
+// row's partial results are many, all take one row and every so-many-th result of it.
+constexpr int JOIN_BLOCKS = 1024;
 template <int D, int MT>
-__global__ void __launch_bounds__(256) attention_join_kernel(AttnParams p) {
+__global__ void __launch_bounds__(256) attention_join_kernel(AttnParams p, int jr, int jblocks) {
   constexpr int LD = D / 4, SL = 256 / LD, BR = MT * 16;
   __shared__ f32x4_t sums[SL][LD];
   const int lane = threadIdx.x & 63;
-  const int m = blockIdx.x % (unsigned)p.rows;
-  int r = blockIdx.x / (unsigned)p.rows;
+  const int part = blockIdx.x % (unsigned)jblocks;
+  int r = blockIdx.x / (unsigned)jblocks;
+  const int mb = r % p.mblocks;
+  r /= p.mblocks;
   const int h = r % p.hkv, b = r / p.hkv;
-  const int units = seq_units(p, b), mb = m / BR, row = m - mb * BR;
-  const int node = fdiv(m, p.dg);
-  const int64_t out = (((int64_t)b * p.T + node) * p.hq + (int64_t)h * p.g + (m - node * p.g)) * D;
+  const int units = seq_units(p, b);
+  const int row0 = part * jr, row1 = min(min(row0 + jr, BR), p.rows - mb * BR);
+  const int here = p.nodes ? p.nodes[b] : p.T;
   const int c = threadIdx.x % LD, sl = threadIdx.x / LD;
-  if (units == 0 || (p.nodes && node >= p.nodes[b])) {
-    if (sl == 0) *reinterpret_cast<uint2*>(p.out + out + c * 4) = make_uint2(0, 0);
+  auto out_at = [&](int row) {
+    const int m = mb * BR + row, node = fdiv(m, p.dg);
+    return p.out + (((int64_t)b * p.T + node) * p.hq + (int64_t)h * p.g + (m - node * p.g)) * D + c * 4;
+  };
+  if (units == 0) {
+    for (int row = row0 + sl; sl < SL && row < row1; row += SL) *reinterpret_cast<uint2*>(out_at(row)) = make_uint2(0, 0);
     return;
   }
   const Batch batch(p, lane);
   const int ipb = p.hkv * p.mblocks;
   const Runs runs(batch.total * ipb, p.nwg);
   const int u0 = batch.before(p, b) * ipb + (h * p.mblocks + mb) * units;
-  const int w0 = runs.owner(u0), w1 = runs.owner(u0 + units - 1);
-  if (w0 == w1) return;
+  const int w0 = runs.owner(u0), w1 = runs.owner(u0 + units - 1), n = w1 - w0 + 1;
+  if (n == 1) return;
   const int64_t head = (int64_t)w0 * 2 + (runs.start(w0) < u0 ? 1 : 0);
-  auto slot_of = [&](int w) { return (w == w0 ? head : (int64_t)w * 2) * BR + row; };
-  float top = M_NONE;
-  for (int w = w0 + lane; w <= w1; w += 64) top = fmaxf(top, p.stat[slot_of(w)].x);
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
-  float l = 0.f;
-  for (int w = w0 + lane; w <= w1; w += 64) {
-    const float2 s = p.stat[slot_of(w)];
-    l += s.y * __builtin_amdgcn_exp2f(s.x - top);
-  }
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) l += __shfl_xor(l, o);
-  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-  if (sl < SL)
+  auto slot_of = [&](int w) { return (w == w0 ? head : (int64_t)w * 2) * BR; };
+  auto store = [&](int row, const f32x4_t& acc, float l) {
+    const float f = 1.f / l;
+    const bool live = l != 0.f && fdiv(mb * BR + row, p.dg) < here;
+    *reinterpret_cast<uint2*>(out_at(row)) =
+        live ? make_uint2(pack_bf16x2(acc[0] * f, acc[1] * f), pack_bf16x2(acc[2] * f, acc[3] * f)) : make_uint2(0, 0);
+  };
+  // sum of the results w0 + first, + step, ... of one row, relative to its largest reference
+  auto gather = [&](int row, int first, int step, float& top, float& l) {
+    top = M_NONE;
+    for (int w = w0; w <= w1; ++w) top = fmaxf(top, p.stat[slot_of(w) + row].x);
+    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+    l = 0.f;
 #pragma unroll 4
-    for (int w = w0 + sl; w <= w1; w += SL) {
-      const int64_t at = slot_of(w);
-      const float f = __builtin_amdgcn_exp2f(p.stat[at].x - top);
+    for (int w = w0 + first; w <= w1; w += step) {
+      const int64_t at = slot_of(w) + row;
+      const float2 s = p.stat[at];
+      const float f = __builtin_amdgcn_exp2f(s.x - top);
+      l += s.y * f;
       acc += *reinterpret_cast<const f32x4_t*>(p.part + at * D + c * 4) * f;
     }
-  if (sl < SL) sums[sl][c] = acc;
-  __syncthreads();
-  if (sl != 0) return;
-  acc = sums[0][c];
+    return acc;
+  };
+  float top, l;
+  if (n <= SL && row1 - row0 > 1) {
+    for (int row = row0 + sl; sl < SL && row < row1; row += SL) {
+      const f32x4_t acc = gather(row, 0, 1, top, l);
+      store(row, acc, l);
+    }
+    return;
+  }
+  for (int row = row0; row < row1; ++row) {
+    // references and sums by the lanes of every wave, the values by the slices
+    top = M_NONE;
+    for (int w = w0 + lane; w <= w1; w += 64) top = fmaxf(top, p.stat[slot_of(w) + row].x);
 #pragma unroll
-  for (int i = 1; i < SL; ++i) acc += sums[i][c];
-  const float f = 1.f / l;
-  *reinterpret_cast<uint2*>(p.out + out + c * 4) =
-      l != 0.f ? make_uint2(pack_bf16x2(acc[0] * f, acc[1] * f), pack_bf16x2(acc[2] * f, acc[3] * f)) : make_uint2(0, 0);
+    for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
+    l = 0.f;
+    for (int w = w0 + lane; w <= w1; w += 64) {
+      const float2 s = p.stat[slot_of(w) + row];
+      l += s.y * __builtin_amdgcn_exp2f(s.x - top);
+    }
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) l += __shfl_xor(l, o);
+    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int w = w0 + sl; sl < SL && w <= w1; w += SL) {
+      const int64_t at = slot_of(w) + row;
+      acc += *reinterpret_cast<const f32x4_t*>(p.part + at * D + c * 4) * __builtin_amdgcn_exp2f(p.stat[at].x - top);
+    }
+    if (sl < SL) sums[sl][c] = acc;
+    __syncthreads();
+    if (sl == 0) {
+#pragma unroll
+      for (int i = 1; i < SL; ++i) acc += sums[i][c];
+      store(row, acc, l);
+    }
+    __syncthreads();
+  }
 }
 
 struct AttnPlan {
@@ -607,8 +704,12 @@ template <int D, int MT, int NS>
 int run(const AttnParams& p, hipStream_t stream) {
   hipLaunchKernelGGL((attention_kernel<D, MT, NS>), dim3((unsigned)p.nwg), dim3(64 * NW), 0, stream, p);
   if (hipGetLastError() != hipSuccess) return BSFP8_EHIP;
-  hipLaunchKernelGGL((attention_join_kernel<D, MT>), dim3((unsigned)((int64_t)p.B * p.hkv * p.rows)), dim3(256), 0,
-                     stream, p);
+  const int64_t items = (int64_t)p.B * p.hkv * p.mblocks, rows = p.rows < MT * 16 ? p.rows : MT * 16;
+  int64_t jr = items * rows / JOIN_BLOCKS;
+  jr = jr < 1 ? 1 : jr > rows ? rows : jr;
+  const int64_t jblocks = (rows + jr - 1) / jr;
+  hipLaunchKernelGGL((attention_join_kernel<D, MT>), dim3((unsigned)(items * jblocks)), dim3(256), 0, stream, p, (int)jr,
+                     (int)jblocks);
   return hip_status(hipGetLastError());
 }
 
@@ -641,7 +742,9 @@ int launch_tree_attention(const AttentionArgs& a, hipStream_t stream) {
   p.ldq = a.ldq;
   p.ld_pages = a.ld_pages;
   p.n_pages = a.cache.pages;
-  p.scale2 = a.scale * 1.4426950408889634f;
+  p.scale2 = a.scale == 0.f ? 1.f : (a.scale < 0.f ? -a.scale : a.scale) * 1.4426950408889634f;
+  p.q_keep = a.scale == 0.f ? 0u : ~0u;
+  p.q_flip = a.scale < 0.f ? 0x80008000u : 0u;
   p.B = (int)a.B;
   p.T = (int)a.T;
   p.hq = (int)a.hq;

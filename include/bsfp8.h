@@ -393,6 +393,7 @@ BSFP8_API size_t bsfp8_attention_workspace_bytes(int64_t B, int64_t T, int64_t h
  *   lens  : int32_t [B] (device), the nodes included; cut to [0, min(max_len, ld_pages * page)].
  *   nodes : int32_t [B] (device), cut to [0, T]; NULL: T everywhere. Rows t >= nodes[b] are zeros.
  *   mask  : int64_t [B][T] (device) or NULL; with a mask T <= 64.
+ *   scale : finite (BSFP8_EINVAL).
  *   out   : bf16 [B][T][hq][dim] (contiguous, 16-byte aligned). A node that sees nothing gets zeros.
  * Values of positions that a node does not see never reach it, also when they are NaN or infinite
  * (a rejected draft's leftovers, a page never written). hq is a multiple of cache->heads, at most
