@@ -174,6 +174,7 @@ int check_cache(const bsfp8_kv_cache* c) {
   if ((c->dim != 64 && c->dim != 128 && c->dim != 192 && c->dim != 256) || c->page < 16 || c->page % 16) return BSFP8_ESHAPE;
   if (c->heads < 1 || c->heads > 65536 || c->pages < 0 || c->page >= ((int64_t)1 << 31)) return BSFP8_ESHAPE;
   if (c->pages >= ((int64_t)1 << 31) || c->pages * c->page >= ((int64_t)1 << 31)) return BSFP8_ESHAPE;
+  if (c->pages * c->page / 16 * c->heads >= ((int64_t)1 << 31)) return BSFP8_ESHAPE;   // groups of 16 tokens are counted in 32 bits
   if (c->pages == 0) return BSFP8_OK;
   if (!c->kq || !c->ks || !c->vq || !c->vs) return BSFP8_EINVAL;
   if (!aligned16(c->kq) || !aligned16(c->ks) || !aligned16(c->vq) || !aligned16(c->vs)) return BSFP8_ESTRIDE;

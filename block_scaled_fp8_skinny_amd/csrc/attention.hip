@@ -23,6 +23,8 @@
 // all sequences, in order, are divided into equal runs, one per workgroup, so that ragged lengths
 // leave nobody idle; a head that falls into several runs leaves partial (m, l, O) in the workspace
 // for a second kernel to join.
+#include <type_traits>
+
 #include "device.h"
 
 namespace bsfp8 {
@@ -31,7 +33,6 @@ namespace {
 constexpr int NW = 4;                               // waves per workgroup
 constexpr int TILE = 32;                            // tokens of a wave's tile
 constexpr int UNIT = NW * TILE;
-constexpr int TABLE = 512;                          // page numbers held in LDS at a time
 constexpr float MOVE = 8.f;
 constexpr float M_NONE = -1e30f;                    // reference of a row that has seen nothing
 
@@ -47,11 +48,12 @@ struct AttnParams {
   float scale2;                                     // |scale| * log2 e (1 for a scale of 0)
   uint32_t q_keep, q_flip;                          // the scale's sign, or a scale of 0, on the queries
   int B, T, hq, hkv, g, rows, mblocks, page, max_len, nwg;
+  int br, unit, unit_shift;                         // rows of a block, tokens of a unit and their logarithm
   FastDiv dpage, dg;
 };
 
 __device__ __forceinline__ int seq_len(const AttnParams& p, int b) { return max(0, min(p.lens[b], p.max_len)); }
-__device__ __forceinline__ int seq_units(const AttnParams& p, int b) { return (seq_len(p, b) + UNIT - 1) / UNIT; }
+__device__ __forceinline__ int seq_units(const AttnParams& p, int b) { return (seq_len(p, b) + p.unit - 1) >> p.unit_shift; }
 
 // The run of units of workgroup w out of `total`: the first `rem` runs hold per + 1.
 struct Runs {
@@ -108,15 +110,63 @@ __device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
   return reinterpret_cast<const uint8_t*>((uint64_t)hi << 32 | lo);
 }
-__device__ __forceinline__ void gload_lds16(const uint8_t* base, uint32_t off, lds_addr_t lds) {
+// N loads of 1 KB from one base to N consecutive kilobytes of LDS
+template <int N>
+__device__ __forceinline__ void gload_lds16(const uint8_t* base, const uint32_t* off, lds_addr_t lds) {
+  static_assert(N >= 1 && N <= 4, "up to four kilobytes");
   uint32_t saved;
-  asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %2, %3\n\ts_mov_b32 m0, %0"
-               : "=&s"(saved) : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(uniform(base)) : "memory");
+  const uint32_t to = __builtin_amdgcn_readfirstlane(lds);
+  base = uniform(base);
+  if constexpr (N == 1)
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %3, %2\n\ts_mov_b32 m0, %0"
+                 : "=&s"(saved) : "s"(to), "s"(base), "v"(off[0]) : "memory");
+  else if constexpr (N == 2)
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %3, %2\n\t"
+                 "s_add_i32 m0, m0, 0x400\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %4, %2\n\ts_mov_b32 m0, %0"
+                 : "=&s"(saved) : "s"(to), "s"(base), "v"(off[0]), "v"(off[1]) : "memory", "scc");
+  else if constexpr (N == 3)
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %3, %2\n\t"
+                 "s_add_i32 m0, m0, 0x400\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %4, %2\n\t"
+                 "s_add_i32 m0, m0, 0x400\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %5, %2\n\ts_mov_b32 m0, %0"
+                 : "=&s"(saved) : "s"(to), "s"(base), "v"(off[0]), "v"(off[1]), "v"(off[2]) : "memory", "scc");
+  else
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %3, %2\n\t"
+                 "s_add_i32 m0, m0, 0x400\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %4, %2\n\t"
+                 "s_add_i32 m0, m0, 0x400\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %5, %2\n\t"
+                 "s_add_i32 m0, m0, 0x400\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %6, %2\n\ts_mov_b32 m0, %0"
+                 : "=&s"(saved) : "s"(to), "s"(base), "v"(off[0]), "v"(off[1]), "v"(off[2]), "v"(off[3]) : "memory", "scc");
 }
 __device__ __forceinline__ void gload_lds4(const uint8_t* addr, lds_addr_t lds) {
   uint32_t saved;
   asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %2, off\n\ts_mov_b32 m0, %0"
                : "=&s"(saved) : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(addr) : "memory");
+}
+
+// Where the 16-token groups of a stretch of a sequence lie, in LDS: entry i = the group of tokens t0 + 16 i .., as its
+// index among the cache's groups of all heads ((page, head) major, so its codes start at 16 D times that), or -1
+// past the sequence's end and in a page that does not exist. Filled by the whole workgroup, between barriers;
+// true if a group below the end is absent.
+constexpr int TABLE = 512;                          // the last eight hold the waves' findings
+constexpr int STRETCH = (TABLE - 8) * 16;
+__device__ __forceinline__ bool fill_table(const AttnParams& p, int b, int h, int t0, int len, int32_t* table) {
+  __syncthreads();                                  // whatever used the table, ring and buffers is done
+  bool absent = false;
+  for (int i = threadIdx.x; i < TABLE - 8; i += blockDim.x) {
+    const int t = t0 + i * 16;
+    int entry = -1;
+    if (t < len) {
+      const int at = fdiv(t, p.dpage), pg = p.pages[(int64_t)b * p.ld_pages + at];
+      if (pg >= 0 && pg < p.n_pages) entry = (int)((((int64_t)pg * p.hkv + h) * p.page + (t - at * p.page)) >> 4);
+      else absent = true;
+    }
+    table[i] = entry;
+  }
+  absent = __any(absent);
+  if ((threadIdx.x & 63) == 0) table[TABLE - 8 + (threadIdx.x >> 6)] = absent;
+  __syncthreads();
+  int any = 0;
+  for (int w = 0; w < (int)blockDim.x / 64; ++w) any |= table[TABLE - 8 + w];
+  return __builtin_amdgcn_readfirstlane(any) != 0;
 }
 
 // Geometry of one 16-token group in LDS.
@@ -177,23 +227,17 @@ __device__ __forceinline__ int v_value(int x, int i) {
 // NaN and infinite values of V (a, four operand tiles) must not reach rows that do not see their token,
 // though 0 * NaN is NaN in the product: they are replaced by zeros here, and the rows that do see one
 // (the product of the flags of such values with the flags of seen tokens is positive) get NaN.
+__device__ __forceinline__ uint32_t nonfinite(uint32_t v) {   // ones in the halves of a bf16 pair that are NaN or infinite
+  return ((v & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((v & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
+}
 template <int MT>
-__device__ __forceinline__ void unseen_nonfinite(bf16x8_t (&a)[4], const uint32_t (&sees)[MT], f32x4_t* o, int stride) {
-  auto bad = [](uint32_t v) {                       // ones where a half is NaN or infinite
-    return ((v & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((v & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
-  };
-  uint32_t any = 0;
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) any |= bad(__builtin_bit_cast(u32x4_t, a[k])[j]);
-  if (!__any(any != 0)) return;
+__device__ __forceinline__ void flag_rows(bf16x8_t (&a)[4], const uint32_t (&sees)[MT], f32x4_t* o, int stride) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     u32x4_t v = __builtin_bit_cast(u32x4_t, a[k]), flag;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t x = bad(v[j]);
+      const uint32_t x = nonfinite(v[j]);
       flag[j] = 0x3F803F80u & x;
       v[j] &= ~x;
     }
@@ -211,6 +255,68 @@ __device__ __forceinline__ void unseen_nonfinite(bf16x8_t (&a)[4], const uint32_
         if (n[r] > 0.f) o[mt * stride + k][r] = __uint_as_float(0x7FC00000u);
     }
   }
+}
+template <int MT>
+__device__ __forceinline__ void unseen_nonfinite(bf16x8_t (&a)[4], const uint32_t (&sees)[MT], f32x4_t* o, int stride) {
+  uint32_t any = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) any |= nonfinite(__builtin_bit_cast(u32x4_t, a[k])[j]);
+  if (__any(any != 0)) flag_rows<MT>(a, sees, o, stride);
+}
+
+// Scores of tokens that a row does not see: -inf, and its bit of `sees` cleared. s: two 16-token groups of MT
+// row blocks, m = the lane's row of the first block, tok0 = its first token of the first group.
+template <int MT>
+__device__ __forceinline__ void mask_scores(const AttnParams& p, int b, int m, int here, int prefix, int len, int tok0,
+                                            int pg0, int pg1, f32x4_t (&s)[2][MT], uint32_t (&sees)[MT]) {
+  asm volatile("" : "+v"(m), "+v"(tok0));           // nothing of this is worth a register across the loop
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt, m += 16) {
+    const int nd = m < p.rows ? fdiv(m, p.dg) : here;
+    uint64_t bits = 0;
+    if (p.mask && nd < here) bits = (uint64_t)p.mask[(int64_t)b * p.T + nd];
+    uint32_t see = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int tok = tok0 + (e >> 2) * 16 + (e & 3), rel = tok - prefix;
+      bool seen = tok < len && (e < 4 ? pg0 : pg1) >= 0 && nd < here;
+      if (rel >= 0) seen = seen && (p.mask ? (bits >> (rel & 63) & 1) != 0 : rel <= nd);
+      s[e >> 2][mt][e & 3] = seen ? s[e >> 2][mt][e & 3] : -__builtin_inff();
+      see |= seen ? 1u << e : 0u;
+    }
+    sees[mt] = see;
+  }
+}
+
+// The weights 2^(s - m) of one row's eight scores (q . k, times scale2 for the base-2 score) as the B operand, and
+// their sum; true (for the wave) when the reference moved: then f is the factor of everything so far. The
+// weights are rounded to bf16 for the matrix product (at most half a step, 2^-8, each); the sum takes them
+// unrounded.
+__device__ __forceinline__ bool weights(const f32x4_t& s0, const f32x4_t& s1, float scale2, float& mref, float& l,
+                                        bf16x8_t& pf, float& f) {
+  float x[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = e < 4 ? s0[e] : s1[e - 4];
+  float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]))) * scale2;
+  const bool moved = __any(top > mref + MOVE);
+  if (moved) {
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    const float m = fmaxf(mref, top);
+    f = __builtin_amdgcn_exp2f(mref - m);
+    mref = m;
+    l *= f;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    x[e] = __builtin_amdgcn_exp2f(fmaf(x[e], scale2, -mref));
+    l += x[e];
+  }
+  const u32x4_t w = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
+  pf = __builtin_bit_cast(bf16x8_t, w);
+  return moved;
 }
 
 // Scale factors (2^(byte - 127), in the exponent field; the conversions read nothing else of the operand,
@@ -265,6 +371,7 @@ __global__ void __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) attention_kernel(At
   constexpr int ND = D / 16, NK = D / 32, BR = MT * 16;
   constexpr int RING = NW * NS * G::STAGE, JOIN = 2 * MT * ND * 1024;
   constexpr int BYTES = RING > JOIN ? RING : JOIN;
+  static_assert(UNIT == 128, "the plan's unit");
   static_assert((NS - 1) * G::PER_TILE <= 63, "vector memory counter range");
   static_assert(NW * BR * 8 <= TABLE * 4, "the statistics take the table's place");
   __shared__ __align__(16) uint8_t ring[BYTES];
@@ -327,51 +434,37 @@ __global__ void __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) attention_kernel(At
       for (int i = 0; i < ND; ++i) o[mt][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     }
 
-    for (int uc = ua; uc < ub;) {                   // as many units as the table's page numbers cover
-      const int p0 = fdiv(uc * UNIT, p.dpage);
-      const int uz = (int)min((int64_t)ub, ((int64_t)p0 + TABLE) * p.page / UNIT);
-      const int np = fdiv(min(uz * UNIT, len) - 1, p.dpage) + 1 - p0;
-      if (uc != ua) __syncthreads();                // the table is free
-      for (int i = threadIdx.x; i < np; i += 64 * NW) {
-        const int pg = p.pages[(int64_t)b * p.ld_pages + p0 + i];
-        table[i] = pg >= 0 && pg < p.n_pages ? pg : -1;
-      }
-      __syncthreads();
-      const int t0 = uc * UNIT + wave * TILE;       // this wave's first token; then every UNIT
+    for (int uc = ua; uc < ub;) {                   // as many units as the table covers
+      const int uz = min(ub, uc + STRETCH / UNIT), tbase = uc * UNIT;
+      const bool absent = fill_table(p, b, h, tbase, len, table);
+      const int t0 = tbase + wave * TILE;           // this wave's first token; then every UNIT
       const int nt = t0 < len ? min(uz - uc, (len - t0 + UNIT - 1) / UNIT) : 0;
 
-      auto page_of = [&](int t) {                   // page number of the group at t; -1: no tokens there
-        return t < len ? __builtin_amdgcn_readfirstlane(table[fdiv(t, p.dpage) - p0]) : -1;
-      };
       auto issue = [&](int i) {
         uint8_t* st = my_ring + (i % NS) * G::STAGE;
-        int64_t at[2];                              // the groups' first rows; absent tokens: some page, not used
+        const int2 en = *reinterpret_cast<const int2*>(table + ((t0 - tbase + i * UNIT) >> 4));
+        // absent tokens: some group, not used
+        const int64_t at[2] = {max(__builtin_amdgcn_readfirstlane(en.x), 0), max(__builtin_amdgcn_readfirstlane(en.y), 0)};
 #pragma unroll
         for (int gr = 0; gr < 2; ++gr) {
-          const int t = t0 + i * UNIT + gr * 16;
-          const int pg = max(page_of(t), 0);
-          const int off = t < len ? t - fdiv(t, p.dpage) * p.page : 0;
-          at[gr] = ((int64_t)pg * p.hkv + h) * p.page + off;
-#pragma unroll
-          for (int n = 0; n < G::LOADS; ++n) {
-            gload_lds16(p.kq + at[gr] * D, ksrc[n], lds_addr(st + gr * G::CODES + n * 1024));
-            gload_lds16(p.vq + at[gr] * D, vsrc[n], lds_addr(st + (2 + gr) * G::CODES + n * 1024));
-          }
+          gload_lds16<G::LOADS>(p.kq + at[gr] * (16 * D), ksrc, lds_addr(st + gr * G::CODES));
+          gload_lds16<G::LOADS>(p.vq + at[gr] * (16 * D), vsrc, lds_addr(st + (2 + gr) * G::CODES));
         }
         constexpr int Q = D / 8;                    // dwords of one group's scales
 #pragma unroll
         for (int n = 0; n < G::SLOADS; ++n) {
           const int e = n * 64 + lane, quarter = e / Q;
-          const uint8_t* a = (quarter & 2 ? p.vs : p.ks) + (quarter & 1 ? at[1] : at[0]) * (D / 32);
+          const uint8_t* a = (quarter & 2 ? p.vs : p.ks) + (quarter & 1 ? at[1] : at[0]) * (D / 2);
           if (e < 4 * Q) gload_lds4(a + (e - quarter * Q) * 4, lds_addr(st + 4 * G::CODES + n * 256));
         }
       };
       auto compute = [&](int i) {
         const uint8_t* st = my_ring + (i % NS) * G::STAGE;
         const uint8_t* scales = st + 4 * G::CODES;
-        const int t = t0 + i * UNIT, pg0 = page_of(t), pg1 = page_of(t + 16);
-        // a tile that some row does not see whole: nodes, the sequence's end, an absent page (uniform)
-        const bool special = t + TILE > prefix || t + TILE > len || pg0 < 0 || pg1 < 0;
+        const int t = t0 + i * UNIT;
+        // a tile that some row may not see whole: nodes, the sequence's end, absent pages (uniform)
+        const bool special = t + TILE > min(prefix, len) || absent;
+        const int* pg = table + ((t - tbase) >> 4);   // the groups' entries: below 0, no tokens (special tiles)
         f32x4_t s[2][MT];
         float kf[2][D / 64];
 #pragma unroll
@@ -402,51 +495,17 @@ __global__ void __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) attention_kernel(At
         }
         // tokens of the lane: t + (e / 4) * 16 + q4 * 4 + e % 4, e = 0..7
         bf16x8_t pf[MT];
-        uint32_t sees[MT];                          // bit e: the row sees token e (special tiles)
-        if (special) {
+        uint32_t sees[MT];                          // bit e: the row sees token e
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            const int m = mb * BR + mt * 16 + r16, nd = m < p.rows ? fdiv(m, p.dg) : here;
-            uint64_t bits = 0;
-            if (p.mask && nd < here) bits = (uint64_t)p.mask[(int64_t)b * p.T + nd];
-            uint32_t see = 0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int tok = t + (e >> 2) * 16 + q4 * 4 + (e & 3), rel = tok - prefix;
-              bool seen = tok < len && (e < 4 ? pg0 : pg1) >= 0 && nd < here;
-              if (rel >= 0) seen = seen && (p.mask ? (bits >> (rel & 63) & 1) != 0 : rel <= nd);
-              s[e >> 2][mt][e & 3] = seen ? s[e >> 2][mt][e & 3] : -__builtin_inff();
-              see |= seen ? 1u << e : 0u;
-            }
-            sees[mt] = see;
-          }
-        } else {
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) sees[mt] = 0xFF;
-        }
+        for (int mt = 0; mt < MT; ++mt) sees[mt] = 0xFF;
+        if (special) mask_scores<MT>(p, b, mb * BR + r16, here, prefix, len, t + q4 * 4, pg[0], pg[1], s, sees);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          float x[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = s[e >> 2][mt][e & 3];
-          float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]))) * p.scale2;
-          if (__any(top > mref[mt] + MOVE)) {
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            const float m = fmaxf(mref[mt], top), f = __builtin_amdgcn_exp2f(mref[mt] - m);
-            mref[mt] = m;
-            l[mt] *= f;
+          float f;
+          if (weights(s[0][mt], s[1][mt], p.scale2, mref[mt], l[mt], pf[mt], f)) {
 #pragma unroll
             for (int k = 0; k < ND; ++k) o[mt][k] *= f;
           }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            x[e] = __builtin_amdgcn_exp2f(fmaf(x[e], p.scale2, -mref[mt]));
-            l[mt] += x[e];
-          }
-          const u32x4_t w = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                             pack_bf16x2(x[6], x[7])};
-          pf[mt] = __builtin_bit_cast(bf16x8_t, w);
         }
         // V: dword c of the lane's values of each token; their block is the same for all four
 #pragma unroll
@@ -467,7 +526,7 @@ __global__ void __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) attention_kernel(At
           if (special) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              if (t + (e >> 2) * 16 + q4 * 4 + (e & 3) >= len || (e < 4 ? pg0 : pg1) < 0) {
+              if (t + (e >> 2) * 16 + q4 * 4 + (e & 3) >= len || pg[e >> 2] < 0) {
                 raw[e] = 0;
                 f[e] = 1.f;
               }
@@ -594,9 +653,10 @@ __global__ void __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) attention_kernel(At
 // four values of a row each; the workgroup's 256 / (D/4) slices take rows side by side, or, when a
 // row's partial results are many, all take one row and every so-many-th result of it.
 constexpr int JOIN_BLOCKS = 1024;
-template <int D, int MT>
+template <int D>
 __global__ void __launch_bounds__(256) attention_join_kernel(AttnParams p, int jr, int jblocks) {
-  constexpr int LD = D / 4, SL = 256 / LD, BR = MT * 16;
+  constexpr int LD = D / 4, SL = 256 / LD;
+  const int BR = p.br;
   __shared__ f32x4_t sums[SL][LD];
   const int lane = threadIdx.x & 63;
   const int part = blockIdx.x % (unsigned)jblocks;
@@ -684,33 +744,379 @@ __global__ void __launch_bounds__(256) attention_join_kernel(AttnParams p, int j
   }
 }
 
-struct AttnPlan {
-  int mt, mblocks, nwg;
+// ------------------------------------------------------------------------------------------------
+// Many rows (trees, or many heads that share a key/value head): the waves of a workgroup take different
+// rows, MT blocks of 16 each, and share the tokens. Codes and scales of a tile travel through a ring of
+// STAGES tiles in LDS (the LDS mode of global loads); from there K and V are rebuilt once per workgroup
+// into operand order, also in LDS (a fragment of one MFMA is 64 lanes x 16 bytes, read back without bank
+// conflicts), two buffers deep: while a tile is computed, the next one is rebuilt, a unit of K and one of V
+// by each wave. The operand order of V is value c * 64 + x * 4 + k for column x of 16-row tile 4c + k.
+// ------------------------------------------------------------------------------------------------
+constexpr int WW = 8;                               // waves per workgroup
+
+template <int D>
+struct Wide {
+  static constexpr int TOKENS = D == 64 ? 128 : D == 128 ? 64 : 32;   // of a tile
+  static constexpr int SHIFT = D == 64 ? 7 : D == 128 ? 6 : 5;
+  static constexpr int SETS = TOKENS / 32, GROUPS = TOKENS / 16;
+  static constexpr int KU = GROUPS * (D / 64), VU = SETS * (D / 64) * 2;   // rebuilding units: 16 codes, 8 x 2 codes a lane
+  static constexpr int KF = GROUPS * (D / 32) * 64, VF = SETS * (D / 16) * 64;   // 16-byte words of a buffer
+  static constexpr int CODES = TOKENS * D;                            // bytes of K's codes of a tile, and of V's
+  static constexpr int SCALES = CODES / 32;
+  static constexpr int STAGE = 2 * CODES + 2 * SCALES, STAGES = 4;    // K, V, K's scales, V's scales
+  static constexpr int CL = 2 * GROUPS * (D / 64), LOADS = CL + 2 * GROUPS;   // loads of a tile: 1 KB of codes; a group's scales
+  static_assert(KU <= WW && VU <= WW, "one unit of each per wave");
+  static_assert(CODES * 4 + STAGES * STAGE + TABLE * 4 <= 160 * 1024 && 2 * (KF + VF) * 16 == CODES * 8, "LDS");
 };
-// Row blocks of 16 * mt rows, and the grid: every unit its own workgroup up to two per CU.
+
+template <int D, int MT>
+__global__ void __launch_bounds__(64 * WW, 2) attention_wide_kernel(AttnParams p) {
+  using W = Wide<D>;
+  constexpr int ND = D / 16, NK = D / 32, NC = D / 64, BR = WW * MT * 16, STAGES = W::STAGES;
+  __shared__ __align__(16) uint4 frags[2][W::KF + W::VF];
+  __shared__ __align__(16) uint8_t ring[STAGES * W::STAGE];
+  __shared__ int32_t table[TABLE];
+  __shared__ int spoiled[3][W::SETS];               // of tile i in slot i % 3: a set holds NaN or infinite values of V that some row may not see
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, q4 = lane >> 4;
+  const Batch batch(p, lane);
+  const int ipb = p.hkv * p.mblocks;
+  const Runs runs(batch.total * ipb, p.nwg);
+  int u = runs.start(blockIdx.x);
+  const int u_end = runs.start(blockIdx.x + 1);
+  if (u >= u_end) return;
+  int before;
+  int b = batch.find(p, u / ipb, before);
+  int base = before * ipb;
+  const int first_u = u;
+
+  // this wave's loads of a tile: 1 KB of a group's codes of K or V, or the scales of a group
+  constexpr int MY = (W::LOADS + WW - 1) / WW;
+  struct {
+    const uint8_t* base;
+    uint32_t off;
+    int group, lds;
+  } my[MY];
+#pragma unroll
+  for (int k = 0; k < MY; ++k) {
+    const int n = wave + k * WW;
+    const bool codes = n < W::CL;
+    const int per = codes ? 2 * NC : 2, at = codes ? n : n - W::CL;
+    const int gr = at / per, x = at % per, c = x % NC;
+    const bool is_v = x >= per / 2;                 // the first half of a group's loads are K's
+    my[k].group = gr;
+    my[k].base = codes ? (is_v ? p.vq : p.kq) : (is_v ? p.vs : p.ks);
+    my[k].off = is_v ? v_source<D>(c, lane) : k_source<D>(c, lane);
+    my[k].lds = codes ? (is_v ? W::CODES : 0) + gr * 16 * D + c * 1024 : 2 * W::CODES + (is_v ? W::SCALES : 0) + gr * (D / 2);
+  }
+
+  while (u < u_end) {
+    const int len = seq_len(p, b), units = (len + W::TOKENS - 1) / W::TOKENS;
+    const int item = (u - base) / units;
+    const int ua = (u - base) - item * units, ub = min(units, ua + (u_end - u));
+    const int h = item / p.mblocks, mb = item - h * p.mblocks;
+    const int here = p.nodes ? max(0, min(p.nodes[b], p.T)) : p.T;
+    const int prefix = len - here;
+    const int m0 = mb * BR + wave * MT * 16;        // this wave's first row
+
+    bf16x8_t qf[MT][NK];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const int m = m0 + mt * 16 + r16, nd = fdiv(min(m, p.rows - 1), p.dg), hd = m - nd * p.g;
+      const bool on = m < p.rows && nd < here;
+      const uint16_t* src = p.q + ((int64_t)b * p.T + nd) * p.ldq + ((int64_t)h * p.g + hd) * D;
+#pragma unroll
+      for (int j = 0; j < NK; ++j) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (on) v = *reinterpret_cast<const uint4*>(src + (j >> 1) * 64 + q4 * 16 + (j & 1) * 8);
+        const u32x4_t w = {(v.x & p.q_keep) ^ p.q_flip, (v.y & p.q_keep) ^ p.q_flip, (v.z & p.q_keep) ^ p.q_flip,
+                           (v.w & p.q_keep) ^ p.q_flip};
+        qf[mt][j] = __builtin_bit_cast(bf16x8_t, w);
+      }
+    }
+    f32x4_t o[MT][ND];
+    float mref[MT], l[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      mref[mt] = M_NONE;
+      l[mt] = 0.f;
+#pragma unroll
+      for (int i = 0; i < ND; ++i) o[mt][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+
+    for (int uc = ua; uc < ub;) {                   // as many tiles as the table covers
+      const int uz = min(ub, uc + STRETCH / W::TOKENS), tbase = uc * W::TOKENS;
+      const bool absent = fill_table(p, b, h, tbase, len, table);   // (nothing is in flight here)
+      auto issue = [&](int i) {
+        uint8_t* st = ring + (i % STAGES) * W::STAGE;
+        const int* en = table + (i - uc) * W::GROUPS;
+#pragma unroll
+        for (int k = 0; k < MY; ++k) {
+          if (wave + k * WW >= W::LOADS) break;
+          const int64_t at = max(__builtin_amdgcn_readfirstlane(en[my[k].group]), 0);   // absent: some group, not used
+          if (k < W::CL / WW || wave + k * WW < W::CL)
+            gload_lds16<1>(my[k].base + at * (16 * D), &my[k].off, lds_addr(st + my[k].lds));
+          else if (lane < D / 8)
+            gload_lds4(uniform(my[k].base + at * (D / 2)) + lane * 4, lds_addr(st + my[k].lds));
+        }
+      };
+      // wait for this wave's loads but those of the newest `tiles` tiles
+      auto landed = [&](int tiles) {
+        constexpr int FEW = W::LOADS / WW, MANY = (W::LOADS + WW - 1) / WW;
+        if (wave < W::LOADS % WW) {
+          if (tiles >= 2) wait_vmcnt_le<2 * MANY>();
+          else if (tiles == 1) wait_vmcnt_le<MANY>();
+          else wait_vmcnt_le<0>();
+        } else {
+          if (tiles >= 2) wait_vmcnt_le<2 * FEW>();
+          else if (tiles == 1) wait_vmcnt_le<FEW>();
+          else wait_vmcnt_le<0>();
+        }
+      };
+      auto rebuild = [&](int i, uint4* buf) {
+        const uint8_t* st = ring + (i % STAGES) * W::STAGE;
+        if (wave < W::KU) {
+          const int gr = wave / NC, j = wave % NC;
+          const uint4 w = *reinterpret_cast<const uint4*>(st + gr * 16 * D + r16 * D + (((4 * j + q4) ^ Geo<D>::swizzle(r16)) * 16));
+          const float f = block_scale(st[2 * W::CODES + gr * (D / 2) + r16 * (D / 32) + 2 * j + (q4 >> 1)]);
+          uint4* dst = buf + (gr * NK + 2 * j) * 64 + lane;
+          dst[0] = __builtin_bit_cast(uint4, dequant8(w.x, w.y, f));
+          dst[64] = __builtin_bit_cast(uint4, dequant8(w.z, w.w, f));
+        }
+        if (wave < W::VU) {
+          const int half = wave & 1, set = (wave >> 1) / NC, c = (wave >> 1) % NC;
+          const int t = i * W::TOKENS + set * 32;
+          uint32_t raw[8];
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int gr = set * 2 + (e >> 2), j = e & 3;
+            raw[e] = *reinterpret_cast<const uint16_t*>(st + W::CODES + gr * 16 * D + (j * 4 + q4) * D + c * 64 + r16 * 4 + half * 2);
+            f[e] = block_scale(st[2 * W::CODES + W::SCALES + gr * (D / 2) + (q4 * 4 + j) * (D / 32) + 2 * c + (r16 >> 3)]);
+          }
+          if (t + 32 > len || absent) {             // tokens that are not there: zeros
+            const int* pg = table + ((t - tbase) >> 4);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (t + (e >> 2) * 16 + q4 * 4 + (e & 3) >= len || pg[e >> 2] < 0) {
+                raw[e] = 0;
+                f[e] = 1.f;
+              }
+          }
+          u32x4_t a0, a1;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t x = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw[2 * j], f[2 * j], false));
+            const uint32_t y = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw[2 * j + 1], f[2 * j + 1], false));
+            a0[j] = __builtin_amdgcn_perm(y, x, 0x05040100u);
+            a1[j] = __builtin_amdgcn_perm(y, x, 0x07060302u);
+          }
+          // a row may not see its token: NaN and infinite values leave the product (see poison)
+          if (t + 32 > prefix) {
+            uint32_t any = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t x = nonfinite(a0[j]), y = nonfinite(a1[j]);
+              a0[j] &= ~x;
+              a1[j] &= ~y;
+              any |= x | y;
+            }
+            if (__any(any != 0) && lane == 0) spoiled[i % 3][set] = 1;
+          }
+          uint4* dst = buf + W::KF + (set * ND + 4 * c + 2 * half) * 64 + lane;
+          dst[0] = __builtin_bit_cast(uint4, a0);
+          dst[64] = __builtin_bit_cast(uint4, a1);
+        }
+      };
+      auto ask_k = [&](const uint4* buf, int set, uint4 (&fr)[2 * NK]) {
+#pragma unroll
+        for (int j = 0; j < 2 * NK; ++j) fr[j] = buf[(set * 2 * NK + j) * 64 + lane];
+      };
+      // Rows that see a NaN or infinite value of V get NaN there (the rebuilt fragments hold zeros in its place):
+      // the product of such values' flags, from the raw codes, with the flags of seen tokens is positive.
+      auto poison = [&](int i, int set, const uint32_t (&sees)[MT]) {
+        const uint8_t* st = ring + (i % STAGES) * W::STAGE;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          uint32_t raw[8];
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int gr = set * 2 + (e >> 2), j = e & 3;
+            raw[e] = *reinterpret_cast<const uint32_t*>(st + W::CODES + gr * 16 * D + (j * 4 + q4) * D + c * 64 + r16 * 4);
+            f[e] = block_scale(st[2 * W::CODES + W::SCALES + gr * (D / 2) + (q4 * 4 + j) * (D / 32) + 2 * c + (r16 >> 3)]);
+          }
+          bf16x8_t a[4];
+          v_operands(raw, f, a);
+          flag_rows<MT>(a, sees, &o[0][0] + 4 * c, ND);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      };
+      // One tile; `kf` = the K fragments of its first set, asked for before. Fragments are asked for a phase ahead: V's
+      // before the softmax, the next set's K before the products with V.
+      auto compute = [&](int i, const uint4* buf, uint4 (&kf)[2 * NK]) {
+#pragma unroll
+        for (int set = 0; set < W::SETS; ++set) {
+          const int t = i * W::TOKENS + set * 32;
+          // some row may not see all of it: nodes, the sequence's end, absent pages (uniform)
+          const bool special = t + 32 > min(prefix, len) || absent;
+          f32x4_t s[2][MT];
+#pragma unroll
+          for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) s[gr][mt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < NK; ++j)
+#pragma unroll
+            for (int gr = 0; gr < 2; ++gr)
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+                s[gr][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, kf[gr * NK + j]), qf[mt][j],
+                                                                    s[gr][mt], 0, 0, 0);
+          const uint4* vf = buf + W::KF + set * ND * 64 + lane;
+          uint4 fr[ND];
+#pragma unroll
+          for (int k = 0; k < ND; ++k) fr[k] = vf[k * 64];
+          __builtin_amdgcn_sched_barrier(0);
+          if (__builtin_expect(special, 0)) {
+            uint32_t sees[MT];
+            const int* pg = table + ((t - tbase) >> 4);
+            mask_scores<MT>(p, b, m0 + r16, here, prefix, len, t + q4 * 4, pg[0], pg[1], s, sees);
+            if (__builtin_amdgcn_readfirstlane(spoiled[i % 3][set])) poison(i, set, sees);
+          }
+          bf16x8_t pf[MT];
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            float f;
+            if (weights(s[0][mt], s[1][mt], p.scale2, mref[mt], l[mt], pf[mt], f)) {
+#pragma unroll
+              for (int k = 0; k < ND; ++k) o[mt][k] *= f;
+            }
+          }
+          if (set + 1 < W::SETS) ask_k(buf, set + 1, kf);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int k = 0; k < ND; ++k)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+              o[mt][k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, fr[k]), pf[mt], o[mt][k], 0, 0, 0);
+        }
+      };
+
+      // tile i is rebuilt from its stage during iteration i - 1 and computed in iteration i; its loads go out in
+      // iteration i - 3. The barrier that ends an iteration says that everyone's loads of the tile to be
+      // rebuilt next have landed, its buffer's readers are done, and the next tile is whole.
+#pragma unroll 1
+      for (int i = uc; i < min(uc + 3, uz); ++i) issue(i);
+      if (threadIdx.x < 3 * W::SETS) spoiled[threadIdx.x / W::SETS][threadIdx.x % W::SETS] = 0;
+      landed(min(uz - uc, 3) - 1);
+      __syncthreads();
+      rebuild(uc, frags[uc & 1]);
+      landed(max(min(uz - uc, 3) - 2, 0));
+      __syncthreads();
+#pragma unroll 1
+      for (int i = uc; i < uz; ++i) {
+        const uint4* buf = frags[i & 1];
+        uint4 kf[2 * NK];
+        ask_k(buf, 0, kf);
+        if (threadIdx.x < W::SETS) spoiled[(i + 2) % 3][threadIdx.x] = 0;   // read an iteration ago, set in the next
+        if (i + 3 < uz) issue(i + 3);
+        if (i + 1 < uz) rebuild(i + 1, frags[(i + 1) & 1]);
+        __builtin_amdgcn_sched_barrier(0);
+        compute(i, buf, kf);
+        landed(i + 3 < uz ? 1 : 0);                 // all but tile i + 3's: tile i + 2 is there
+        __syncthreads();
+      }
+      uc = uz;
+    }
+
+    const bool whole = ua == 0 && ub == units;
+    const int64_t slot = (int64_t)blockIdx.x * 2 + (u == first_u ? 0 : 1);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      l[mt] += __shfl_xor(l[mt], 16);
+      l[mt] += __shfl_xor(l[mt], 32);
+      const int m = m0 + mt * 16 + r16, row = m - mb * BR;
+      if (m >= p.rows) continue;
+      if (whole) {
+        const int nd = fdiv(m, p.dg);
+        const bool live = nd < here && l[mt] != 0.f;   // NaN passes
+        const float f = 1.f / l[mt];
+        uint16_t* dst = p.out + (((int64_t)b * p.T + nd) * p.hq + (int64_t)h * p.g + (m - nd * p.g)) * D + q4 * 16;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) {
+            u32x4_t w;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int k = 4 * c + (x & 1) * 2, r = e + (x >> 1);
+              w[x] = live ? pack_bf16x2(o[mt][k][r] * f, o[mt][k + 1][r] * f) : 0u;
+            }
+            *reinterpret_cast<u32x4_t*>(dst + c * 64 + e * 4) = w;
+          }
+      } else {
+        float* dst = p.part + (slot * BR + row) * D + q4 * 16;
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<f32x4_t*>(dst + c * 64 + e * 4) =
+                f32x4_t{o[mt][4 * c][e], o[mt][4 * c + 1][e], o[mt][4 * c + 2][e], o[mt][4 * c + 3][e]};
+        if (q4 == 0) p.stat[slot * BR + row] = make_float2(mref[mt], l[mt]);
+      }
+    }
+    u += ub - ua;
+    while (u < u_end && u >= base + seq_units(p, b) * ipb) {
+      base += seq_units(p, b) * ipb;
+      ++b;
+    }
+  }
+}
+
+struct AttnPlan {
+  int wide, mt, br, unit_shift, mblocks, nwg;
+};
+// Rows of a block and the grid: every unit its own workgroup up to one (wide) or two workgroups per CU.
 AttnPlan attention_plan(const AttentionArgs& a) {
   const int64_t rows = a.T * (a.hq / a.cache.heads);
-  const int most = a.cache.dim <= 128 ? 3 : 2;
+  const bool small = a.cache.dim <= 128;
   AttnPlan p;
-  p.mt = (int)((rows + 15) / 16);
-  if (p.mt > most) p.mt = most;
-  p.mblocks = (int)((rows + p.mt * 16 - 1) / (p.mt * 16));
-  const int64_t units = a.B * a.cache.heads * p.mblocks * ((a.max_len + UNIT - 1) / UNIT);
-  p.nwg = (int)(units < 1 ? 1 : units > 512 ? 512 : units);
+  const int narrow = small ? 3 : 2;                 // blocks of 16 rows that a wave of the ring kernel holds
+  p.wide = rows > narrow * 16;
+  const int64_t step = p.wide ? WW * 16 : 16, most = p.wide ? (a.cache.dim == 64 ? 4 : small ? 2 : 1) : narrow;
+  const int64_t blocks = (rows + step * most - 1) / (step * most);
+  p.mt = (int)((rows + step * blocks - 1) / (step * blocks));
+  p.br = (int)(p.mt * step);
+  p.mblocks = (int)((rows + p.br - 1) / p.br);
+  p.unit_shift = !p.wide ? 7 : a.cache.dim == 64 ? 7 : a.cache.dim == 128 ? 6 : 5;
+  const int64_t units = a.B * a.cache.heads * p.mblocks * ((a.max_len + (1 << p.unit_shift) - 1) >> p.unit_shift);
+  const int64_t grid = p.wide ? 256 : 512;
+  p.nwg = (int)(units < 1 ? 1 : units > grid ? grid : units);
   return p;
 }
 
-template <int D, int MT, int NS>
-int run(const AttnParams& p, hipStream_t stream) {
-  hipLaunchKernelGGL((attention_kernel<D, MT, NS>), dim3((unsigned)p.nwg), dim3(64 * NW), 0, stream, p);
-  if (hipGetLastError() != hipSuccess) return BSFP8_EHIP;
-  const int64_t items = (int64_t)p.B * p.hkv * p.mblocks, rows = p.rows < MT * 16 ? p.rows : MT * 16;
+template <int D>
+int join(const AttnParams& p, hipStream_t stream) {
+  const int64_t items = (int64_t)p.B * p.hkv * p.mblocks, rows = p.rows < p.br ? p.rows : p.br;
   int64_t jr = items * rows / JOIN_BLOCKS;
   jr = jr < 1 ? 1 : jr > rows ? rows : jr;
   const int64_t jblocks = (rows + jr - 1) / jr;
-  hipLaunchKernelGGL((attention_join_kernel<D, MT>), dim3((unsigned)(items * jblocks)), dim3(256), 0, stream, p, (int)jr,
+  hipLaunchKernelGGL((attention_join_kernel<D>), dim3((unsigned)(items * jblocks)), dim3(256), 0, stream, p, (int)jr,
                      (int)jblocks);
   return hip_status(hipGetLastError());
+}
+
+template <int D, int MT, int NS>
+int ring(const AttnParams& p, hipStream_t stream) {
+  hipLaunchKernelGGL((attention_kernel<D, MT, NS>), dim3((unsigned)p.nwg), dim3(64 * NW), 0, stream, p);
+  return hipGetLastError() == hipSuccess ? join<D>(p, stream) : BSFP8_EHIP;
+}
+template <int D, int MT>
+int wide(const AttnParams& p, hipStream_t stream) {
+  hipLaunchKernelGGL((attention_wide_kernel<D, MT>), dim3((unsigned)p.nwg), dim3(64 * WW), 0, stream, p);
+  return hipGetLastError() == hipSuccess ? join<D>(p, stream) : BSFP8_EHIP;
 }
 
 inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -719,7 +1125,7 @@ inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 size_t attention_ws_bytes(const AttentionArgs& a) {
   const AttnPlan pl = attention_plan(a);
-  const size_t rows = (size_t)pl.nwg * 2 * pl.mt * 16;
+  const size_t rows = (size_t)pl.nwg * 2 * pl.br;
   return align256(rows * sizeof(float2)) + rows * (size_t)a.cache.dim * 4;
 }
 
@@ -738,7 +1144,7 @@ int launch_tree_attention(const AttentionArgs& a, hipStream_t stream) {
   p.out = a.out;
   p.stat = reinterpret_cast<float2*>(a.ws);
   p.part = reinterpret_cast<float*>(reinterpret_cast<char*>(a.ws) +
-                                    align256((size_t)pl.nwg * 2 * pl.mt * 16 * sizeof(float2)));
+                                    align256((size_t)pl.nwg * 2 * pl.br * sizeof(float2)));
   p.ldq = a.ldq;
   p.ld_pages = a.ld_pages;
   p.n_pages = a.cache.pages;
@@ -756,13 +1162,23 @@ int launch_tree_attention(const AttentionArgs& a, hipStream_t stream) {
   const int64_t held = a.cache.pages == 0 ? 0 : a.ld_pages * a.cache.page;
   p.max_len = (int)(a.max_len < held ? a.max_len : held);
   p.nwg = pl.nwg;
+  p.br = pl.br;
+  p.unit_shift = pl.unit_shift;
+  p.unit = 1 << pl.unit_shift;
   p.dpage = make_fastdiv((uint32_t)a.cache.page);
   p.dg = make_fastdiv((uint32_t)p.g);
   const int D = (int)a.cache.dim, mt = pl.mt;
-  if (D == 64) return mt == 1 ? run<64, 1, 4>(p, stream) : mt == 2 ? run<64, 2, 4>(p, stream) : run<64, 3, 4>(p, stream);
-  if (D == 128) return mt == 1 ? run<128, 1, 2>(p, stream) : mt == 2 ? run<128, 2, 2>(p, stream) : run<128, 3, 2>(p, stream);
-  if (D == 192) return mt == 1 ? run<192, 1, 2>(p, stream) : run<192, 2, 2>(p, stream);
-  return mt == 1 ? run<256, 1, 2>(p, stream) : run<256, 2, 2>(p, stream);
+  if (pl.wide) {
+    if (D == 64)
+      return mt == 1 ? wide<64, 1>(p, stream) : mt == 2 ? wide<64, 2>(p, stream) : mt == 3 ? wide<64, 3>(p, stream)
+                                                                                 : wide<64, 4>(p, stream);
+    if (D == 128) return mt == 1 ? wide<128, 1>(p, stream) : wide<128, 2>(p, stream);
+    return D == 192 ? wide<192, 1>(p, stream) : wide<256, 1>(p, stream);
+  }
+  if (D == 64) return mt == 1 ? ring<64, 1, 4>(p, stream) : mt == 2 ? ring<64, 2, 4>(p, stream) : ring<64, 3, 4>(p, stream);
+  if (D == 128) return mt == 1 ? ring<128, 1, 2>(p, stream) : mt == 2 ? ring<128, 2, 2>(p, stream) : ring<128, 3, 2>(p, stream);
+  if (D == 192) return mt == 1 ? ring<192, 1, 2>(p, stream) : ring<192, 2, 2>(p, stream);
+  return mt == 1 ? ring<256, 1, 2>(p, stream) : ring<256, 2, 2>(p, stream);
 }
 
 }  // namespace bsfp8

@@ -331,7 +331,7 @@ BSFP8_API int bsfp8_gemm_mxfp8(const uint16_t* x, int64_t ldx, int64_t M, int64_
  *   kq, vq : uint8_t e4m3 codes [pages][heads][page][dim] (device, 16-byte aligned);
  *   ks, vs : uint8_t scale bytes [pages][heads][page][dim/32] (device, 16-byte aligned), 2^(byte-127).
  * dim is 64, 128, 192 or 256; page (tokens per page) a multiple of 16; heads >= 1; pages >= 0 and
- * pages * page < 2^31 (offsets inside the cache are 64-bit). Slot s is token s % page of page
+ * pages * page < 2^31, pages * page * heads < 2^35 (offsets inside the cache are 64-bit). Slot s is token s % page of page
  * s / page. Every call below returns BSFP8_ESHAPE for sizes outside these, BSFP8_EINVAL for a
  * missing pointer, BSFP8_ESTRIDE for a misaligned one. */
 typedef struct bsfp8_kv_cache {
