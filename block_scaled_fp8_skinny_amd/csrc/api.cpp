@@ -188,8 +188,9 @@ int check_attention_sizes(int64_t B, int64_t T, int64_t hq, int64_t hkv, int64_t
   if (B < 0 || T < 1 || hkv < 1 || hkv > 65536 || hq < hkv || hq % hkv || hq > 64 * hkv || max_len < 0) return BSFP8_ESHAPE;
   const int64_t lim = (int64_t)1 << 31;
   if (max_len >= lim || B >= lim || T >= lim || B * T >= lim || B * T * hq >= lim) return BSFP8_ESHAPE;
-  // units of 128 positions of a head and a block of at least 16 rows are counted in 32 bits
-  const int64_t blocks = (T * (hq / hkv) + 15) / 16, units = max_len / 128 + 1;
+  // units of at least 32 positions (and the cost of a start) of a head and a block of at least 16 rows are
+  // counted in 32 bits
+  const int64_t blocks = (T * (hq / hkv) + 15) / 16, units = max_len / 32 + 10;
   if (B > 0 && (hkv * blocks >= lim || B * hkv * blocks >= lim / units)) return BSFP8_ESHAPE;
   return BSFP8_OK;
 }

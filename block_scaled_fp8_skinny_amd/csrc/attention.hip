@@ -48,12 +48,20 @@ struct AttnParams {
   float scale2;                                     // |scale| * log2 e (1 for a scale of 0)
   uint32_t q_keep, q_flip;                          // the scale's sign, or a scale of 0, on the queries
   int B, T, hq, hkv, g, rows, mblocks, page, max_len, nwg;
-  int br, unit, unit_shift;                         // rows of a block, tokens of a unit and their logarithm
+  int br, unit, unit_shift, start_cost;             // rows of a block; tokens of a unit and their logarithm
   FastDiv dpage, dg;
 };
 
 __device__ __forceinline__ int seq_len(const AttnParams& p, int b) { return max(0, min(p.lens[b], p.max_len)); }
+// Units of an item, and its length in the order that is cut into runs: `start_cost` more, what it costs a
+// workgroup to begin another item in units (drain, join, queries, table, first tiles), so that runs that
+// hold the beginnings of items get fewer of them.
 __device__ __forceinline__ int seq_units(const AttnParams& p, int b) { return (seq_len(p, b) + p.unit - 1) >> p.unit_shift; }
+
+__device__ __forceinline__ int seq_span(const AttnParams& p, int b) {
+  const int n = seq_units(p, b);
+  return n > 0 ? n + p.start_cost : 0;
+}
 
 // The run of units of workgroup w out of `total`: the first `rem` runs hold per + 1.
 struct Runs {
@@ -73,7 +81,7 @@ struct Batch {
   __device__ __forceinline__ Batch(const AttnParams& p, int lane) {
     c = (p.B + 63) >> 6;
     own = 0;
-    for (int i = lane * c; i < min(lane * c + c, p.B); ++i) own += seq_units(p, i);
+    for (int i = lane * c; i < min(lane * c + c, p.B); ++i) own += seq_span(p, i);
     incl = own;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -88,7 +96,7 @@ struct Batch {
     before = __builtin_amdgcn_readfirstlane(__shfl(incl, l) - __shfl(own, l));
     int b = l * c;
     for (;; ++b) {
-      const int n = seq_units(p, b);
+      const int n = seq_span(p, b);
       if (v < before + n) return b;
       before += n;
     }
@@ -97,7 +105,7 @@ struct Batch {
   __device__ __forceinline__ int before(const AttnParams& p, int b) const {
     const int l = b / c;
     int v = __shfl(incl, l) - __shfl(own, l);
-    for (int i = l * c; i < b; ++i) v += seq_units(p, i);
+    for (int i = l * c; i < b; ++i) v += seq_span(p, i);
     return v;
   }
 };
@@ -144,12 +152,11 @@ __device__ __forceinline__ void gload_lds4(const uint8_t* addr, lds_addr_t lds) 
 
 // Where the 16-token groups of a stretch of a sequence lie, in LDS: entry i = the group of tokens t0 + 16 i .., as its
 // index among the cache's groups of all heads ((page, head) major, so its codes start at 16 D times that), or -1
-// past the sequence's end and in a page that does not exist. Filled by the whole workgroup, between barriers;
-// true if a group below the end is absent.
+// past the sequence's end and in a page that does not exist. Filled by the whole workgroup, with a barrier of the
+// caller's before and after; table_absent, after it, says whether a group below the end is absent.
 constexpr int TABLE = 512;                          // the last eight hold the waves' findings
 constexpr int STRETCH = (TABLE - 8) * 16;
 __device__ __forceinline__ bool fill_table(const AttnParams& p, int b, int h, int t0, int len, int32_t* table) {
-  __syncthreads();                                  // whatever used the table, ring and buffers is done
   bool absent = false;
   for (int i = threadIdx.x; i < TABLE - 8; i += blockDim.x) {
     const int t = t0 + i * 16;
@@ -163,8 +170,10 @@ __device__ __forceinline__ bool fill_table(const AttnParams& p, int b, int h, in
   }
   absent = __any(absent);
   if ((threadIdx.x & 63) == 0) table[TABLE - 8 + (threadIdx.x >> 6)] = absent;
-  __syncthreads();
-  int any = 0;
+  return absent;
+}
+__device__ __forceinline__ bool table_absent(bool mine, const int32_t* table) {
+  int any = mine;
   for (int w = 0; w < (int)blockDim.x / 64; ++w) any |= table[TABLE - 8 + w];
   return __builtin_amdgcn_readfirstlane(any) != 0;
 }
@@ -402,28 +411,37 @@ __global__ void __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) attention_kernel(At
   uint8_t* const my_ring = ring + wave * NS * G::STAGE;
 
   while (u < u_end) {
-    const int len = seq_len(p, b), units = (len + UNIT - 1) / UNIT;
-    const int item = (u - base) / units;            // head and row block
-    const int ua = (u - base) - item * units, ub = min(units, ua + (u_end - u));
+    const int len = seq_len(p, b), units = (len + UNIT - 1) / UNIT, span = units + p.start_cost;
+    const int item = (u - base) / span;             // head and row block
+    const int va = (u - base) - item * span, vb = min(span, va + (u_end - u));
+    const int ua = max(va - p.start_cost, 0), ub = vb - p.start_cost;
     const int h = item / p.mblocks, mb = item - h * p.mblocks;
     const int here = p.nodes ? max(0, min(p.nodes[b], p.T)) : p.T;
     const int prefix = len - here;
 
-    __syncthreads();                                // the last run's ring, queries and statistics are done with
-    for (int i = threadIdx.x; i < MT * NK * 64; i += 64 * NW) {
-      const int l = i & 63, j = (i >> 6) % NK, m = mb * BR + (i >> 6) / NK * 16 + (l & 15);
+    if (ub <= ua) break;                            // the run ends in the item's cost
+    // the queries and the first stretch of the table, asked for together
+    __syncthreads();                                // the last item's ring, queries and statistics are done with
+    uint4 qv[(MT * NK + NW - 1) / NW];
+#pragma unroll
+    for (int k = 0; k < (MT * NK + NW - 1) / NW; ++k) {
+      const int f = wave + k * NW, j = f % NK, m = mb * BR + f / NK * 16 + r16;   // fragment f: rows, values
       const int nd = fdiv(min(m, p.rows - 1), p.dg), hd = m - nd * p.g;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (m < p.rows && nd < here) {
-        v = *reinterpret_cast<const uint4*>(p.q + ((int64_t)b * p.T + nd) * p.ldq + ((int64_t)h * p.g + hd) * D +
-                                            (j >> 1) * 64 + (l >> 4) * 16 + (j & 1) * 8);
-        v.x = (v.x & p.q_keep) ^ p.q_flip;
-        v.y = (v.y & p.q_keep) ^ p.q_flip;
-        v.z = (v.z & p.q_keep) ^ p.q_flip;
-        v.w = (v.w & p.q_keep) ^ p.q_flip;
-      }
-      queries[i] = v;
+      qv[k] = make_uint4(0, 0, 0, 0);
+      if (f < MT * NK && m < p.rows && nd < here)
+        qv[k] = *reinterpret_cast<const uint4*>(p.q + ((int64_t)b * p.T + nd) * p.ldq + ((int64_t)h * p.g + hd) * D +
+                                                (j >> 1) * 64 + q4 * 16 + (j & 1) * 8);
     }
+    bool absent = fill_table(p, b, h, ua * UNIT, len, table);
+#pragma unroll
+    for (int k = 0; k < (MT * NK + NW - 1) / NW; ++k) {
+      const int f = wave + k * NW;
+      if (f >= MT * NK) break;
+      queries[f * 64 + lane] = make_uint4((qv[k].x & p.q_keep) ^ p.q_flip, (qv[k].y & p.q_keep) ^ p.q_flip,
+                                          (qv[k].z & p.q_keep) ^ p.q_flip, (qv[k].w & p.q_keep) ^ p.q_flip);
+    }
+    __syncthreads();
+    absent = table_absent(absent, table);
     f32x4_t o[MT][ND];
     float mref[MT], l[MT];
 #pragma unroll
@@ -436,7 +454,12 @@ __global__ void __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) attention_kernel(At
 
     for (int uc = ua; uc < ub;) {                   // as many units as the table covers
       const int uz = min(ub, uc + STRETCH / UNIT), tbase = uc * UNIT;
-      const bool absent = fill_table(p, b, h, tbase, len, table);
+      if (uc != ua) {
+        __syncthreads();                            // the table is free
+        absent = fill_table(p, b, h, tbase, len, table);
+        __syncthreads();
+        absent = table_absent(absent, table);
+      }
       const int t0 = tbase + wave * TILE;           // this wave's first token; then every UNIT
       const int nt = t0 < len ? min(uz - uc, (len - t0 + UNIT - 1) / UNIT) : 0;
 
@@ -639,9 +662,9 @@ __global__ void __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) attention_kernel(At
         }
       }
     }
-    u += ub - ua;
-    while (u < u_end && u >= base + seq_units(p, b) * ipb) {
-      base += seq_units(p, b) * ipb;
+    u += vb - va;
+    while (u < u_end && u >= base + seq_span(p, b) * ipb) {
+      base += seq_span(p, b) * ipb;
       ++b;
     }
   }
@@ -679,8 +702,8 @@ __global__ void __launch_bounds__(256) attention_join_kernel(AttnParams p, int j
   const Batch batch(p, lane);
   const int ipb = p.hkv * p.mblocks;
   const Runs runs(batch.total * ipb, p.nwg);
-  const int u0 = batch.before(p, b) * ipb + (h * p.mblocks + mb) * units;
-  const int w0 = runs.owner(u0), w1 = runs.owner(u0 + units - 1), n = w1 - w0 + 1;
+  const int u0 = batch.before(p, b) * ipb + (h * p.mblocks + mb) * (units + p.start_cost);
+  const int w0 = runs.owner(u0 + p.start_cost), w1 = runs.owner(u0 + p.start_cost + units - 1), n = w1 - w0 + 1;
   if (n == 1) return;
   const int64_t head = (int64_t)w0 * 2 + (runs.start(w0) < u0 ? 1 : 0);
   auto slot_of = [&](int w) { return (w == w0 ? head : (int64_t)w * 2) * BR; };
@@ -812,9 +835,11 @@ __global__ void __launch_bounds__(64 * WW, 2) attention_wide_kernel(AttnParams p
   }
 
   while (u < u_end) {
-    const int len = seq_len(p, b), units = (len + W::TOKENS - 1) / W::TOKENS;
-    const int item = (u - base) / units;
-    const int ua = (u - base) - item * units, ub = min(units, ua + (u_end - u));
+    const int len = seq_len(p, b), units = (len + W::TOKENS - 1) / W::TOKENS, span = units + p.start_cost;
+    const int item = (u - base) / span;
+    const int va = (u - base) - item * span, vb = min(span, va + (u_end - u));
+    const int ua = max(va - p.start_cost, 0), ub = vb - p.start_cost;
+    if (ub <= ua) break;                            // the run ends in the item's cost
     const int h = item / p.mblocks, mb = item - h * p.mblocks;
     const int here = p.nodes ? max(0, min(p.nodes[b], p.T)) : p.T;
     const int prefix = len - here;
@@ -847,7 +872,10 @@ __global__ void __launch_bounds__(64 * WW, 2) attention_wide_kernel(AttnParams p
 
     for (int uc = ua; uc < ub;) {                   // as many tiles as the table covers
       const int uz = min(ub, uc + STRETCH / W::TOKENS), tbase = uc * W::TOKENS;
-      const bool absent = fill_table(p, b, h, tbase, len, table);   // (nothing is in flight here)
+      __syncthreads();                              // the table, ring and buffers are free; nothing is in flight
+      bool absent = fill_table(p, b, h, tbase, len, table);
+      __syncthreads();
+      absent = table_absent(absent, table);
       auto issue = [&](int i) {
         uint8_t* st = ring + (i % STAGES) * W::STAGE;
         const int* en = table + (i - uc) * W::GROUPS;
@@ -1067,16 +1095,16 @@ __global__ void __launch_bounds__(64 * WW, 2) attention_wide_kernel(AttnParams p
         if (q4 == 0) p.stat[slot * BR + row] = make_float2(mref[mt], l[mt]);
       }
     }
-    u += ub - ua;
-    while (u < u_end && u >= base + seq_units(p, b) * ipb) {
-      base += seq_units(p, b) * ipb;
+    u += vb - va;
+    while (u < u_end && u >= base + seq_span(p, b) * ipb) {
+      base += seq_span(p, b) * ipb;
       ++b;
     }
   }
 }
 
 struct AttnPlan {
-  int wide, mt, br, unit_shift, mblocks, nwg;
+  int wide, mt, br, unit_shift, start_cost, mblocks, nwg;
 };
 // Rows of a block and the grid: every unit its own workgroup up to one (wide) or two workgroups per CU.
 AttnPlan attention_plan(const AttentionArgs& a) {
@@ -1094,6 +1122,9 @@ AttnPlan attention_plan(const AttentionArgs& a) {
   const int64_t units = a.B * a.cache.heads * p.mblocks * ((a.max_len + (1 << p.unit_shift) - 1) >> p.unit_shift);
   const int64_t grid = p.wide ? 256 : 512;
   p.nwg = (int)(units < 1 ? 1 : units > grid ? grid : units);
+  // beginning an item costs about as long as half a kilobyte-wide unit's 128 tokens take (13 us against 2.9 us
+  // a unit at dim 128 and 48 rows); with few units a workgroup has no second item
+  p.start_cost = units > 4 * grid ? (int)(512 / a.cache.dim) : 0;
   return p;
 }
 
@@ -1165,6 +1196,7 @@ int launch_tree_attention(const AttentionArgs& a, hipStream_t stream) {
   p.br = pl.br;
   p.unit_shift = pl.unit_shift;
   p.unit = 1 << pl.unit_shift;
+  p.start_cost = pl.start_cost;
   p.dpage = make_fastdiv((uint32_t)a.cache.page);
   p.dg = make_fastdiv((uint32_t)p.g);
   const int D = (int)a.cache.dim, mt = pl.mt;
