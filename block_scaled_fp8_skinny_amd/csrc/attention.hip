@@ -4,8 +4,8 @@
 // are its (node, query head) pairs, g * T of them (g query heads share it). With s = q . k * scale in
 // base 2 (scale * log2 e), a running reference m per row, and weights w = 2^(s - m):
 //   l = sum w,  O = sum w V,  out = O / l,
-// one pass over the positions; m only moves (and O and l are rescaled) when a tile's maximum passes
-// it by more than MOVE, so that 2^MOVE bounds the weights.
+// one pass over the positions; m only moves (to the largest score so far; O and l are rescaled) when eight
+// weights of a lane sum to more than LIMIT, which bounds them.
 //
 // Products on bf16 MFMA (16x16x32), transposed so that nothing crosses lanes between them:
 //   S^T = K Q^T: a lane ends with four tokens of one row, which in pairs of 16-token groups are just
@@ -33,7 +33,7 @@ namespace {
 constexpr int NW = 4;                               // waves per workgroup
 constexpr int TILE = 32;                            // tokens of a wave's tile
 constexpr int UNIT = NW * TILE;
-constexpr float MOVE = 8.f;
+constexpr float LIMIT = 256.f;                       // of a lane's eight weights' sum
 constexpr float M_NONE = -1e30f;                    // reference of a row that has seen nothing
 
 struct AttnParams {
@@ -297,32 +297,40 @@ __device__ __forceinline__ void mask_scores(const AttnParams& p, int b, int m, i
     }
     sees[mt] = see;
   }
+  // The compiler would else wait, after the branch that this stands in, for the loads above to land, on
+  // the way without them too: and with them for the loads of the ring, which it does not know of.
+  __builtin_amdgcn_s_waitcnt(0x0F70);               // vmcnt(0)
 }
 
 // The weights 2^(s - m) of one row's eight scores (q . k, times scale2 for the base-2 score) as the B operand, and
-// their sum; true (for the wave) when the reference moved: then f is the factor of everything so far. The
-// weights are rounded to bf16 for the matrix product (at most half a step, 2^-8, each); the sum takes them
+// their sum; true (for the wave) when the reference moved: then f is the factor of everything so far. Whether it
+// has to move is seen from the weights' own sum, which is needed anyway: no maximum is taken while it does not.
+// The weights are rounded to bf16 for the matrix product (at most half a step, 2^-8, each); the sum takes them
 // unrounded.
 __device__ __forceinline__ bool weights(const f32x4_t& s0, const f32x4_t& s1, float scale2, float& mref, float& l,
                                         bf16x8_t& pf, float& f) {
-  float x[8];
+  float x[8], sum = 0.f;
+  auto run = [&] {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = e < 4 ? s0[e] : s1[e - 4];
-  float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7]))) * scale2;
-  const bool moved = __any(top > mref + MOVE);
-  if (moved) {
+    for (int e = 0; e < 8; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(e < 4 ? s0[e] : s1[e - 4], scale2, -mref));
+    sum = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+  };
+  run();
+  const bool moved = __any(sum > LIMIT);
+  if (__builtin_expect(moved, 0)) {
+    float top = s0[0];
+#pragma unroll
+    for (int e = 1; e < 8; ++e) top = fmaxf(top, e < 4 ? s0[e] : s1[e - 4]);
+    top *= scale2;
     top = fmaxf(top, __shfl_xor(top, 16));
     top = fmaxf(top, __shfl_xor(top, 32));
     const float m = fmaxf(mref, top);
     f = __builtin_amdgcn_exp2f(mref - m);
     mref = m;
     l *= f;
+    run();
   }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    x[e] = __builtin_amdgcn_exp2f(fmaf(x[e], scale2, -mref));
-    l += x[e];
-  }
+  l += sum;
   const u32x4_t w = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
   pf = __builtin_bit_cast(bf16x8_t, w);
   return moved;
@@ -902,41 +910,68 @@ __global__ void __launch_bounds__(64 * WW, 2) attention_wide_kernel(AttnParams p
           else wait_vmcnt_le<0>();
         }
       };
-      auto rebuild = [&](int i, uint4* buf) {
+      // Rebuilding tile i: a unit of K (two fragments of 16 tokens) and one of V (two fragments of 32 tokens) per
+      // wave; the codes and scales are read a phase before they are converted.
+      struct Raw {
+        uint4 k;
+        uint32_t v[8];
+        float kf, vf[8];
+      };
+      const int kgr = wave / NC, kj = wave % NC;                          // K's unit
+      const int vhalf = wave & 1, vset = (wave >> 1) / NC, vc = (wave >> 1) % NC;   // V's
+      auto read_raw = [&](int i, Raw& r) {
         const uint8_t* st = ring + (i % STAGES) * W::STAGE;
+        const uint8_t* sc = st + 2 * W::CODES;
         if (wave < W::KU) {
-          const int gr = wave / NC, j = wave % NC;
-          const uint4 w = *reinterpret_cast<const uint4*>(st + gr * 16 * D + r16 * D + (((4 * j + q4) ^ Geo<D>::swizzle(r16)) * 16));
-          const float f = block_scale(st[2 * W::CODES + gr * (D / 2) + r16 * (D / 32) + 2 * j + (q4 >> 1)]);
-          uint4* dst = buf + (gr * NK + 2 * j) * 64 + lane;
-          dst[0] = __builtin_bit_cast(uint4, dequant8(w.x, w.y, f));
-          dst[64] = __builtin_bit_cast(uint4, dequant8(w.z, w.w, f));
+          r.k = *reinterpret_cast<const uint4*>(st + kgr * 16 * D + r16 * D + (((4 * kj + q4) ^ Geo<D>::swizzle(r16)) * 16));
+          r.kf = block_scale(sc[kgr * (D / 2) + r16 * (D / 32) + 2 * kj + (q4 >> 1)]);
         }
         if (wave < W::VU) {
-          const int half = wave & 1, set = (wave >> 1) / NC, c = (wave >> 1) % NC;
-          const int t = i * W::TOKENS + set * 32;
-          uint32_t raw[8];
-          float f[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int gr = set * 2 + (e >> 2), j = e & 3;
-            raw[e] = *reinterpret_cast<const uint16_t*>(st + W::CODES + gr * 16 * D + (j * 4 + q4) * D + c * 64 + r16 * 4 + half * 2);
-            f[e] = block_scale(st[2 * W::CODES + W::SCALES + gr * (D / 2) + (q4 * 4 + j) * (D / 32) + 2 * c + (r16 >> 3)]);
+          for (int gr = 0; gr < 2; ++gr) {
+            const uint8_t* codes = st + W::CODES + (vset * 2 + gr) * 16 * D + q4 * D + vc * 64 + r16 * 4 + vhalf * 2;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r.v[gr * 4 + j] = *reinterpret_cast<const uint16_t*>(codes + j * 4 * D);
+            const uint8_t* g = sc + W::SCALES + (vset * 2 + gr) * (D / 2);
+            if constexpr (D == 128) {
+              const uint4 w = *reinterpret_cast<const uint4*>(g + q4 * 16);
+              const uint32_t t[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) r.vf[gr * 4 + j] = Scales<D>::rotated(t[j], 2 * vc + (r16 >> 3));
+            } else if constexpr (D == 64) {
+              const uint2 w = *reinterpret_cast<const uint2*>(g + q4 * 8);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) r.vf[gr * 4 + j] = Scales<D>::rotated(j < 2 ? w.x : w.y, 2 * (j & 1) + (r16 >> 3));
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                r.vf[gr * 4 + j] = Scales<D>::rotated(*reinterpret_cast<const uint16_t*>(g + (q4 * 4 + j) * (D / 32) + 2 * vc), r16 >> 3);
+            }
           }
+        }
+      };
+      auto rebuild = [&](int i, Raw& r, uint4* buf) {
+        if (wave < W::KU) {
+          uint4* dst = buf + (kgr * NK + 2 * kj) * 64 + lane;
+          dst[0] = __builtin_bit_cast(uint4, dequant8(r.k.x, r.k.y, r.kf));
+          dst[64] = __builtin_bit_cast(uint4, dequant8(r.k.z, r.k.w, r.kf));
+        }
+        if (wave < W::VU) {
+          const int t = i * W::TOKENS + vset * 32;
           if (t + 32 > len || absent) {             // tokens that are not there: zeros
             const int* pg = table + ((t - tbase) >> 4);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               if (t + (e >> 2) * 16 + q4 * 4 + (e & 3) >= len || pg[e >> 2] < 0) {
-                raw[e] = 0;
-                f[e] = 1.f;
+                r.v[e] = 0;
+                r.vf[e] = 1.f;
               }
           }
           u32x4_t a0, a1;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint32_t x = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw[2 * j], f[2 * j], false));
-            const uint32_t y = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(raw[2 * j + 1], f[2 * j + 1], false));
+            const uint32_t x = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r.v[2 * j], r.vf[2 * j], false));
+            const uint32_t y = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r.v[2 * j + 1], r.vf[2 * j + 1], false));
             a0[j] = __builtin_amdgcn_perm(y, x, 0x05040100u);
             a1[j] = __builtin_amdgcn_perm(y, x, 0x07060302u);
           }
@@ -950,9 +985,9 @@ __global__ void __launch_bounds__(64 * WW, 2) attention_wide_kernel(AttnParams p
               a1[j] &= ~y;
               any |= x | y;
             }
-            if (__any(any != 0) && lane == 0) spoiled[i % 3][set] = 1;
+            if (__any(any != 0) && lane == 0) spoiled[i % 3][vset] = 1;
           }
-          uint4* dst = buf + W::KF + (set * ND + 4 * c + 2 * half) * 64 + lane;
+          uint4* dst = buf + W::KF + (vset * ND + 4 * vc + 2 * vhalf) * 64 + lane;
           dst[0] = __builtin_bit_cast(uint4, a0);
           dst[64] = __builtin_bit_cast(uint4, a1);
         }
@@ -981,9 +1016,29 @@ __global__ void __launch_bounds__(64 * WW, 2) attention_wide_kernel(AttnParams p
           __builtin_amdgcn_sched_barrier(0);
         }
       };
-      // One tile; `kf` = the K fragments of its first set, asked for before. Fragments are asked for a phase ahead: V's
-      // before the softmax, the next set's K before the products with V.
-      auto compute = [&](int i, const uint4* buf, uint4 (&kf)[2 * NK]) {
+      // Tile i is loaded in iteration i - 3, rebuilt in iteration i - 1 and computed in iteration i. One barrier an
+      // iteration, before its last products with V: by then everyone has rebuilt its share of the next tile, has
+      // this tile's last fragments in registers (so its buffer is free), and its loads of the tile after the
+      // next have landed. Every read of LDS is asked for a phase ahead: V's fragments before the softmax, the next
+      // K's before the products with V, the codes to rebuild at the top.
+#pragma unroll 1
+      for (int i = uc; i < min(uc + 3, uz); ++i) issue(i);
+      if (threadIdx.x < 3 * W::SETS) spoiled[threadIdx.x / W::SETS][threadIdx.x % W::SETS] = 0;
+      landed(min(uz - uc, 3) - 1);
+      __syncthreads();
+      Raw raw;
+      read_raw(uc, raw);
+      rebuild(uc, raw, frags[uc & 1]);
+      landed(max(min(uz - uc, 3) - 2, 0));
+      __syncthreads();
+      uint4 kf[2 * NK];
+      ask_k(frags[uc & 1], 0, kf);
+#pragma unroll 1
+      for (int i = uc; i < uz; ++i) {
+        const uint4* buf = frags[i & 1];
+        if (threadIdx.x < W::SETS) spoiled[(i + 2) % 3][threadIdx.x] = 0;   // read an iteration ago, set in the next
+        if (i + 3 < uz) issue(i + 3);
+        if (i + 1 < uz) read_raw(i + 1, raw);
 #pragma unroll
         for (int set = 0; set < W::SETS; ++set) {
           const int t = i * W::TOKENS + set * 32;
@@ -1013,6 +1068,7 @@ __global__ void __launch_bounds__(64 * WW, 2) attention_wide_kernel(AttnParams p
             mask_scores<MT>(p, b, m0 + r16, here, prefix, len, t + q4 * 4, pg[0], pg[1], s, sees);
             if (__builtin_amdgcn_readfirstlane(spoiled[i % 3][set])) poison(i, set, sees);
           }
+          if (set == 0 && i + 1 < uz) rebuild(i + 1, raw, frags[(i + 1) & 1]);
           bf16x8_t pf[MT];
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
@@ -1022,7 +1078,13 @@ __global__ void __launch_bounds__(64 * WW, 2) attention_wide_kernel(AttnParams p
               for (int k = 0; k < ND; ++k) o[mt][k] *= f;
             }
           }
-          if (set + 1 < W::SETS) ask_k(buf, set + 1, kf);
+          if (set + 1 < W::SETS) {
+            ask_k(buf, set + 1, kf);
+          } else {
+            landed(i + 3 < uz ? 1 : 0);             // all but tile i + 3's: tile i + 2 is there
+            __syncthreads();
+            ask_k(frags[(i + 1) & 1], 0, kf);       // (after the last tile: not used)
+          }
           __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
           for (int k = 0; k < ND; ++k)
@@ -1030,31 +1092,6 @@ __global__ void __launch_bounds__(64 * WW, 2) attention_wide_kernel(AttnParams p
             for (int mt = 0; mt < MT; ++mt)
               o[mt][k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, fr[k]), pf[mt], o[mt][k], 0, 0, 0);
         }
-      };
-
-      // tile i is rebuilt from its stage during iteration i - 1 and computed in iteration i; its loads go out in
-      // iteration i - 3. The barrier that ends an iteration says that everyone's loads of the tile to be
-      // rebuilt next have landed, its buffer's readers are done, and the next tile is whole.
-#pragma unroll 1
-      for (int i = uc; i < min(uc + 3, uz); ++i) issue(i);
-      if (threadIdx.x < 3 * W::SETS) spoiled[threadIdx.x / W::SETS][threadIdx.x % W::SETS] = 0;
-      landed(min(uz - uc, 3) - 1);
-      __syncthreads();
-      rebuild(uc, frags[uc & 1]);
-      landed(max(min(uz - uc, 3) - 2, 0));
-      __syncthreads();
-#pragma unroll 1
-      for (int i = uc; i < uz; ++i) {
-        const uint4* buf = frags[i & 1];
-        uint4 kf[2 * NK];
-        ask_k(buf, 0, kf);
-        if (threadIdx.x < W::SETS) spoiled[(i + 2) % 3][threadIdx.x] = 0;   // read an iteration ago, set in the next
-        if (i + 3 < uz) issue(i + 3);
-        if (i + 1 < uz) rebuild(i + 1, frags[(i + 1) & 1]);
-        __builtin_amdgcn_sched_barrier(0);
-        compute(i, buf, kf);
-        landed(i + 3 < uz ? 1 : 0);                 // all but tile i + 3's: tile i + 2 is there
-        __syncthreads();
       }
       uc = uz;
     }
