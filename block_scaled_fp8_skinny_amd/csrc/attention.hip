@@ -44,6 +44,7 @@ struct AttnParams {
   uint16_t* out;
   float* part;                                      // [nwg][2][rows of a block][D]
   float2* stat;                                     // [nwg][2][rows of a block]: m, l
+  int2* owners;                                     // [items]: the workgroups of an item's first and last unit
   int64_t ldq, ld_pages, n_pages;
   float scale2;                                     // |scale| * log2 e (1 for a scale of 0)
   uint32_t q_keep, q_flip;                          // the scale's sign, or a scale of 0, on the queries
@@ -68,10 +69,6 @@ struct Runs {
   int per, rem;
   __device__ __forceinline__ Runs(int total, int nwg) : per(total / nwg), rem(total - (total / nwg) * nwg) {}
   __device__ __forceinline__ int start(int w) const { return w * per + min(w, rem); }
-  __device__ __forceinline__ int owner(int u) const {
-    const int wide = rem * (per + 1);
-    return u < wide ? u / (per + 1) : rem + (u - wide) / per;
-  }
 };
 
 // Units before each sequence, per head and row block, by a scan over the batch (whole wave; lane l
@@ -100,13 +97,6 @@ struct Batch {
       if (v < before + n) return b;
       before += n;
     }
-  }
-  // the units before sequence b
-  __device__ __forceinline__ int before(const AttnParams& p, int b) const {
-    const int l = b / c;
-    int v = __shfl(incl, l) - __shfl(own, l);
-    for (int i = l * c; i < b; ++i) v += seq_span(p, i);
-    return v;
   }
 };
 
@@ -641,6 +631,11 @@ __global__ void __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) attention_kernel(At
       add(join + SPAN);
       const bool whole = ua == 0 && ub == units;
       const int64_t slot = (int64_t)blockIdx.x * 2 + (u == first_u ? 0 : 1);
+      if (lane == 0) {
+        int2* own = p.owners + ((int64_t)b * p.hkv + h) * p.mblocks + mb;
+        if (ua == 0) own->x = (int)slot;
+        if (ub == units) own->y = blockIdx.x;
+      }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         const int row = mt * 16 + r16, m = mb * BR + row;
@@ -679,79 +674,75 @@ __global__ void __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) attention_kernel(At
 }
 
 // Join the partial results of the heads that several workgroups shared, and zero the rows that nobody
-// wrote (empty sequences). A workgroup takes `jr` rows of a head and row block, so that there are about
-// JOIN_BLOCKS of them: the search for the runs' owners comes before the first row. D/4 lanes hold
-// four values of a row each; the workgroup's 256 / (D/4) slices take rows side by side, or, when a
-// row's partial results are many, all take one row and every so-many-th result of it.
+// wrote (empty sequences). Who holds an item's partial results stands in `owners`. A workgroup takes `jr` rows of a
+// head and row block, so that there are about JOIN_BLOCKS of them. D/4 lanes hold four values of a row each; the
+// workgroup's 256 / (D/4) slices take rows side by side, or, when a row's partial results are many, all take one
+// row and every so-many-th result of it.
 constexpr int JOIN_BLOCKS = 1024;
 template <int D>
 __global__ void __launch_bounds__(256) attention_join_kernel(AttnParams p, int jr, int jblocks) {
   constexpr int LD = D / 4, SL = 256 / LD;
-  const int BR = p.br;
   __shared__ f32x4_t sums[SL][LD];
-  const int lane = threadIdx.x & 63;
-  const int part = blockIdx.x % (unsigned)jblocks;
-  int r = blockIdx.x / (unsigned)jblocks;
+  const int BR = p.br, lane = threadIdx.x & 63;
+  const int part = blockIdx.x % (unsigned)jblocks, item = blockIdx.x / (unsigned)jblocks;
+  int r = item;
   const int mb = r % p.mblocks;
   r /= p.mblocks;
   const int h = r % p.hkv, b = r / p.hkv;
-  const int units = seq_units(p, b);
+  const int2 own = p.owners[item];                  // (of an empty sequence: whatever, not used)
+  const int len = seq_len(p, b), here = p.nodes ? p.nodes[b] : p.T;
   const int row0 = part * jr, row1 = min(min(row0 + jr, BR), p.rows - mb * BR);
-  const int here = p.nodes ? p.nodes[b] : p.T;
   const int c = threadIdx.x % LD, sl = threadIdx.x / LD;
   auto out_at = [&](int row) {
     const int m = mb * BR + row, node = fdiv(m, p.dg);
     return p.out + (((int64_t)b * p.T + node) * p.hq + (int64_t)h * p.g + (m - node * p.g)) * D + c * 4;
   };
-  if (units == 0) {
+  if (len == 0) {
     for (int row = row0 + sl; sl < SL && row < row1; row += SL) *reinterpret_cast<uint2*>(out_at(row)) = make_uint2(0, 0);
     return;
   }
-  const Batch batch(p, lane);
-  const int ipb = p.hkv * p.mblocks;
-  const Runs runs(batch.total * ipb, p.nwg);
-  const int u0 = batch.before(p, b) * ipb + (h * p.mblocks + mb) * (units + p.start_cost);
-  const int w0 = runs.owner(u0 + p.start_cost), w1 = runs.owner(u0 + p.start_cost + units - 1), n = w1 - w0 + 1;
+  const int w0 = own.x >> 1, w1 = own.y, n = w1 - w0 + 1;
   if (n == 1) return;
-  const int64_t head = (int64_t)w0 * 2 + (runs.start(w0) < u0 ? 1 : 0);
-  auto slot_of = [&](int w) { return (w == w0 ? head : (int64_t)w * 2) * BR; };
+  // the first workgroup's result stands in its slot own.x & 1, the others' in their first
+  auto slot_of = [&](int w) { return (int64_t)(w == w0 ? own.x : w * 2) * BR; };
   auto store = [&](int row, const f32x4_t& acc, float l) {
     const float f = 1.f / l;
     const bool live = l != 0.f && fdiv(mb * BR + row, p.dg) < here;
     *reinterpret_cast<uint2*>(out_at(row)) =
         live ? make_uint2(pack_bf16x2(acc[0] * f, acc[1] * f), pack_bf16x2(acc[2] * f, acc[3] * f)) : make_uint2(0, 0);
   };
-  // sum of the results w0 + first, + step, ... of one row, relative to its largest reference
-  auto gather = [&](int row, int first, int step, float& top, float& l) {
-    top = M_NONE;
-    for (int w = w0; w <= w1; ++w) top = fmaxf(top, p.stat[slot_of(w) + row].x);
-    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-    l = 0.f;
-#pragma unroll 4
-    for (int w = w0 + first; w <= w1; w += step) {
-      const int64_t at = slot_of(w) + row;
-      const float2 s = p.stat[at];
-      const float f = __builtin_amdgcn_exp2f(s.x - top);
-      l += s.y * f;
-      acc += *reinterpret_cast<const f32x4_t*>(p.part + at * D + c * 4) * f;
-    }
-    return acc;
-  };
-  float top, l;
-  if (n <= SL && row1 - row0 > 1) {
+  if (n <= 8) {                                     // all results of a row at once, one row per slice
     for (int row = row0 + sl; sl < SL && row < row1; row += SL) {
-      const f32x4_t acc = gather(row, 0, 1, top, l);
+      float2 st[8];
+      f32x4_t v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (k % 4 == 0 && k >= n) break;
+        const int64_t at = slot_of(min(w0 + k, w1)) + row;
+        st[k] = p.stat[at];
+        v[k] = *reinterpret_cast<const f32x4_t*>(p.part + at * D + c * 4);
+      }
+      float top = fmaxf(fmaxf(st[0].x, st[1].x), fmaxf(st[2].x, st[3].x));
+      if (n > 4) top = fmaxf(top, fmaxf(fmaxf(st[4].x, st[5].x), fmaxf(st[6].x, st[7].x)));
+      f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+      float l = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (k >= n) break;
+        const float f = __builtin_amdgcn_exp2f(st[k].x - top);
+        l += st[k].y * f;
+        acc += v[k] * f;
+      }
       store(row, acc, l);
     }
     return;
   }
   for (int row = row0; row < row1; ++row) {
     // references and sums by the lanes of every wave, the values by the slices
-    top = M_NONE;
+    float top = M_NONE, l = 0.f;
     for (int w = w0 + lane; w <= w1; w += 64) top = fmaxf(top, p.stat[slot_of(w) + row].x);
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) top = fmaxf(top, __shfl_xor(top, o));
-    l = 0.f;
     for (int w = w0 + lane; w <= w1; w += 64) {
       const float2 s = p.stat[slot_of(w) + row];
       l += s.y * __builtin_amdgcn_exp2f(s.x - top);
@@ -796,7 +787,7 @@ struct Wide {
   static constexpr int SCALES = CODES / 32;
   static constexpr int STAGE = 2 * CODES + 2 * SCALES, STAGES = 4;    // K, V, K's scales, V's scales
   static constexpr int CL = 2 * GROUPS * (D / 64), LOADS = CL + 2 * GROUPS;   // loads of a tile: 1 KB of codes; a group's scales
-  static_assert(KU <= WW && VU <= WW, "one unit of each per wave");
+  static constexpr int KW = (KU + WW - 1) / WW, VW = (VU + WW - 1) / WW;   // units per wave
   static_assert(CODES * 4 + STAGES * STAGE + TABLE * 4 <= 160 * 1024 && 2 * (KF + VF) * 16 == CODES * 8, "LDS");
 };
 
@@ -913,65 +904,76 @@ __global__ void __launch_bounds__(64 * WW, 2) attention_wide_kernel(AttnParams p
       // Rebuilding tile i: a unit of K (two fragments of 16 tokens) and one of V (two fragments of 32 tokens) per
       // wave; the codes and scales are read a phase before they are converted.
       struct Raw {
-        uint4 k;
-        uint32_t v[8];
-        float kf, vf[8];
+        uint4 k[W::KW];
+        uint32_t v[W::VW][8];
+        float kf[W::KW], vf[W::VW][8];
       };
-      const int kgr = wave / NC, kj = wave % NC;                          // K's unit
-      const int vhalf = wave & 1, vset = (wave >> 1) / NC, vc = (wave >> 1) % NC;   // V's
       auto read_raw = [&](int i, Raw& r) {
         const uint8_t* st = ring + (i % STAGES) * W::STAGE;
         const uint8_t* sc = st + 2 * W::CODES;
-        if (wave < W::KU) {
-          r.k = *reinterpret_cast<const uint4*>(st + kgr * 16 * D + r16 * D + (((4 * kj + q4) ^ Geo<D>::swizzle(r16)) * 16));
-          r.kf = block_scale(sc[kgr * (D / 2) + r16 * (D / 32) + 2 * kj + (q4 >> 1)]);
+#pragma unroll
+        for (int n = 0; n < W::KW; ++n) {
+          const int unit = wave + n * WW, gr = unit / NC, j = unit % NC;
+          if (W::KU % WW && unit >= W::KU) break;
+          r.k[n] = *reinterpret_cast<const uint4*>(st + gr * 16 * D + r16 * D + (((4 * j + q4) ^ Geo<D>::swizzle(r16)) * 16));
+          r.kf[n] = block_scale(sc[gr * (D / 2) + r16 * (D / 32) + 2 * j + (q4 >> 1)]);
         }
-        if (wave < W::VU) {
+#pragma unroll
+        for (int n = 0; n < W::VW; ++n) {
+          const int unit = wave + n * WW, half = unit & 1, set = (unit >> 1) / NC, c = (unit >> 1) % NC;
+          if (W::VU % WW && unit >= W::VU) break;
 #pragma unroll
           for (int gr = 0; gr < 2; ++gr) {
-            const uint8_t* codes = st + W::CODES + (vset * 2 + gr) * 16 * D + q4 * D + vc * 64 + r16 * 4 + vhalf * 2;
+            const uint8_t* codes = st + W::CODES + (set * 2 + gr) * 16 * D + q4 * D + c * 64 + r16 * 4 + half * 2;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) r.v[gr * 4 + j] = *reinterpret_cast<const uint16_t*>(codes + j * 4 * D);
-            const uint8_t* g = sc + W::SCALES + (vset * 2 + gr) * (D / 2);
+            for (int j = 0; j < 4; ++j) r.v[n][gr * 4 + j] = *reinterpret_cast<const uint16_t*>(codes + j * 4 * D);
+            const uint8_t* g = sc + W::SCALES + (set * 2 + gr) * (D / 2);
+            float* f = r.vf[n] + gr * 4;
             if constexpr (D == 128) {
               const uint4 w = *reinterpret_cast<const uint4*>(g + q4 * 16);
               const uint32_t t[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-              for (int j = 0; j < 4; ++j) r.vf[gr * 4 + j] = Scales<D>::rotated(t[j], 2 * vc + (r16 >> 3));
+              for (int j = 0; j < 4; ++j) f[j] = Scales<D>::rotated(t[j], 2 * c + (r16 >> 3));
             } else if constexpr (D == 64) {
               const uint2 w = *reinterpret_cast<const uint2*>(g + q4 * 8);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) r.vf[gr * 4 + j] = Scales<D>::rotated(j < 2 ? w.x : w.y, 2 * (j & 1) + (r16 >> 3));
+              for (int j = 0; j < 4; ++j) f[j] = Scales<D>::rotated(j < 2 ? w.x : w.y, 2 * (j & 1) + (r16 >> 3));
             } else {
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                r.vf[gr * 4 + j] = Scales<D>::rotated(*reinterpret_cast<const uint16_t*>(g + (q4 * 4 + j) * (D / 32) + 2 * vc), r16 >> 3);
+                f[j] = Scales<D>::rotated(*reinterpret_cast<const uint16_t*>(g + (q4 * 4 + j) * (D / 32) + 2 * c), r16 >> 3);
             }
           }
         }
       };
       auto rebuild = [&](int i, Raw& r, uint4* buf) {
-        if (wave < W::KU) {
-          uint4* dst = buf + (kgr * NK + 2 * kj) * 64 + lane;
-          dst[0] = __builtin_bit_cast(uint4, dequant8(r.k.x, r.k.y, r.kf));
-          dst[64] = __builtin_bit_cast(uint4, dequant8(r.k.z, r.k.w, r.kf));
+#pragma unroll
+        for (int n = 0; n < W::KW; ++n) {
+          const int unit = wave + n * WW, gr = unit / NC, j = unit % NC;
+          if (W::KU % WW && unit >= W::KU) break;
+          uint4* dst = buf + (gr * NK + 2 * j) * 64 + lane;
+          dst[0] = __builtin_bit_cast(uint4, dequant8(r.k[n].x, r.k[n].y, r.kf[n]));
+          dst[64] = __builtin_bit_cast(uint4, dequant8(r.k[n].z, r.k[n].w, r.kf[n]));
         }
-        if (wave < W::VU) {
-          const int t = i * W::TOKENS + vset * 32;
+#pragma unroll
+        for (int n = 0; n < W::VW; ++n) {
+          const int unit = wave + n * WW, half = unit & 1, set = (unit >> 1) / NC, c = (unit >> 1) % NC;
+          if (W::VU % WW && unit >= W::VU) break;
+          const int t = i * W::TOKENS + set * 32;
           if (t + 32 > len || absent) {             // tokens that are not there: zeros
             const int* pg = table + ((t - tbase) >> 4);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               if (t + (e >> 2) * 16 + q4 * 4 + (e & 3) >= len || pg[e >> 2] < 0) {
-                r.v[e] = 0;
-                r.vf[e] = 1.f;
+                r.v[n][e] = 0;
+                r.vf[n][e] = 1.f;
               }
           }
           u32x4_t a0, a1;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint32_t x = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r.v[2 * j], r.vf[2 * j], false));
-            const uint32_t y = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r.v[2 * j + 1], r.vf[2 * j + 1], false));
+            const uint32_t x = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r.v[n][2 * j], r.vf[n][2 * j], false));
+            const uint32_t y = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r.v[n][2 * j + 1], r.vf[n][2 * j + 1], false));
             a0[j] = __builtin_amdgcn_perm(y, x, 0x05040100u);
             a1[j] = __builtin_amdgcn_perm(y, x, 0x07060302u);
           }
@@ -985,9 +987,9 @@ __global__ void __launch_bounds__(64 * WW, 2) attention_wide_kernel(AttnParams p
               a1[j] &= ~y;
               any |= x | y;
             }
-            if (__any(any != 0) && lane == 0) spoiled[i % 3][vset] = 1;
+            if (__any(any != 0) && lane == 0) spoiled[i % 3][set] = 1;
           }
-          uint4* dst = buf + W::KF + (vset * ND + 4 * vc + 2 * vhalf) * 64 + lane;
+          uint4* dst = buf + W::KF + (set * ND + 4 * c + 2 * half) * 64 + lane;
           dst[0] = __builtin_bit_cast(uint4, a0);
           dst[64] = __builtin_bit_cast(uint4, a1);
         }
@@ -1098,6 +1100,11 @@ __global__ void __launch_bounds__(64 * WW, 2) attention_wide_kernel(AttnParams p
 
     const bool whole = ua == 0 && ub == units;
     const int64_t slot = (int64_t)blockIdx.x * 2 + (u == first_u ? 0 : 1);
+    if (threadIdx.x == 0) {
+      int2* own = p.owners + ((int64_t)b * p.hkv + h) * p.mblocks + mb;
+      if (ua == 0) own->x = (int)slot;
+      if (ub == units) own->y = blockIdx.x;
+    }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       l[mt] += __shfl_xor(l[mt], 16);
@@ -1194,7 +1201,8 @@ inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 size_t attention_ws_bytes(const AttentionArgs& a) {
   const AttnPlan pl = attention_plan(a);
   const size_t rows = (size_t)pl.nwg * 2 * pl.br;
-  return align256(rows * sizeof(float2)) + rows * (size_t)a.cache.dim * 4;
+  return align256((size_t)a.B * a.cache.heads * pl.mblocks * sizeof(int2)) + align256(rows * sizeof(float2)) +
+         rows * (size_t)a.cache.dim * 4;
 }
 
 int launch_tree_attention(const AttentionArgs& a, hipStream_t stream) {
@@ -1210,9 +1218,11 @@ int launch_tree_attention(const AttentionArgs& a, hipStream_t stream) {
   p.nodes = a.nodes;
   p.mask = a.mask;
   p.out = a.out;
-  p.stat = reinterpret_cast<float2*>(a.ws);
-  p.part = reinterpret_cast<float*>(reinterpret_cast<char*>(a.ws) +
-                                    align256((size_t)pl.nwg * 2 * pl.br * sizeof(float2)));
+  char* ws = reinterpret_cast<char*>(a.ws);
+  p.owners = reinterpret_cast<int2*>(ws);
+  ws += align256((size_t)a.B * a.cache.heads * pl.mblocks * sizeof(int2));
+  p.stat = reinterpret_cast<float2*>(ws);
+  p.part = reinterpret_cast<float*>(ws + align256((size_t)pl.nwg * 2 * pl.br * sizeof(float2)));
   p.ldq = a.ldq;
   p.ld_pages = a.ld_pages;
   p.n_pages = a.cache.pages;
