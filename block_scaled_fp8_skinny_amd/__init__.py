@@ -105,7 +105,9 @@ def _check(status, where):
 
 
 def _stream(t):
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+    """torch's current stream of the tensor's device, by its handle: building torch's Stream object around it
+    costs 2 us a call, as much as a kernel launch."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _ptr(t):
@@ -677,7 +679,10 @@ def _cache(cache):
 
 
 def _vec(t, dtype, name, shape, device):
-    """_need, and the exact shape."""
+    """_need, and the exact shape. The pointer. (One test of everything first: these calls take up to ten tensors
+    each and may be as short as 3 us on the GPU.)"""
+    if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
     _need(t, dtype, name, device=device)
     if tuple(t.shape) != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
@@ -685,21 +690,26 @@ def _vec(t, dtype, name, shape, device):
 
 
 def _heads_view(x, name, R, heads, dim, device):
-    """bf16 rows of heads, [R, heads, dim] or [R, heads * dim] with any row stride -> (pointer, row stride)."""
-    if not isinstance(x, torch.Tensor) or x.dtype != torch.bfloat16:
+    """bf16 rows of heads, [R, heads, dim] or [R, heads * dim] with any row stride (heads None: as many as x has)
+    -> (pointer, row stride, heads)."""
+    if not isinstance(x, torch.Tensor) or x.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be a bf16 tensor")
     if x.device != device:
         raise ValueError(f"{name} is on {x.device}, expected {device}")
     shape, stride = x.shape, x.stride()
-    if len(shape) == 3 and heads is None:
-        heads = shape[1]
-    elif heads is None:
-        heads = shape[1] // dim if len(shape) == 2 else -1
-    ok = (len(shape) == 3 and shape[1] == heads and shape[2] == dim and stride[2] == 1 and (heads <= 1 or stride[1] == dim)
-          or len(shape) == 2 and shape[1] == heads * dim and stride[1] == 1)
-    if not ok or shape[0] != R:
-        raise ValueError(f"{name} must be [{R}, heads, {dim}] with strides (any, {dim}, 1), got {list(shape)}, {list(stride)}")
-    return x.data_ptr(), stride[0] if R > 1 else max(heads, 1) * dim, heads
+    if len(shape) == 3:
+        rows, n, d = shape
+        ok = d == dim and stride[2] == 1 and (n <= 1 or stride[1] == dim)
+    elif len(shape) == 2:
+        rows, w = shape
+        n = w // dim
+        ok = n * dim == w and stride[1] == 1
+    else:
+        ok = False
+    if not ok or rows != R or (heads is not None and n != heads):
+        raise ValueError(f"{name} must be [{R}, {'heads' if heads is None else heads}, {dim}] with strides (any, {dim}, 1), "
+                         f"got {list(shape)}, {list(stride)}")
+    return x.data_ptr(), stride[0] if R > 1 else max(n, 1) * dim, n
 
 
 def bsfp8_cache_write(cache, slots, k, v, q=None, q_out=None, q_weight=None, k_weight=None, eps=1e-6, cos_sin=None,
@@ -720,21 +730,20 @@ def bsfp8_cache_write(cache, slots, k, v, q=None, q_out=None, q_weight=None, k_w
         pq, ldq, hq = _heads_view(q, "q", R, None, D, dev)
         if q_out is None:
             q_out = torch.empty((R, hq, D), dtype=torch.bfloat16, device=dev)
-        _need(q_out, torch.bfloat16, "q_out", device=dev)
         if q_out.numel() != R * hq * D:
             raise ValueError(f"q_out holds {q_out.numel()} values, expected {R * hq * D}")
-        pqo = q_out.data_ptr()
+        pqo = _vec(q_out, torch.bfloat16, "q_out", q_out.shape, dev)
     elif q_out is not None or q_weight is not None:
         raise ValueError("q_out and q_weight need q")
     pqw = _vec(q_weight, torch.bfloat16, "q_weight", (D,), dev) if q_weight is not None else 0
     pkw = _vec(k_weight, torch.bfloat16, "k_weight", (D,), dev) if k_weight is not None else 0
     pcs = pp = n_pos = rot = 0
     if cos_sin is not None:
-        _need(cos_sin, torch.float32, "cos_sin", device=dev)
-        if cos_sin.dim() != 2:
+        shape = cos_sin.shape
+        if len(shape) != 2:
             raise ValueError("cos_sin must be [n_positions, rot]")
-        n_pos, rot = cos_sin.shape
-        pcs, pp = cos_sin.data_ptr(), _vec(positions, torch.int64, "positions", (R,), dev)
+        n_pos, rot = shape
+        pcs, pp = _vec(cos_sin, torch.float32, "cos_sin", shape, dev), _vec(positions, torch.int64, "positions", (R,), dev)
     st = lib().bsfp8_cache_write(c._ref, ps, R, pk, ldk, pv, ldv, pq, ldq, hq, pqo, pqw, pkw, eps, pcs, n_pos, rot, pp,
                                  1 if interleaved else 0, _stream(k))
     _check(st, "bsfp8_cache_write")
@@ -777,13 +786,14 @@ def bsfp8_tree_attention(q, cache, pages, lens, nodes=None, mask=None, scale=Non
     wider projection: heads and values contiguous, one stride between tokens."""
     c = _cache(cache)
     dev = c.device
-    if not isinstance(q, torch.Tensor) or q.dtype != torch.bfloat16:
+    if not isinstance(q, torch.Tensor) or q.dtype is not torch.bfloat16:
         raise TypeError("q must be a bf16 tensor")
     if q.device != dev:
         raise ValueError(f"q is on {q.device}, expected {dev}")
-    if q.dim() != 4 or q.shape[3] != c.dim:
-        raise ValueError(f"q must be [B, T, hq, {c.dim}], got {list(q.shape)}")
-    B, T, hq, D = q.shape
+    shape = q.shape
+    if len(shape) != 4 or shape[3] != c.dim:
+        raise ValueError(f"q must be [B, T, hq, {c.dim}], got {list(shape)}")
+    B, T, hq, D = shape
     if q.is_contiguous():
         ldq = hq * D
     else:
@@ -801,12 +811,12 @@ def bsfp8_tree_attention(q, cache, pages, lens, nodes=None, mask=None, scale=Non
     max_len = W * c.page if max_len is None else max_len
     if ws is None:
         ws = workspace_attention(B, T, hq, c.heads, D, max_len, device=dev)
-    _need(ws, torch.uint8, "ws", device=dev)
+    pw = _vec(ws, torch.uint8, "ws", ws.shape, dev)
     if out is None:
-        out = torch.empty((B, T, hq, D), dtype=torch.bfloat16, device=dev)
-    po = _vec(out, torch.bfloat16, "out", (B, T, hq, D), dev)
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    po = _vec(out, torch.bfloat16, "out", shape, dev)
     st = lib().bsfp8_tree_attention(q.data_ptr(), ldq, B, T, hq, c._ref, pp, W, pl, pn, pm,
-                                    D ** -0.5 if scale is None else scale, max_len, ws.data_ptr(), ws.numel(), po,
+                                    D ** -0.5 if scale is None else scale, max_len, pw, ws.numel(), po,
                                     _stream(q))
     _check(st, "bsfp8_tree_attention")
     return out
@@ -824,32 +834,31 @@ def workspace_verify(B, T, V, device="cuda"):
 def _verify_args(logits, ws, out_tokens, n_accepted):
     if not isinstance(logits, torch.Tensor) or logits.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("logits must be fp32 or bf16")
-    _need(logits, logits.dtype, "logits")
-    if logits.dim() != 3:
+    shape, dtype, dev = logits.shape, logits.dtype, logits.device
+    if len(shape) != 3:
         raise ValueError("logits must be [B, T, V]")
-    B, T, V = logits.shape
-    dev = logits.device
+    B, T, V = shape
+    if not logits.is_cuda:
+        raise ValueError("logits must be a GPU tensor")
     ws = workspace_verify(B, T, V, device=dev) if ws is None else ws
-    _need(ws, torch.uint8, "ws", device=dev)
     out_tokens = torch.empty((B, T), dtype=torch.int32, device=dev) if out_tokens is None else out_tokens
     n_accepted = torch.empty((B,), dtype=torch.int32, device=dev) if n_accepted is None else n_accepted
-    _vec(out_tokens, torch.int32, "out_tokens", (B, T), dev)
-    _vec(n_accepted, torch.int32, "n_accepted", (B,), dev)
-    return B, T, V, dev, 1 if logits.dtype == torch.float32 else 0, ws, out_tokens, n_accepted
+    at = (_vec(logits, dtype, "logits", shape, dev), _vec(ws, torch.uint8, "ws", ws.shape, dev),
+          _vec(out_tokens, torch.int32, "out_tokens", (B, T), dev), _vec(n_accepted, torch.int32, "n_accepted", (B,), dev))
+    return B, T, V, dev, 1 if dtype is torch.float32 else 0, ws, at, out_tokens, n_accepted
 
 
 def bsfp8_verify_chain(logits, draft, tokens, temperature, u, u_sample, ws=None, out_tokens=None, n_accepted=None):
     """Verify a chain of T - 1 drafted tokens a sequence: logits [B, T, V] of the target and draft [B, T-1, V] of the
     drafter (fp32 or bf16, alike), tokens int32 [B, T-1], temperature fp32 [B] (0: greedy), u fp32 [B, T-1] and u_sample
     fp32 [B] uniform in [0, 1). -> (out_tokens int32 [B, T]: accepted tokens, the next one, -1s; n_accepted int32 [B])."""
-    B, T, V, dev, dt, ws, out_tokens, n_accepted = _verify_args(logits, ws, out_tokens, n_accepted)
+    B, T, V, dev, dt, ws, (pl, pw, po, pn), out_tokens, n_accepted = _verify_args(logits, ws, out_tokens, n_accepted)
     pd = _vec(draft, logits.dtype, "draft", (B, T - 1, V), dev)
     pt = _vec(tokens, torch.int32, "tokens", (B, T - 1), dev)
     pe = _vec(temperature, torch.float32, "temperature", (B,), dev)
     pu = _vec(u, torch.float32, "u", (B, T - 1), dev)
     ps = _vec(u_sample, torch.float32, "u_sample", (B,), dev)
-    st = lib().bsfp8_verify_chain(logits.data_ptr(), pd, dt, B, T, V, pt, pe, pu, ps, ws.data_ptr(), ws.numel(),
-                                  out_tokens.data_ptr(), n_accepted.data_ptr(), _stream(logits))
+    st = lib().bsfp8_verify_chain(pl, pd, dt, B, T, V, pt, pe, pu, ps, pw, ws.numel(), po, pn, _stream(logits))
     _check(st, "bsfp8_verify_chain")
     return out_tokens, n_accepted
 
@@ -859,14 +868,13 @@ def bsfp8_verify_tree(logits, tokens, parents, temperature, u, ws=None, out_toke
     (node 0 the root), temperature fp32 [B] (0: greedy), u fp32 [B, T] uniform in [0, 1).
     -> (out_tokens int32 [B, T]: accepted tokens, the next one, -1s; path int32 [B, T]: the path's nodes, -1s;
     n_accepted int32 [B])."""
-    B, T, V, dev, dt, ws, out_tokens, n_accepted = _verify_args(logits, ws, out_tokens, n_accepted)
+    B, T, V, dev, dt, ws, (pl, pw, po, pn), out_tokens, n_accepted = _verify_args(logits, ws, out_tokens, n_accepted)
     path = torch.empty((B, T), dtype=torch.int32, device=dev) if path is None else path
     pp = _vec(path, torch.int32, "path", (B, T), dev)
     pt = _vec(tokens, torch.int32, "tokens", (B, T), dev)
     pr = _vec(parents, torch.int32, "parents", (B, T), dev)
     pe = _vec(temperature, torch.float32, "temperature", (B,), dev)
     pu = _vec(u, torch.float32, "u", (B, T), dev)
-    st = lib().bsfp8_verify_tree(logits.data_ptr(), dt, B, T, V, pt, pr, pe, pu, ws.data_ptr(), ws.numel(),
-                                 out_tokens.data_ptr(), pp, n_accepted.data_ptr(), _stream(logits))
+    st = lib().bsfp8_verify_tree(pl, dt, B, T, V, pt, pr, pe, pu, pw, ws.numel(), po, pp, pn, _stream(logits))
     _check(st, "bsfp8_verify_tree")
     return out_tokens, path, n_accepted

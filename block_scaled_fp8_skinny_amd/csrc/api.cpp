@@ -168,6 +168,9 @@ int run_gemm_mxfp8(const GemmShape& s, const GemmPlan& p, const uint16_t* x, con
                                    gemm_partials_order(p), yq, ys, stream);
 }
 
+// Workgroups of 256 threads along one axis of a grid: its threads are counted in 32 bits.
+constexpr int64_t MAX_BLOCKS = (int64_t)1 << 24;
+
 // Sizes of the cache (BSFP8_ESHAPE), its pointers and their alignment.
 int check_cache(const bsfp8_kv_cache* c) {
   if (!c) return BSFP8_EINVAL;
@@ -191,12 +194,12 @@ int check_attention_sizes(int64_t B, int64_t T, int64_t hq, int64_t hkv, int64_t
   // units of at least 32 positions (and the cost of a start) of a head and a block of at least 16 rows are
   // counted in 32 bits
   const int64_t blocks = (T * (hq / hkv) + 15) / 16, units = max_len / 32 + 10;
-  if (B > 0 && (hkv * blocks >= lim || B * hkv * blocks >= lim / units)) return BSFP8_ESHAPE;
+  if (B > 0 && (hkv * blocks >= lim || B * hkv * blocks >= lim / units || B * hkv * blocks >= MAX_BLOCKS)) return BSFP8_ESHAPE;
   return BSFP8_OK;
 }
 
 int check_verify_sizes(int64_t B, int64_t T, int64_t V) {
-  if (B < 0 || B > (1 << 24) || T < 1 || T > 64 || V < 1 || V > (1 << 24)) return BSFP8_ESHAPE;
+  if (T < 1 || T > 64 || V < 1 || V > (1 << 24) || B < 0 || B * (2 * T - 1) >= MAX_BLOCKS) return BSFP8_ESHAPE;
   return BSFP8_OK;
 }
 // What the two verification calls have in common.
@@ -623,7 +626,7 @@ int bsfp8_cache_write(const bsfp8_kv_cache* cache, const int64_t* slots, int64_t
   int st = check_cache(cache);
   if (st != BSFP8_OK) return st;
   const int64_t D = cache->dim, kv = cache->heads * D;
-  if (R < 0 || R >= ((int64_t)1 << 31) || hq < 0 || hq > (1 << 20) || rot < 0 || rot > D || rot % 16) return BSFP8_ESHAPE;
+  if (R < 0 || R >= MAX_BLOCKS || hq < 0 || hq > (1 << 20) || rot < 0 || rot > D || rot % 16) return BSFP8_ESHAPE;
   if (n_positions < 0) return BSFP8_ESHAPE;
   if (!(eps >= 0.f) || eps > 3.4e38f || (interleaved != 0 && interleaved != 1)) return BSFP8_EINVAL;
   if (R == 0) return BSFP8_OK;
@@ -651,6 +654,7 @@ int bsfp8_cache_read(const bsfp8_kv_cache* cache, const int64_t* slots, int64_t 
   const int st = check_cache(cache);
   if (st != BSFP8_OK) return st;
   if (R < 0 || R >= ((int64_t)1 << 31) || R * cache->heads >= ((int64_t)1 << 31)) return BSFP8_ESHAPE;
+  if (R * cache->heads * (cache->dim / 16) >= MAX_BLOCKS * 256) return BSFP8_ESHAPE;
   if (R == 0) return BSFP8_OK;
   if (!slots || !k_out || !v_out) return BSFP8_EINVAL;
   if (!aligned16(k_out) || !aligned16(v_out)) return BSFP8_ESTRIDE;

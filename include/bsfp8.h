@@ -361,7 +361,7 @@ typedef struct bsfp8_kv_cache {
  *   rot       : 0 or a multiple of 16 up to dim (cos_sin and positions are not read when 0).
  *   positions : int64_t [R] (device). A position outside [0, n_positions) gives NaN in the rotated
  *               values (and so a NaN block, scale byte 255, in the cache).
- * q_out must not overlap an input or the cache, and the cache no input (BSFP8_EINVAL). */
+ * R < 2^24. q_out must not overlap an input or the cache, and the cache no input (BSFP8_EINVAL). */
 BSFP8_API int bsfp8_cache_write(const bsfp8_kv_cache* cache, const int64_t* slots, int64_t R,
                                 const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv,
                                 const uint16_t* q, int64_t ldq, int64_t hq, uint16_t* q_out,
@@ -371,7 +371,8 @@ BSFP8_API int bsfp8_cache_write(const bsfp8_kv_cache* cache, const int64_t* slot
 
 /* Rows of the cache as bf16: k_out, v_out [R][heads][dim] (contiguous, 16-byte aligned), each value
  * e4m3(code) * 2^(byte-127) rounded once to bf16 (exact unless it falls below the bf16 normals;
- * scale byte 255 and NaN codes give NaN). A slot outside the cache gives zeros. */
+ * scale byte 255 and NaN codes give NaN). A slot outside the cache gives zeros. R * heads < 2^31 and
+ * R * heads * dim < 2^36. */
 BSFP8_API int bsfp8_cache_read(const bsfp8_kv_cache* cache, const int64_t* slots, int64_t R,
                                uint16_t* k_out, uint16_t* v_out, void* stream);
 
@@ -397,7 +398,8 @@ BSFP8_API size_t bsfp8_attention_workspace_bytes(int64_t B, int64_t T, int64_t h
  *   out   : bf16 [B][T][hq][dim] (contiguous, 16-byte aligned). A node that sees nothing gets zeros.
  * Values of positions that a node does not see never reach it, also when they are NaN or infinite
  * (a rejected draft's leftovers, a page never written). hq is a multiple of cache->heads, at most
- * 64 times it; T >= 1; B * T * hq < 2^31. Scores and sums are fp32; the weights of one tile are
+ * 64 times it; T >= 1; B * T * hq < 2^31, and fewer than 2^24 blocks of 16 rows (B times the key/value
+ * heads times T * hq / heads / 16, rounded up). Scores and sums are fp32; the weights of one tile are
  * rounded to bf16 for the product with V (rebuilt exactly from its codes, as K is). The split of
  * the positions over workgroups depends on lens and the sizes only: results repeat bit for bit. */
 BSFP8_API int bsfp8_tree_attention(const uint16_t* q, int64_t ldq, int64_t B, int64_t T, int64_t hq,
@@ -429,7 +431,7 @@ BSFP8_API size_t bsfp8_verify_workspace_bytes(int64_t B, int64_t T, int64_t V);
  *            [B][T-1]; u_sample: float [B], uniform in [0, 1) (all device; the draft arrays may be NULL
  *            when T = 1).
  *   out_tokens : int32_t [B][T]: the n accepted tokens, the next one, then -1. n_accepted: int32_t [B].
- * 1 <= T <= 64, 1 <= V <= 2^24. Probabilities and running sums are 64-bit, so that neighbouring
+ * 1 <= T <= 64, 1 <= V <= 2^24, B * (2 T - 1) < 2^24. Probabilities and running sums are 64-bit, so that neighbouring
  * sums are told apart. -inf logits have probability 0; a NaN logit counts as -inf; +inf ones share
  * the row. A row of nothing but -inf or NaN gives index 0. */
 BSFP8_API int bsfp8_verify_chain(const void* logits, const void* draft, int dtype, int64_t B, int64_t T, int64_t V,

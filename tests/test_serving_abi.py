@@ -67,6 +67,17 @@ def test_read_refusals(lib):
     assert rd(cache(), P(5), 4, P(6, 8), P(7), NULL) == B.ESTRIDE
 
 
+def test_grid_limits(lib):
+    """More workgroups than a launch can count (2^24 of 256 threads) are refused, not handed to the launch."""
+    assert write(lib, R=1 << 24, k=P(1 << 10), v=P(2 << 10), q=P(3 << 10), qo=P(4 << 10), slots=P(5 << 10),
+                 pos=P(6 << 10)) == B.ESHAPE
+    assert lib.bsfp8_cache_read(cache(dim=256), P(5), 1 << 27, P(1 << 10), P(2 << 10), NULL) == B.ESHAPE
+    assert B.bsfp8_attention_workspace_bytes(1 << 20, 1, 16, 16, 64, 64) == 0
+    assert B.bsfp8_attention_workspace_bytes((1 << 20) - 1, 1, 16, 16, 64, 64) > 0
+    assert B.bsfp8_verify_workspace_bytes(1 << 18, 64, 8) == 0
+    assert B.bsfp8_verify_workspace_bytes(1 << 18, 32, 8) > 0
+
+
 def attn(lib, c=None, q=P(5), ldq=256, Bn=3, T=2, hq=4, pages=P(6), ld=4, lens=P(7), nodes=NULL, mask=P(8), max_len=64,
          ws=P(9), wsb=1 << 30, out=P(10)):
     return lib.bsfp8_tree_attention(q, ldq, Bn, T, hq, c if c is not None else cache(), pages, ld, lens, nodes, mask, 0.1,
