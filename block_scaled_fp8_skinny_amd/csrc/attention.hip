@@ -30,9 +30,13 @@
 namespace bsfp8 {
 namespace {
 
-constexpr int NW = 4;                               // waves per workgroup
 constexpr int TILE = 32;                            // tokens of a wave's tile
-constexpr int UNIT = NW * TILE;
+// Waves of the ring kernel's workgroup. A CU's LDS has rings for eight waves (dim <= 128) or four. Eight in one
+// workgroup leave half as many partial results as two workgroups of four (a chain over 131072 positions, 48 rows: 75
+// against 89 us); two workgroups hide each other's beginnings and ends, which counts for more where results are small
+// (16 sequences' single tokens, dim 64: 25 against 29 us).
+constexpr int ring_waves(int dim, int mt) { return dim == 128 && mt >= 2 ? 8 : 4; }
+constexpr int ring_grid(int dim, int mt) { return dim <= 128 && ring_waves(dim, mt) == 4 ? 512 : 256; }
 constexpr float LIMIT = 256.f;                       // of a lane's eight weights' sum
 constexpr float M_NONE = -1e30f;                    // reference of a row that has seen nothing
 
@@ -50,6 +54,7 @@ struct AttnParams {
   uint32_t q_keep, q_flip;                          // the scale's sign, or a scale of 0, on the queries
   int B, T, hq, hkv, g, rows, mblocks, page, max_len, nwg;
   int br, unit, unit_shift, start_cost;             // rows of a block; tokens of a unit and their logarithm
+  int direct;                                       // a workgroup for each item
   FastDiv dpage, dg;
 };
 
@@ -255,41 +260,58 @@ __device__ __forceinline__ void flag_rows(bf16x8_t (&a)[4], const uint32_t (&see
     }
   }
 }
-template <int MT>
-__device__ __forceinline__ void unseen_nonfinite(bf16x8_t (&a)[4], const uint32_t (&sees)[MT], f32x4_t* o, int stride) {
-  uint32_t any = 0;
+// Whether codes (of one 32-bit word a token) or their scales can give such values: a NaN code (all ones but the
+// sign), a scale byte of 255, or one from 247, where 448 times the scale passes the largest bf16. (May say so of
+// values that are finite, not the reverse.)
+__device__ __forceinline__ bool maybe_nonfinite(const uint32_t (&raw)[8], const float (&sc)[8]) {
+  uint32_t nan = 0, top = 0;
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) any |= nonfinite(__builtin_bit_cast(u32x4_t, a[k])[j]);
-  if (__any(any != 0)) flag_rows<MT>(a, sees, o, stride);
+  for (int e = 0; e < 8; ++e) {
+    nan |= (raw[e] & 0x7F7F7F7Fu) + 0x01010101u;
+    top = max(top, __float_as_uint(sc[e]) & 0x7F800000u);
+  }
+  return (nan & 0x80808080u) != 0 || top >= 247u << 23;
+}
+
+// Four bits, of tokens first .. first + 3 (counted from the sequence's first node): bit i is set where node `nd` sees
+// the token. `word`: the node's mask; without masks (a chain) every token up to its own.
+__device__ __forceinline__ uint32_t seen4(bool masks, uint64_t word, int nd, int first) {
+  if (!masks) return first > nd ? 0u : 15u >> max(first + 3 - nd, 0);   // (28 at most when first <= nd)
+  const uint32_t before = first >= 0 ? 0u : 15u >> max(first + 4, 0);   // the prefix: seen
+  const int at = max(first, 0);
+  return before | ((at < 64 ? (uint32_t)(word >> at) : 0u) << min(at - first, 31) & 15u);
 }
 
 // Scores of tokens that a row does not see: -inf, and its bit of `sees` cleared. s: two 16-token groups of MT
-// row blocks, m = the lane's row of the first block, tok0 = its first token of the first group.
+// row blocks, m = the lane's row of the first block, tok0 = its first token of the first group; exist: bit e is
+// set where the lane's token e is below the sequence's end, in a page that exists.
 template <int MT>
-__device__ __forceinline__ void mask_scores(const AttnParams& p, int b, int m, int here, int prefix, int len, int tok0,
-                                            int pg0, int pg1, f32x4_t (&s)[2][MT], uint32_t (&sees)[MT]) {
+__device__ __forceinline__ void mask_scores(const AttnParams& p, int b, int m, int here, int prefix, int tok0, uint32_t exist,
+                                            f32x4_t (&s)[2][MT], uint32_t (&sees)[MT]) {
   asm volatile("" : "+v"(m), "+v"(tok0));           // nothing of this is worth a register across the loop
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt, m += 16) {
     const int nd = m < p.rows ? fdiv(m, p.dg) : here;
-    uint64_t bits = 0;
-    if (p.mask && nd < here) bits = (uint64_t)p.mask[(int64_t)b * p.T + nd];
-    uint32_t see = 0;
+    uint64_t word = 0;
+    if (p.mask && nd < here) word = (uint64_t)p.mask[(int64_t)b * p.T + nd];
+    const int first = tok0 - prefix;
+    uint32_t see = seen4(p.mask != nullptr, word, nd, first) | seen4(p.mask != nullptr, word, nd, first + 16) << 4;
+    see = nd < here ? see & exist : 0u;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int tok = tok0 + (e >> 2) * 16 + (e & 3), rel = tok - prefix;
-      bool seen = tok < len && (e < 4 ? pg0 : pg1) >= 0 && nd < here;
-      if (rel >= 0) seen = seen && (p.mask ? (bits >> (rel & 63) & 1) != 0 : rel <= nd);
-      s[e >> 2][mt][e & 3] = seen ? s[e >> 2][mt][e & 3] : -__builtin_inff();
-      see |= seen ? 1u << e : 0u;
-    }
+    for (int e = 0; e < 8; ++e) s[e >> 2][mt][e & 3] = see & (1u << e) ? s[e >> 2][mt][e & 3] : -__builtin_inff();
     sees[mt] = see;
   }
   // The compiler would else wait, after the branch that this stands in, for the loads above to land, on
   // the way without them too: and with them for the loads of the ring, which it does not know of.
   __builtin_amdgcn_s_waitcnt(0x0F70);               // vmcnt(0)
+}
+
+// The lane's eight tokens tok0 + 0..3 and + 16..19 that are there (see mask_scores).
+__device__ __forceinline__ uint32_t existing(int tok0, int len, int pg0, int pg1) {
+  const int left = len - tok0;
+  const uint32_t low = pg0 < 0 || left <= 0 ? 0u : 15u >> max(4 - left, 0);
+  const uint32_t high = pg1 < 0 || left <= 16 ? 0u : 15u >> max(20 - left, 0);
+  return low | high << 4;
 }
 
 // The weights 2^(s - m) of one row's eight scores (q . k, times scale2 for the base-2 score) as the B operand, and
@@ -373,31 +395,50 @@ struct Scales {
 };
 
 template <int D, int MT, int NS>
-__global__ void __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) attention_kernel(AttnParams p) {
+__global__ void __launch_bounds__(64 * ring_waves(D, MT), D <= 128 ? 2 : 1) attention_kernel(AttnParams p) {
   using G = Geo<D>;
+  constexpr int NW = ring_waves(D, MT), UNIT = NW * TILE;
   constexpr int ND = D / 16, NK = D / 32, BR = MT * 16;
-  constexpr int RING = NW * NS * G::STAGE, JOIN = 2 * MT * ND * 1024;
-  constexpr int BYTES = RING > JOIN ? RING : JOIN;
-  static_assert(UNIT == 128, "the plan's unit");
+  constexpr int RING = NW * NS * G::STAGE, RESULT = MT * ND * 1024;
+  // waves that put their result into LDS for the join: all, or half of them after adding the other half's
+  constexpr int HELD = NW * RESULT <= RING ? NW : NW / 2;
+  static_assert(HELD * RESULT <= RING, "the results take the ring's place");
   static_assert((NS - 1) * G::PER_TILE <= 63, "vector memory counter range");
-  static_assert(NW * BR * 8 <= TABLE * 4, "the statistics take the table's place");
-  __shared__ __align__(16) uint8_t ring[BYTES];
+  static_assert(NW * 8 <= NK * 64, "the statistics take the queries' place");
+  __shared__ __align__(16) uint8_t ring[RING];
   __shared__ __align__(16) uint4 queries[MT * NK * 64];   // B operands: row mt*16 + r16, values of K's operand order
   __shared__ __align__(16) int32_t table[TABLE];
-  float2* const stats = reinterpret_cast<float2*>(table);
+  float2* const stats = reinterpret_cast<float2*>(queries);
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, q4 = lane >> 4;
-  const Batch batch(p, lane);
   const int ipb = p.hkv * p.mblocks;                // heads and row blocks of a sequence
-  const int total = batch.total * ipb;
-  const Runs runs(total, p.nwg);
-  int u = runs.start(blockIdx.x);
-  const int u_end = runs.start(blockIdx.x + 1);
-  if (u >= u_end) return;
-  int before;
-  int b = batch.find(p, u / ipb, before);
-  int base = before * ipb;                          // first unit of sequence b
+  int u, u_end, b, base;                            // the run; its first sequence and that one's first unit
+  if (p.direct) {
+    b = blockIdx.x / ipb;
+    base = 0;
+    const int item = blockIdx.x - b * ipb, span = seq_span(p, b);
+    if (span == 0) {                                // an empty sequence
+      const int h = item / p.mblocks, m0 = (item - h * p.mblocks) * BR, rows = min(BR, p.rows - m0);
+      for (int x = threadIdx.x; x < rows * (D / 8); x += 64 * NW) {
+        const int m = m0 + x / (D / 8), nd = fdiv(m, p.dg);
+        *reinterpret_cast<uint4*>(p.out + (((int64_t)b * p.T + nd) * p.hq + (int64_t)h * p.g + (m - nd * p.g)) * D +
+                                  x % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
+      }
+      return;
+    }
+    u = item * span;
+    u_end = u + span;
+  } else {
+    const Batch batch(p, lane);
+    const Runs runs(batch.total * ipb, p.nwg);
+    u = runs.start(blockIdx.x);
+    u_end = runs.start(blockIdx.x + 1);
+    if (u >= u_end) return;
+    int before;
+    b = batch.find(p, u / ipb, before);
+    base = before * ipb;
+  }
   const int first_u = u;
 
   uint32_t ksrc[G::LOADS], vsrc[G::LOADS];
@@ -420,10 +461,12 @@ __global__ void __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) attention_kernel(At
     if (ub <= ua) break;                            // the run ends in the item's cost
     // the queries and the first stretch of the table, asked for together
     __syncthreads();                                // the last item's ring, queries and statistics are done with
+    int qw = wave;                                  // what follows from it is not worth keeping from item to item
+    asm volatile("" : "+s"(qw));
     uint4 qv[(MT * NK + NW - 1) / NW];
 #pragma unroll
     for (int k = 0; k < (MT * NK + NW - 1) / NW; ++k) {
-      const int f = wave + k * NW, j = f % NK, m = mb * BR + f / NK * 16 + r16;   // fragment f: rows, values
+      const int f = qw + k * NW, j = f % NK, m = mb * BR + f / NK * 16 + r16;   // fragment f: rows, values
       const int nd = fdiv(min(m, p.rows - 1), p.dg), hd = m - nd * p.g;
       qv[k] = make_uint4(0, 0, 0, 0);
       if (f < MT * NK && m < p.rows && nd < here)
@@ -431,13 +474,6 @@ __global__ void __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) attention_kernel(At
                                                 (j >> 1) * 64 + q4 * 16 + (j & 1) * 8);
     }
     bool absent = fill_table(p, b, h, ua * UNIT, len, table);
-#pragma unroll
-    for (int k = 0; k < (MT * NK + NW - 1) / NW; ++k) {
-      const int f = wave + k * NW;
-      if (f >= MT * NK) break;
-      queries[f * 64 + lane] = make_uint4((qv[k].x & p.q_keep) ^ p.q_flip, (qv[k].y & p.q_keep) ^ p.q_flip,
-                                          (qv[k].z & p.q_keep) ^ p.q_flip, (qv[k].w & p.q_keep) ^ p.q_flip);
-    }
     __syncthreads();
     absent = table_absent(absent, table);
     f32x4_t o[MT][ND];
@@ -519,7 +555,11 @@ __global__ void __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) attention_kernel(At
         uint32_t sees[MT];                          // bit e: the row sees token e
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) sees[mt] = 0xFF;
-        if (special) mask_scores<MT>(p, b, mb * BR + r16, here, prefix, len, t + q4 * 4, pg[0], pg[1], s, sees);
+        uint32_t exist = 0xFF;
+        if (special) {
+          exist = existing(t + q4 * 4, len, pg[0], pg[1]);
+          mask_scores<MT>(p, b, mb * BR + r16, here, prefix, t + q4 * 4, exist, s, sees);
+        }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           float f;
@@ -544,17 +584,18 @@ __global__ void __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) attention_kernel(At
               raw[gr * 4 + j] = *reinterpret_cast<const uint32_t*>(st + (2 + gr) * G::CODES + (j * 4 + q4) * D + d);
             Scales<D>::v(scales + (2 + gr) * G::SCALES, r16, q4, c, f + gr * 4);
           }
+          bool flagged = false;
           if (special) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (t + (e >> 2) * 16 + q4 * 4 + (e & 3) >= len || pg[e >> 2] < 0) {
-                raw[e] = 0;
-                f[e] = 1.f;
-              }
+            for (int e = 0; e < 8; ++e) {
+              raw[e] = exist & (1u << e) ? raw[e] : 0u;
+              f[e] = exist & (1u << e) ? f[e] : 1.f;
+            }
+            flagged = __any(maybe_nonfinite(raw, f));
           }
           bf16x8_t a[4];
           v_operands(raw, f, a);
-          if (special) unseen_nonfinite<MT>(a, sees, &o[0][0] + 4 * c, ND);
+          if (__builtin_expect(flagged, 0)) flag_rows<MT>(a, sees, &o[0][0] + 4 * c, ND);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -565,6 +606,16 @@ __global__ void __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) attention_kernel(At
 
 #pragma unroll 1
       for (int i = 0; i < NS && i < nt; ++i) issue(i);
+      if (uc == ua) {                               // while the first tiles are on their way
+#pragma unroll
+        for (int k = 0; k < (MT * NK + NW - 1) / NW; ++k) {
+          const int f = qw + k * NW;
+          if (f >= MT * NK) break;
+          queries[f * 64 + lane] = make_uint4((qv[k].x & p.q_keep) ^ p.q_flip, (qv[k].y & p.q_keep) ^ p.q_flip,
+                                              (qv[k].z & p.q_keep) ^ p.q_flip, (qv[k].w & p.q_keep) ^ p.q_flip);
+        }
+        __syncthreads();
+      }
 #pragma unroll 1
       for (int i = 0; i < nt; ++i) {
         const int ahead = min(NS - 1, nt - 1 - i);  // tiles in flight beyond this one
@@ -581,8 +632,8 @@ __global__ void __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) attention_kernel(At
       uc = uz;
     }
 
-    // join the waves: common reference, then the sums by a fixed tree (2, 3 into 0, 1; 1 into 0)
-    __syncthreads();                                // the table's page numbers are done with
+    // join the waves: a common reference, then the sums in a fixed order, a part of them by each wave
+    __syncthreads();                                // the rings and queries are done with
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       l[mt] += __shfl_xor(l[mt], 16);
@@ -590,79 +641,82 @@ __global__ void __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) attention_kernel(At
       if (q4 == 0) stats[wave * BR + mt * 16 + r16] = make_float2(mref[mt], l[mt]);
     }
     __syncthreads();
+    f32x4_t* const join = reinterpret_cast<f32x4_t*>(ring);
+    constexpr int SPAN = RESULT / 16;
+    auto total = [&](int row, float& m) {           // a row's reference and sum
+      m = M_NONE;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      float2 st[NW];
-      float m = M_NONE;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        st[w] = stats[w * BR + mt * 16 + r16];
-        m = fmaxf(m, st[w].x);
-      }
+      for (int w = 0; w < NW; ++w) m = fmaxf(m, stats[w * BR + row].x);
       float sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < NW; ++w) sum += st[w].y * __builtin_amdgcn_exp2f(st[w].x - m);
+      for (int w = 0; w < NW; ++w) sum += stats[w * BR + row].y * __builtin_amdgcn_exp2f(stats[w * BR + row].x - m);
+      return sum;
+    };
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      float m = M_NONE;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) m = fmaxf(m, stats[w * BR + mt * 16 + r16].x);
       const float f = __builtin_amdgcn_exp2f(mref[mt] - m);
 #pragma unroll
       for (int i = 0; i < ND; ++i) o[mt][i] *= f;
-      mref[mt] = m;
-      l[mt] = sum;
     }
-    f32x4_t* join = reinterpret_cast<f32x4_t*>(ring);
-    constexpr int SPAN = MT * ND * 64;
     auto put = [&](f32x4_t* d) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int i = 0; i < ND; ++i) d[(mt * ND + i) * 64 + lane] = o[mt][i];
     };
-    auto add = [&](const f32x4_t* d) {
+    if (HELD == NW || wave >= HELD) put(join + wave % HELD * SPAN);
+    if constexpr (HELD < NW) {
+      __syncthreads();
+      if (wave < HELD) {
+        f32x4_t* d = join + wave * SPAN;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int i = 0; i < ND; ++i) o[mt][i] += d[(mt * ND + i) * 64 + lane];
-    };
-    if (wave >= 2) put(join + (wave - 2) * SPAN);
-    __syncthreads();
-    if (wave < 2) add(join + wave * SPAN);
-    if (wave == 1) put(join + SPAN);
-    __syncthreads();
-    if (wave == 0) {
-      add(join + SPAN);
-      const bool whole = ua == 0 && ub == units;
-      const int64_t slot = (int64_t)blockIdx.x * 2 + (u == first_u ? 0 : 1);
-      if (lane == 0) {
-        int2* own = p.owners + ((int64_t)b * p.hkv + h) * p.mblocks + mb;
-        if (ua == 0) own->x = (int)slot;
-        if (ub == units) own->y = blockIdx.x;
+          for (int i = 0; i < ND; ++i) d[(mt * ND + i) * 64 + lane] += o[mt][i];
       }
+    }
+    __syncthreads();
+    const bool whole = ua == 0 && ub == units;
+    const int64_t slot = (int64_t)blockIdx.x * 2 + (u == first_u ? 0 : 1);
+    if (threadIdx.x == 0 && !p.direct) {
+      int2* own = p.owners + ((int64_t)b * p.hkv + h) * p.mblocks + mb;
+      if (ua == 0) own->x = (int)slot;
+      if (ub == units) own->y = blockIdx.x;
+    }
+#pragma unroll 1
+    for (int part = wave; part < MT * (ND / 4); part += NW) {   // a row block's values of four operand tiles
+      const int mt = part / (ND / 4), c = part % (ND / 4);
+      const f32x4_t* d = join + (mt * ND + 4 * c) * 64 + lane;
+      f32x4_t v[4];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const int row = mt * 16 + r16, m = mb * BR + row;
-        if (m >= p.rows) continue;
-        if (whole) {
-          const int nd = fdiv(m, p.dg);
-          const bool live = nd < here && l[mt] != 0.f;   // NaN passes
-          const float f = 1.f / l[mt];
-          uint16_t* dst = p.out + (((int64_t)b * p.T + nd) * p.hq + (int64_t)h * p.g + (m - nd * p.g)) * D;
+      for (int k = 0; k < 4; ++k) {
+        v[k] = d[k * 64];
 #pragma unroll
-          for (int c = 0; c < ND / 4; ++c)
+        for (int w = 1; w < HELD; ++w) v[k] += d[w * SPAN + k * 64];
+      }
+      const int row = mt * 16 + r16, m = mb * BR + row;
+      if (m >= p.rows) continue;
+      float top;
+      const float sum = total(row, top);
+      if (whole) {
+        const int nd = fdiv(m, p.dg);
+        const bool live = nd < here && sum != 0.f;   // NaN passes
+        const float f = 1.f / sum;
+        uint16_t* dst = p.out + (((int64_t)b * p.T + nd) * p.hq + (int64_t)h * p.g + (m - nd * p.g)) * D;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              *reinterpret_cast<uint2*>(dst + v_value<D>(q4 * 4 + e, 4 * c)) =
-                  live ? make_uint2(pack_bf16x2(o[mt][4 * c][e] * f, o[mt][4 * c + 1][e] * f),
-                                    pack_bf16x2(o[mt][4 * c + 2][e] * f, o[mt][4 * c + 3][e] * f))
-                       : make_uint2(0, 0);
-        } else {
-          float* dst = p.part + (slot * BR + row) * D;
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<uint2*>(dst + v_value<D>(q4 * 4 + e, 4 * c)) =
+              live ? make_uint2(pack_bf16x2(v[0][e] * f, v[1][e] * f), pack_bf16x2(v[2][e] * f, v[3][e] * f))
+                   : make_uint2(0, 0);
+      } else {
+        float* dst = p.part + (slot * BR + row) * D;
 #pragma unroll
-          for (int c = 0; c < ND / 4; ++c)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              *reinterpret_cast<f32x4_t*>(dst + v_value<D>(q4 * 4 + e, 4 * c)) =
-                  f32x4_t{o[mt][4 * c][e], o[mt][4 * c + 1][e], o[mt][4 * c + 2][e], o[mt][4 * c + 3][e]};
-          if (q4 == 0) p.stat[slot * BR + row] = make_float2(mref[mt], l[mt]);
-        }
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<f32x4_t*>(dst + v_value<D>(q4 * 4 + e, 4 * c)) = f32x4_t{v[0][e], v[1][e], v[2][e], v[3][e]};
+        if (c == 0 && q4 == 0) p.stat[slot * BR + row] = make_float2(top, sum);
       }
     }
     u += vb - va;
@@ -1067,7 +1121,7 @@ __global__ void __launch_bounds__(64 * WW, 2) attention_wide_kernel(AttnParams p
           if (__builtin_expect(special, 0)) {
             uint32_t sees[MT];
             const int* pg = table + ((t - tbase) >> 4);
-            mask_scores<MT>(p, b, m0 + r16, here, prefix, len, t + q4 * 4, pg[0], pg[1], s, sees);
+            mask_scores<MT>(p, b, m0 + r16, here, prefix, t + q4 * 4, existing(t + q4 * 4, len, pg[0], pg[1]), s, sees);
             if (__builtin_amdgcn_readfirstlane(spoiled[i % 3][set])) poison(i, set, sees);
           }
           if (set == 0 && i + 1 < uz) rebuild(i + 1, raw, frags[(i + 1) & 1]);
@@ -1148,9 +1202,9 @@ __global__ void __launch_bounds__(64 * WW, 2) attention_wide_kernel(AttnParams p
 }
 
 struct AttnPlan {
-  int wide, mt, br, unit_shift, start_cost, mblocks, nwg;
+  int wide, mt, br, unit_shift, start_cost, mblocks, nwg, direct;
 };
-// Rows of a block and the grid: every unit its own workgroup up to one (wide) or two workgroups per CU.
+// Rows of a block and the grid: every unit its own workgroup up to one workgroup per CU.
 AttnPlan attention_plan(const AttentionArgs& a) {
   const int64_t rows = a.T * (a.hq / a.cache.heads);
   const bool small = a.cache.dim <= 128;
@@ -1162,9 +1216,18 @@ AttnPlan attention_plan(const AttentionArgs& a) {
   p.mt = (int)((rows + step * blocks - 1) / (step * blocks));
   p.br = (int)(p.mt * step);
   p.mblocks = (int)((rows + p.br - 1) / p.br);
-  p.unit_shift = !p.wide ? 7 : a.cache.dim == 64 ? 7 : a.cache.dim == 128 ? 6 : 5;
+  p.unit_shift = !p.wide ? (ring_waves((int)a.cache.dim, p.mt) == 8 ? 8 : 7) : a.cache.dim == 64 ? 7 : a.cache.dim == 128 ? 6 : 5;
   const int64_t units = a.B * a.cache.heads * p.mblocks * ((a.max_len + (1 << p.unit_shift) - 1) >> p.unit_shift);
-  const int64_t grid = p.wide ? 256 : 512;
+  const int64_t grid = p.wide ? 256 : ring_grid((int)a.cache.dim, p.mt);
+  const int64_t items = a.B * a.cache.heads * p.mblocks;
+  // short contexts: a workgroup for each item, nothing to join (one sequence of 128 tokens, 16 heads over 2 of dim 64:
+  // 7.7 against 10.0 us; even at 512 tokens, at 1023 13.0 against 11.0; twice the work a token above dim 128)
+  p.direct = !p.wide && a.max_len <= (small ? 512 : 256);
+  if (p.direct) {
+    p.nwg = (int)items;
+    p.start_cost = 0;
+    return p;
+  }
   p.nwg = (int)(units < 1 ? 1 : units > grid ? grid : units);
   // beginning an item costs about as long as half a kilobyte-wide unit's 128 tokens take (13 us against 2.9 us
   // a unit at dim 128 and 48 rows); with few units a workgroup has no second item
@@ -1185,7 +1248,8 @@ int join(const AttnParams& p, hipStream_t stream) {
 
 template <int D, int MT, int NS>
 int ring(const AttnParams& p, hipStream_t stream) {
-  hipLaunchKernelGGL((attention_kernel<D, MT, NS>), dim3((unsigned)p.nwg), dim3(64 * NW), 0, stream, p);
+  hipLaunchKernelGGL((attention_kernel<D, MT, NS>), dim3((unsigned)p.nwg), dim3(64 * ring_waves(D, MT)), 0, stream, p);
+  if (p.direct) return hip_status(hipGetLastError());
   return hipGetLastError() == hipSuccess ? join<D>(p, stream) : BSFP8_EHIP;
 }
 template <int D, int MT>
@@ -1200,6 +1264,7 @@ inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 size_t attention_ws_bytes(const AttentionArgs& a) {
   const AttnPlan pl = attention_plan(a);
+  if (pl.direct) return 256;                        // (not read)
   const size_t rows = (size_t)pl.nwg * 2 * pl.br;
   return align256((size_t)a.B * a.cache.heads * pl.mblocks * sizeof(int2)) + align256(rows * sizeof(float2)) +
          rows * (size_t)a.cache.dim * 4;
@@ -1244,6 +1309,7 @@ int launch_tree_attention(const AttentionArgs& a, hipStream_t stream) {
   p.unit_shift = pl.unit_shift;
   p.unit = 1 << pl.unit_shift;
   p.start_cost = pl.start_cost;
+  p.direct = pl.direct;
   p.dpage = make_fastdiv((uint32_t)a.cache.page);
   p.dg = make_fastdiv((uint32_t)p.g);
   const int D = (int)a.cache.dim, mt = pl.mt;
