@@ -4,8 +4,8 @@
 // are its (node, query head) pairs, g * T of them (g query heads share it). With s = q . k * scale in
 // base 2 (scale * log2 e), a running reference m per row, and weights w = 2^(s - m):
 //   l = sum w,  O = sum w V,  out = O / l,
-// one pass over the positions; m only moves (to the largest score so far; O and l are rescaled) when eight
-// weights of a lane sum to more than LIMIT, which bounds them.
+// one pass over the positions; m only moves (to the largest score so far; O and l are rescaled) when a score
+// passes it by more than HEADROOM, which bounds the weights.
 //
 // Products on bf16 MFMA (16x16x32), transposed so that nothing crosses lanes between them:
 //   S^T = K Q^T: a lane ends with four tokens of one row, which in pairs of 16-token groups are just
@@ -37,7 +37,7 @@ constexpr int TILE = 32;                            // tokens of a wave's tile
 // (16 sequences' single tokens, dim 64: 25 against 29 us).
 constexpr int ring_waves(int dim, int mt) { return dim == 128 && mt >= 2 ? 8 : 4; }
 constexpr int ring_grid(int dim, int mt) { return dim <= 128 && ring_waves(dim, mt) == 4 ? 512 : 256; }
-constexpr float LIMIT = 256.f;                       // of a lane's eight weights' sum
+constexpr float HEADROOM = 8.f;                     // weights are at most 2^8
 constexpr float M_NONE = -1e30f;                    // reference of a row that has seen nothing
 
 struct AttnParams {
@@ -314,38 +314,53 @@ __device__ __forceinline__ uint32_t existing(int tok0, int len, int pg0, int pg1
   return low | high << 4;
 }
 
-// The weights 2^(s - m) of one row's eight scores (q . k, times scale2 for the base-2 score) as the B operand, and
-// their sum; true (for the wave) when the reference moved: then f is the factor of everything so far. Whether it
-// has to move is seen from the weights' own sum, which is needed anyway: no maximum is taken while it does not.
+// The weights 2^(s - m) of MT row blocks' eight scores a lane (q . k, times scale2 for the base-2 score) as B operands, and
+// their sums. The references move to the rows' largest scores when one of the wave's scores is more than 2^HEADROOM times
+// its row's: rarely, so the exchange between lanes and the rescaling (rescale(mt, f): everything so far times f) are off
+// the common path, and all exponentials come after the one branch (taking them first and testing their sums left 11
+// register moves a row block, a sixth of the wide kernel's vector instructions).
 // The weights are rounded to bf16 for the matrix product (at most half a step, 2^-8, each); the sum takes them
 // unrounded.
-__device__ __forceinline__ bool weights(const f32x4_t& s0, const f32x4_t& s1, float scale2, float& mref, float& l,
-                                        bf16x8_t& pf, float& f) {
-  float x[8], sum = 0.f;
-  auto run = [&] {
+template <int MT, typename R>
+__device__ __forceinline__ void weights(const f32x4_t (&s)[2][MT], float scale2, float (&mref)[MT], float (&l)[MT],
+                                        bf16x8_t (&pf)[MT], R rescale) {
+  float x[MT][8];
+  bool far = false;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = __builtin_amdgcn_exp2f(fmaf(e < 4 ? s0[e] : s1[e - 4], scale2, -mref));
-    sum = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
-  };
-  run();
-  const bool moved = __any(sum > LIMIT);
-  if (__builtin_expect(moved, 0)) {
-    float top = s0[0];
+  for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-    for (int e = 1; e < 8; ++e) top = fmaxf(top, e < 4 ? s0[e] : s1[e - 4]);
-    top *= scale2;
-    top = fmaxf(top, __shfl_xor(top, 16));
-    top = fmaxf(top, __shfl_xor(top, 32));
-    const float m = fmaxf(mref, top);
-    f = __builtin_amdgcn_exp2f(mref - m);
-    mref = m;
-    l *= f;
-    run();
+    for (int e = 0; e < 8; ++e) x[mt][e] = fmaf(s[e >> 2][mt][e & 3], scale2, -mref[mt]);
+    float top = x[mt][0];
+#pragma unroll
+    for (int e = 1; e < 8; ++e) top = fmaxf(top, x[mt][e]);
+    far = far || top > HEADROOM;
   }
-  l += sum;
-  const u32x4_t w = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
-  pf = __builtin_bit_cast(bf16x8_t, w);
-  return moved;
+  if (__builtin_expect(__any(far), 0)) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      float t = s[0][mt][0];
+#pragma unroll
+      for (int e = 1; e < 8; ++e) t = fmaxf(t, s[e >> 2][mt][e & 3]);
+      t *= scale2;
+      t = fmaxf(t, __shfl_xor(t, 16));
+      t = fmaxf(t, __shfl_xor(t, 32));
+      const float m = fmaxf(mref[mt], t), f = __builtin_amdgcn_exp2f(mref[mt] - m);
+      mref[mt] = m;
+      l[mt] *= f;
+      rescale(mt, f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[mt][e] = fmaf(s[e >> 2][mt][e & 3], scale2, -m);
+    }
+  }
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[mt][e] = __builtin_amdgcn_exp2f(x[mt][e]);
+    l[mt] += ((x[mt][0] + x[mt][1]) + (x[mt][2] + x[mt][3])) + ((x[mt][4] + x[mt][5]) + (x[mt][6] + x[mt][7]));
+    const u32x4_t w = {pack_bf16x2(x[mt][0], x[mt][1]), pack_bf16x2(x[mt][2], x[mt][3]), pack_bf16x2(x[mt][4], x[mt][5]),
+                       pack_bf16x2(x[mt][6], x[mt][7])};
+    pf[mt] = __builtin_bit_cast(bf16x8_t, w);
+  }
 }
 
 // Scale factors (2^(byte - 127), in the exponent field; the conversions read nothing else of the operand,
@@ -560,14 +575,10 @@ __global__ void __launch_bounds__(64 * ring_waves(D, MT), D <= 128 ? 2 : 1) atte
           exist = existing(t + q4 * 4, len, pg[0], pg[1]);
           mask_scores<MT>(p, b, mb * BR + r16, here, prefix, t + q4 * 4, exist, s, sees);
         }
+        weights<MT>(s, p.scale2, mref, l, pf, [&](int mt, float f) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          float f;
-          if (weights(s[0][mt], s[1][mt], p.scale2, mref[mt], l[mt], pf[mt], f)) {
-#pragma unroll
-            for (int k = 0; k < ND; ++k) o[mt][k] *= f;
-          }
-        }
+          for (int k = 0; k < ND; ++k) o[mt][k] *= f;
+        });
         // V: dword c of the lane's values of each token; their block is the same for all four
 #pragma unroll
         for (int c = 0; c < ND / 4; ++c) {
@@ -959,8 +970,7 @@ __global__ void __launch_bounds__(64 * WW, 2) attention_wide_kernel(AttnParams p
       // wave; the codes and scales are read a phase before they are converted.
       struct Raw {
         uint4 k[W::KW];
-        uint32_t v[W::VW][8];
-        float kf[W::KW], vf[W::VW][8];
+        uint32_t v[W::VW][8], ks[W::KW], vs[W::VW][8];
       };
       auto read_raw = [&](int i, Raw& r) {
         const uint8_t* st = ring + (i % STAGES) * W::STAGE;
@@ -970,7 +980,7 @@ __global__ void __launch_bounds__(64 * WW, 2) attention_wide_kernel(AttnParams p
           const int unit = wave + n * WW, gr = unit / NC, j = unit % NC;
           if (W::KU % WW && unit >= W::KU) break;
           r.k[n] = *reinterpret_cast<const uint4*>(st + gr * 16 * D + r16 * D + (((4 * j + q4) ^ Geo<D>::swizzle(r16)) * 16));
-          r.kf[n] = block_scale(sc[gr * (D / 2) + r16 * (D / 32) + 2 * j + (q4 >> 1)]);
+          r.ks[n] = sc[gr * (D / 2) + r16 * (D / 32) + 2 * j + (q4 >> 1)];
         }
 #pragma unroll
         for (int n = 0; n < W::VW; ++n) {
@@ -982,23 +992,23 @@ __global__ void __launch_bounds__(64 * WW, 2) attention_wide_kernel(AttnParams p
 #pragma unroll
             for (int j = 0; j < 4; ++j) r.v[n][gr * 4 + j] = *reinterpret_cast<const uint16_t*>(codes + j * 4 * D);
             const uint8_t* g = sc + W::SCALES + (set * 2 + gr) * (D / 2);
-            float* f = r.vf[n] + gr * 4;
+            uint32_t* w = r.vs[n] + gr * 4;         // words that hold the tokens' scales (see v_scale)
             if constexpr (D == 128) {
-              const uint4 w = *reinterpret_cast<const uint4*>(g + q4 * 16);
-              const uint32_t t[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j) f[j] = Scales<D>::rotated(t[j], 2 * c + (r16 >> 3));
+              const uint4 x = *reinterpret_cast<const uint4*>(g + q4 * 16);
+              w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
             } else if constexpr (D == 64) {
-              const uint2 w = *reinterpret_cast<const uint2*>(g + q4 * 8);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) f[j] = Scales<D>::rotated(j < 2 ? w.x : w.y, 2 * (j & 1) + (r16 >> 3));
+              const uint2 x = *reinterpret_cast<const uint2*>(g + q4 * 8);
+              w[0] = w[1] = x.x, w[2] = w[3] = x.y;
             } else {
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                f[j] = Scales<D>::rotated(*reinterpret_cast<const uint16_t*>(g + (q4 * 4 + j) * (D / 32) + 2 * c), r16 >> 3);
+              for (int j = 0; j < 4; ++j) w[j] = *reinterpret_cast<const uint16_t*>(g + (q4 * 4 + j) * (D / 32) + 2 * c);
             }
           }
         }
+      };
+      // (kept out of read_raw: nothing there may wait for LDS)
+      auto v_scale = [&](uint32_t word, int j, int c) {
+        return Scales<D>::rotated(word, (D == 128 ? 2 * c : D == 64 ? 2 * (j & 1) : 0) + (r16 >> 3));
       };
       auto rebuild = [&](int i, Raw& r, uint4* buf) {
 #pragma unroll
@@ -1006,28 +1016,32 @@ __global__ void __launch_bounds__(64 * WW, 2) attention_wide_kernel(AttnParams p
           const int unit = wave + n * WW, gr = unit / NC, j = unit % NC;
           if (W::KU % WW && unit >= W::KU) break;
           uint4* dst = buf + (gr * NK + 2 * j) * 64 + lane;
-          dst[0] = __builtin_bit_cast(uint4, dequant8(r.k[n].x, r.k[n].y, r.kf[n]));
-          dst[64] = __builtin_bit_cast(uint4, dequant8(r.k[n].z, r.k[n].w, r.kf[n]));
+          const float f = block_scale(r.ks[n]);
+          dst[0] = __builtin_bit_cast(uint4, dequant8(r.k[n].x, r.k[n].y, f));
+          dst[64] = __builtin_bit_cast(uint4, dequant8(r.k[n].z, r.k[n].w, f));
         }
 #pragma unroll
         for (int n = 0; n < W::VW; ++n) {
           const int unit = wave + n * WW, half = unit & 1, set = (unit >> 1) / NC, c = (unit >> 1) % NC;
           if (W::VU % WW && unit >= W::VU) break;
           const int t = i * W::TOKENS + set * 32;
+          float f[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = v_scale(r.vs[n][e], e & 3, c);
           if (t + 32 > len || absent) {             // tokens that are not there: zeros
             const int* pg = table + ((t - tbase) >> 4);
+            const uint32_t exist = existing(t + q4 * 4, len, pg[0], pg[1]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (t + (e >> 2) * 16 + q4 * 4 + (e & 3) >= len || pg[e >> 2] < 0) {
-                r.v[n][e] = 0;
-                r.vf[n][e] = 1.f;
-              }
+            for (int e = 0; e < 8; ++e) {
+              r.v[n][e] = exist & (1u << e) ? r.v[n][e] : 0u;
+              f[e] = exist & (1u << e) ? f[e] : 1.f;
+            }
           }
           u32x4_t a0, a1;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint32_t x = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r.v[n][2 * j], r.vf[n][2 * j], false));
-            const uint32_t y = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r.v[n][2 * j + 1], r.vf[n][2 * j + 1], false));
+            const uint32_t x = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r.v[n][2 * j], f[2 * j], false));
+            const uint32_t y = bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(r.v[n][2 * j + 1], f[2 * j + 1], false));
             a0[j] = __builtin_amdgcn_perm(y, x, 0x05040100u);
             a1[j] = __builtin_amdgcn_perm(y, x, 0x07060302u);
           }
@@ -1126,14 +1140,10 @@ __global__ void __launch_bounds__(64 * WW, 2) attention_wide_kernel(AttnParams p
           }
           if (set == 0 && i + 1 < uz) rebuild(i + 1, raw, frags[(i + 1) & 1]);
           bf16x8_t pf[MT];
+          weights<MT>(s, p.scale2, mref, l, pf, [&](int mt, float f) {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            float f;
-            if (weights(s[0][mt], s[1][mt], p.scale2, mref[mt], l[mt], pf[mt], f)) {
-#pragma unroll
-              for (int k = 0; k < ND; ++k) o[mt][k] *= f;
-            }
-          }
+            for (int k = 0; k < ND; ++k) o[mt][k] *= f;
+          });
           if (set + 1 < W::SETS) {
             ask_k(buf, set + 1, kf);
           } else {
@@ -1211,7 +1221,7 @@ AttnPlan attention_plan(const AttentionArgs& a) {
   AttnPlan p;
   const int narrow = small ? 3 : 2;                 // blocks of 16 rows that a wave of the ring kernel holds
   p.wide = rows > narrow * 16;
-  const int64_t step = p.wide ? WW * 16 : 16, most = p.wide ? (a.cache.dim == 64 ? 4 : small ? 2 : 1) : narrow;
+  const int64_t step = p.wide ? WW * 16 : 16, most = p.wide ? (a.cache.dim == 64 ? 3 : small ? 2 : 1) : narrow;
   const int64_t blocks = (rows + step * most - 1) / (step * most);
   p.mt = (int)((rows + step * blocks - 1) / (step * blocks));
   p.br = (int)(p.mt * step);
@@ -1315,8 +1325,7 @@ int launch_tree_attention(const AttentionArgs& a, hipStream_t stream) {
   const int D = (int)a.cache.dim, mt = pl.mt;
   if (pl.wide) {
     if (D == 64)
-      return mt == 1 ? wide<64, 1>(p, stream) : mt == 2 ? wide<64, 2>(p, stream) : mt == 3 ? wide<64, 3>(p, stream)
-                                                                                 : wide<64, 4>(p, stream);
+      return mt == 1 ? wide<64, 1>(p, stream) : mt == 2 ? wide<64, 2>(p, stream) : wide<64, 3>(p, stream);
     if (D == 128) return mt == 1 ? wide<128, 1>(p, stream) : wide<128, 2>(p, stream);
     return D == 192 ? wide<192, 1>(p, stream) : wide<256, 1>(p, stream);
   }
