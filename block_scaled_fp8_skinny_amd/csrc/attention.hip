@@ -16,15 +16,18 @@
 // its eight tokens, the codes of D/16 neighbouring values, and interleaves the converted pairs of two
 // tokens (byte permutes).
 //
-// A workgroup is NW waves that share a head's rows and split its tokens in tiles of 32, each wave
-// with a ring of NS tiles in LDS that the LDS mode of global loads fills (codes are contiguous per
-// 16 tokens of a page and head); waves only wait for their own loads. The waves' results are joined
-// through LDS. Work is cut evenly over the grid: the units (128 tokens of one head and row block) of
-// all sequences, in order, are divided into equal runs, one per workgroup, so that ragged lengths
-// leave nobody idle; a head that falls into several runs leaves partial (m, l, O) in the workspace
-// for a second kernel to join.
-#include <type_traits>
-
+// Two kernels, chosen by the rows g * T of a key/value head (attention_plan):
+//   ring  up to 96 rows (64 above dim 128): a workgroup's waves share 16 to 48 rows and split their tokens in tiles of 32,
+//         each wave with a ring of NS tiles in LDS that the LDS mode of global loads fills (codes are contiguous per 16
+//         tokens of a page and head); waves only wait for their own loads, and are joined through LDS at an item's end.
+//         Bound by HBM: the loop of a chain of 6 over 131072 positions (64 heads over 8 of dim 128) streams 6.2 TB/s; 75 us
+//         in all, of which 5 go before the first tile is asked for, 10 to the waves' skew and join, 5 to the joining kernel.
+//   wide  more rows: the waves split the rows and share the tokens, which are rebuilt once per workgroup (see there).
+// Work is cut evenly over the grid: the units (the tokens that a workgroup's waves take in one step, of one head and row
+// block) of all sequences, in order, are divided into equal runs, one per workgroup, so that ragged lengths leave nobody
+// idle; a head that falls into several runs leaves partial (m, l, O) in the workspace for a joining kernel. Short contexts
+// are not cut: a workgroup for each head and row block, one launch. A launch is as short as its code: the instruction
+// cache starts cold, and 5 KB of straight code took 3 us (masks by single comparisons, sums unrolled per row block).
 #include "device.h"
 
 namespace bsfp8 {
@@ -104,6 +107,39 @@ struct Batch {
     }
   }
 };
+
+// A workgroup's run [u, u_end), its first sequence b and the first unit of that (base); false for an empty run. Without
+// splitting (direct) the run is an item; an item of an empty sequence has its outputs zeroed here.
+template <int D>
+__device__ __forceinline__ bool first_run(const AttnParams& p, int lane, int br, int& u, int& u_end, int& b, int& base) {
+  const int ipb = p.hkv * p.mblocks;                // heads and row blocks of a sequence
+  if (p.direct) {
+    b = blockIdx.x / ipb;
+    base = 0;
+    const int item = blockIdx.x - b * ipb, span = seq_span(p, b);
+    if (span == 0) {
+      const int h = item / p.mblocks, m0 = (item - h * p.mblocks) * br, rows = min(br, p.rows - m0);
+      for (int x = threadIdx.x; x < rows * (D / 8); x += blockDim.x) {
+        const int m = m0 + x / (D / 8), nd = fdiv(m, p.dg);
+        *reinterpret_cast<uint4*>(p.out + (((int64_t)b * p.T + nd) * p.hq + (int64_t)h * p.g + (m - nd * p.g)) * D +
+                                  x % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
+      }
+      return false;
+    }
+    u = item * span;
+    u_end = u + span;
+    return true;
+  }
+  const Batch batch(p, lane);
+  const Runs runs(batch.total * ipb, p.nwg);
+  u = runs.start(blockIdx.x);
+  u_end = runs.start(blockIdx.x + 1);
+  if (u >= u_end) return false;
+  int before;
+  b = batch.find(p, u / ipb, before);
+  base = before * ipb;
+  return true;
+}
 
 // Global loads in LDS mode (see lds_load16 of device.h): 64-bit addresses, as a cache passes 4 GiB. The
 // base may come from a lane exchange or readfirstlane, so the five wait states that a vector-written
@@ -230,34 +266,44 @@ __device__ __forceinline__ int v_value(int x, int i) {
 
 // NaN and infinite values of V (a, four operand tiles) must not reach rows that do not see their token,
 // though 0 * NaN is NaN in the product: they are replaced by zeros here, and the rows that do see one
-// (the product of the flags of such values with the flags of seen tokens is positive) get NaN.
+// (the product of the flags of such values with the flags of seen tokens is positive) get it added.
 __device__ __forceinline__ uint32_t nonfinite(uint32_t v) {   // ones in the halves of a bf16 pair that are NaN or infinite
   return ((v & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((v & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
 }
 template <int MT>
 __device__ __forceinline__ void flag_rows(bf16x8_t (&a)[4], const uint32_t (&sees)[MT], f32x4_t* o, int stride) {
+#pragma unroll 1
+  for (int kind = 0; kind < 3; ++kind) {            // infinity, its negative, NaN
+    const float what = __uint_as_float(kind == 0 ? 0x7F800000u : kind == 1 ? 0xFF800000u : 0x7FC00000u);
+    auto flag_of = [&](uint32_t h) {                // h: a bf16 value
+      return (kind == 2 ? (h & 0x7FFFu) > 0x7F80u : h == (kind == 0 ? 0x7F80u : 0xFF80u)) ? 0x3F80u : 0u;
+    };
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const u32x4_t v = __builtin_bit_cast(u32x4_t, a[k]);
+      u32x4_t flag;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) flag[j] = flag_of(v[j] & 0xFFFFu) | flag_of(v[j] >> 16) << 16;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        u32x4_t w;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          w[j] = ((sees[mt] >> (2 * j)) & 1 ? 0x3F80u : 0u) | ((sees[mt] >> (2 * j + 1)) & 1 ? 0x3F800000u : 0u);
+        const f32x4_t n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            __builtin_bit_cast(bf16x8_t, flag), __builtin_bit_cast(bf16x8_t, w), f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (n[r] > 0.f) o[mt * stride + k][r] += what;
+      }
+    }
+  }
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    u32x4_t v = __builtin_bit_cast(u32x4_t, a[k]), flag;
+    u32x4_t v = __builtin_bit_cast(u32x4_t, a[k]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t x = nonfinite(v[j]);
-      flag[j] = 0x3F803F80u & x;
-      v[j] &= ~x;
-    }
+    for (int j = 0; j < 4; ++j) v[j] &= ~nonfinite(v[j]);
     a[k] = __builtin_bit_cast(bf16x8_t, v);
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      u32x4_t w;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        w[j] = ((sees[mt] >> (2 * j)) & 1 ? 0x3F80u : 0u) | ((sees[mt] >> (2 * j + 1)) & 1 ? 0x3F800000u : 0u);
-      const f32x4_t n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-          __builtin_bit_cast(bf16x8_t, flag), __builtin_bit_cast(bf16x8_t, w), f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (n[r] > 0.f) o[mt * stride + k][r] = __uint_as_float(0x7FC00000u);
-    }
   }
 }
 // Whether codes (of one 32-bit word a token) or their scales can give such values: a NaN code (all ones but the
@@ -427,33 +473,9 @@ __global__ void __launch_bounds__(64 * ring_waves(D, MT), D <= 128 ? 2 : 1) atte
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, q4 = lane >> 4;
+  int u, u_end, b, base;
+  if (!first_run<D>(p, lane, BR, u, u_end, b, base)) return;
   const int ipb = p.hkv * p.mblocks;                // heads and row blocks of a sequence
-  int u, u_end, b, base;                            // the run; its first sequence and that one's first unit
-  if (p.direct) {
-    b = blockIdx.x / ipb;
-    base = 0;
-    const int item = blockIdx.x - b * ipb, span = seq_span(p, b);
-    if (span == 0) {                                // an empty sequence
-      const int h = item / p.mblocks, m0 = (item - h * p.mblocks) * BR, rows = min(BR, p.rows - m0);
-      for (int x = threadIdx.x; x < rows * (D / 8); x += 64 * NW) {
-        const int m = m0 + x / (D / 8), nd = fdiv(m, p.dg);
-        *reinterpret_cast<uint4*>(p.out + (((int64_t)b * p.T + nd) * p.hq + (int64_t)h * p.g + (m - nd * p.g)) * D +
-                                  x % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
-      }
-      return;
-    }
-    u = item * span;
-    u_end = u + span;
-  } else {
-    const Batch batch(p, lane);
-    const Runs runs(batch.total * ipb, p.nwg);
-    u = runs.start(blockIdx.x);
-    u_end = runs.start(blockIdx.x + 1);
-    if (u >= u_end) return;
-    int before;
-    b = batch.find(p, u / ipb, before);
-    base = before * ipb;
-  }
   const int first_u = u;
 
   uint32_t ksrc[G::LOADS], vsrc[G::LOADS];
@@ -838,6 +860,10 @@ __global__ void __launch_bounds__(256) attention_join_kernel(AttnParams p, int j
 // into operand order, also in LDS (a fragment of one MFMA is 64 lanes x 16 bytes, read back without bank
 // conflicts), two buffers deep: while a tile is computed, the next one is rebuilt, a unit of K and one of V
 // by each wave. The operand order of V is value c * 64 + x * 4 + k for column x of 16-row tile 4c + k.
+// Trees of 64 nodes over 16384 positions of 4 sequences, 64 heads over 8 of dim 128 (137 GFLOP): 177 us, 0.78 PFLOP/s.
+// Counters: matrix cores busy 33% of the time, vector ALUs 45%, LDS 28%; two waves a SIMD overlap them little (all the
+// registers are taken at 32 rows a wave). Taking turns by halves, products against softmax with a barrier after each
+// phase, was slower (217 us), as was rebuilding V in half the waves and K in the others (180).
 // ------------------------------------------------------------------------------------------------
 constexpr int WW = 8;                               // waves per workgroup
 
@@ -846,6 +872,10 @@ struct Wide {
   static constexpr int TOKENS = D == 64 ? 128 : D == 128 ? 64 : 32;   // of a tile
   static constexpr int SHIFT = D == 64 ? 7 : D == 128 ? 6 : 5;
   static constexpr int SETS = TOKENS / 32, GROUPS = TOKENS / 16;
+  // K's fragments of the next tile are read after the products with V, where both do not fit the registers (reading
+  // them before spilled 43 registers, and a reload waits for the ring)
+  static constexpr bool LATE_K = D == 256;
+  static_assert(!LATE_K || SETS == 1, "the next tile's");
   static constexpr int KU = GROUPS * (D / 64), VU = SETS * (D / 64) * 2;   // rebuilding units: 16 codes, 8 x 2 codes a lane
   static constexpr int KF = GROUPS * (D / 32) * 64, VF = SETS * (D / 16) * 64;   // 16-byte words of a buffer
   static constexpr int CODES = TOKENS * D;                            // bytes of K's codes of a tile, and of V's
@@ -863,19 +893,13 @@ __global__ void __launch_bounds__(64 * WW, 2) attention_wide_kernel(AttnParams p
   __shared__ __align__(16) uint4 frags[2][W::KF + W::VF];
   __shared__ __align__(16) uint8_t ring[STAGES * W::STAGE];
   __shared__ int32_t table[TABLE];
-  __shared__ int spoiled[3][W::SETS];               // of tile i in slot i % 3: a set holds NaN or infinite values of V that some row may not see
+  __shared__ int spoiled[3][W::SETS];               // of tile i in slot i % 3: a set has NaN or infinite values of V
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, q4 = lane >> 4;
-  const Batch batch(p, lane);
+  int u, u_end, b, base;
+  if (!first_run<D>(p, lane, BR, u, u_end, b, base)) return;
   const int ipb = p.hkv * p.mblocks;
-  const Runs runs(batch.total * ipb, p.nwg);
-  int u = runs.start(blockIdx.x);
-  const int u_end = runs.start(blockIdx.x + 1);
-  if (u >= u_end) return;
-  int before;
-  int b = batch.find(p, u / ipb, before);
-  int base = before * ipb;
   const int first_u = u;
 
   // this wave's loads of a tile: 1 KB of a group's codes of K or V, or the scales of a group
@@ -1066,8 +1090,8 @@ __global__ void __launch_bounds__(64 * WW, 2) attention_wide_kernel(AttnParams p
 #pragma unroll
         for (int j = 0; j < 2 * NK; ++j) fr[j] = buf[(set * 2 * NK + j) * 64 + lane];
       };
-      // Rows that see a NaN or infinite value of V get NaN there (the rebuilt fragments hold zeros in its place):
-      // the product of such values' flags, from the raw codes, with the flags of seen tokens is positive.
+      // Rows that see a NaN or infinite value of V get it added there (the rebuilt fragments hold zeros in its place),
+      // from the raw codes (flag_rows).
       auto poison = [&](int i, int set, const uint32_t (&sees)[MT]) {
         const uint8_t* st = ring + (i % STAGES) * W::STAGE;
 #pragma unroll
@@ -1132,11 +1156,10 @@ __global__ void __launch_bounds__(64 * WW, 2) attention_wide_kernel(AttnParams p
 #pragma unroll
           for (int k = 0; k < ND; ++k) fr[k] = vf[k * 64];
           __builtin_amdgcn_sched_barrier(0);
+          uint32_t sees[MT] = {};
           if (__builtin_expect(special, 0)) {
-            uint32_t sees[MT];
             const int* pg = table + ((t - tbase) >> 4);
             mask_scores<MT>(p, b, m0 + r16, here, prefix, t + q4 * 4, existing(t + q4 * 4, len, pg[0], pg[1]), s, sees);
-            if (__builtin_amdgcn_readfirstlane(spoiled[i % 3][set])) poison(i, set, sees);
           }
           if (set == 0 && i + 1 < uz) rebuild(i + 1, raw, frags[(i + 1) & 1]);
           bf16x8_t pf[MT];
@@ -1144,12 +1167,14 @@ __global__ void __launch_bounds__(64 * WW, 2) attention_wide_kernel(AttnParams p
 #pragma unroll
             for (int k = 0; k < ND; ++k) o[mt][k] *= f;
           });
+          // (after the rescaling, which would make a NaN of an infinity)
+          if (__builtin_expect(special, 0) && __builtin_amdgcn_readfirstlane(spoiled[i % 3][set])) poison(i, set, sees);
           if (set + 1 < W::SETS) {
             ask_k(buf, set + 1, kf);
           } else {
             landed(i + 3 < uz ? 1 : 0);             // all but tile i + 3's: tile i + 2 is there
             __syncthreads();
-            ask_k(frags[(i + 1) & 1], 0, kf);       // (after the last tile: not used)
+            if (!W::LATE_K) ask_k(frags[(i + 1) & 1], 0, kf);   // (after the last tile: not used)
           }
           __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -1157,6 +1182,10 @@ __global__ void __launch_bounds__(64 * WW, 2) attention_wide_kernel(AttnParams p
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
               o[mt][k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, fr[k]), pf[mt], o[mt][k], 0, 0, 0);
+          if (W::LATE_K) {
+            __builtin_amdgcn_sched_barrier(0);
+            ask_k(frags[(i + 1) & 1], 0, kf);
+          }
         }
       }
       uc = uz;
@@ -1164,7 +1193,7 @@ __global__ void __launch_bounds__(64 * WW, 2) attention_wide_kernel(AttnParams p
 
     const bool whole = ua == 0 && ub == units;
     const int64_t slot = (int64_t)blockIdx.x * 2 + (u == first_u ? 0 : 1);
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0 && !p.direct) {
       int2* own = p.owners + ((int64_t)b * p.hkv + h) * p.mblocks + mb;
       if (ua == 0) own->x = (int)slot;
       if (ub == units) own->y = blockIdx.x;
@@ -1220,7 +1249,10 @@ AttnPlan attention_plan(const AttentionArgs& a) {
   const bool small = a.cache.dim <= 128;
   AttnPlan p;
   const int narrow = small ? 3 : 2;                 // blocks of 16 rows that a wave of the ring kernel holds
-  p.wide = rows > narrow * 16;
+  // the ring kernel takes up to two of its blocks of rows, though it reads keys and values twice then: 16 sequences of
+  // 4096 positions, 4 heads, 64 rows: 26 against 33 us at dim 64, 38 against 45 at 128, 58 against 62 at 192, 71 against
+  // 77 at 256 (three blocks, 96 rows at dim 256: 99 against 79; 144 rows at dim 64: 38 against 45)
+  p.wide = rows > narrow * 16 * 2;
   const int64_t step = p.wide ? WW * 16 : 16, most = p.wide ? (a.cache.dim == 64 ? 3 : small ? 2 : 1) : narrow;
   const int64_t blocks = (rows + step * most - 1) / (step * most);
   p.mt = (int)((rows + step * blocks - 1) / (step * blocks));
@@ -1230,18 +1262,27 @@ AttnPlan attention_plan(const AttentionArgs& a) {
   const int64_t units = a.B * a.cache.heads * p.mblocks * ((a.max_len + (1 << p.unit_shift) - 1) >> p.unit_shift);
   const int64_t grid = p.wide ? 256 : ring_grid((int)a.cache.dim, p.mt);
   const int64_t items = a.B * a.cache.heads * p.mblocks;
-  // short contexts: a workgroup for each item, nothing to join (one sequence of 128 tokens, 16 heads over 2 of dim 64:
-  // 7.7 against 10.0 us; even at 512 tokens, at 1023 13.0 against 11.0; twice the work a token above dim 128)
-  p.direct = !p.wide && a.max_len <= (small ? 512 : 256);
+  // short contexts: a workgroup for each item, nothing to join (one sequence, 16 heads over 2 of dim 64: at 128 positions
+  // 7.7 against 10.0 us, at 1023 13.0 against 11.0; 59 nodes, 14 heads over 2 of dim 128: at 128 positions 16.4 against
+  // 19.6, at 512 29.6 against 22.0)
+  p.direct = a.max_len <= (small ? 512 : 256) / (p.wide ? 2 : 1);
   if (p.direct) {
     p.nwg = (int)items;
     p.start_cost = 0;
     return p;
   }
-  p.nwg = (int)(units < 1 ? 1 : units > grid ? grid : units);
-  // beginning an item costs about as long as half a kilobyte-wide unit's 128 tokens take (13 us against 2.9 us
-  // a unit at dim 128 and 48 rows); with few units a workgroup has no second item
-  p.start_cost = units > 4 * grid ? (int)(512 / a.cache.dim) : 0;
+  // Units of a run: with n workgroups it costs about t units / n (t = 1 us, wide 2) to compute them, and to write and
+  // read back n partial results at 4 TB/s and 35 ns for each of an item's in the join; the least sum. (One token over
+  // 131072 positions, 8 heads over 1: 25 us, with runs of one unit 40; 59 nodes over 1024, 14 heads over 2: 24 against 30.)
+  const double values = (double)((rows < p.br ? rows : p.br) * a.cache.dim);
+  const double joined = (double)units * (values * 2e-6 + 0.035 / (double)(items > 0 ? items : 1));
+  const double least = __builtin_sqrt(joined / (p.wide ? 2. : 1.));
+  const int64_t run = least < 1.5 ? 1 : (int64_t)(least + 0.5), runs = (units + run - 1) / run;
+  p.nwg = (int)(runs < 1 ? 1 : runs > grid ? grid : runs);
+  // beginning an item costs about as long as four units (32 chains of 6, ragged, 64 heads over 8 of dim 128: 77 us, with 0
+  // 96, with 8 81; 16 single tokens of dim 64: 26, 28 and 27; 24 x 3 nodes of dim 192: 56, 68 and - with 2 - 60); with few
+  // units a workgroup has no second item
+  p.start_cost = units > 4 * grid ? 4 : 0;
   return p;
 }
 
@@ -1265,6 +1306,7 @@ int ring(const AttnParams& p, hipStream_t stream) {
 template <int D, int MT>
 int wide(const AttnParams& p, hipStream_t stream) {
   hipLaunchKernelGGL((attention_wide_kernel<D, MT>), dim3((unsigned)p.nwg), dim3(64 * WW), 0, stream, p);
+  if (p.direct) return hip_status(hipGetLastError());
   return hipGetLastError() == hipSuccess ? join<D>(p, stream) : BSFP8_EHIP;
 }
 

@@ -397,7 +397,8 @@ BSFP8_API size_t bsfp8_attention_workspace_bytes(int64_t B, int64_t T, int64_t h
  *   scale : finite (BSFP8_EINVAL).
  *   out   : bf16 [B][T][hq][dim] (contiguous, 16-byte aligned). A node that sees nothing gets zeros.
  * Values of positions that a node does not see never reach it, also when they are NaN or infinite
- * (a rejected draft's leftovers, a page never written). hq is a multiple of cache->heads, at most
+ * (a rejected draft's leftovers, a page never written); those that it sees have the effect they have in the formula,
+ * values whose code times scale passes bf16 counting as infinite. hq is a multiple of cache->heads, at most
  * 64 times it; T >= 1; B * T * hq < 2^31, and fewer than 2^24 blocks of 16 rows (B times the key/value
  * heads times T * hq / heads / 16, rounded up). Scores and sums are fp32; the weights of one tile are
  * rounded to bf16 for the product with V (rebuilt exactly from its codes, as K is). The split of

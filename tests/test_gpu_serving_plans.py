@@ -1,0 +1,81 @@
+"""Attention of drafted tokens in each of its plans: a workgroup per item or runs that cut items, one or two row blocks of the
+ring kernel, the wide kernel, runs of several units; each with empty sequences, masks, absent pages and non-finite leftovers.
+The bound on the lengths (max_len) chooses between unsplit and split, the rows of a key/value head between the kernels."""
+import numpy as np
+import pytest
+import torch
+
+import block_scaled_fp8_skinny_amd as B
+from test_gpu_serving import attend, bf16, cache_of
+
+pytestmark = pytest.mark.gpu
+
+SPLIT = 6000                                                     # a bound that no unsplit plan has
+
+
+# (query heads of a key/value head, nodes): rows 3, 48, 60 and 96 (ring), 112 and 512 (wide)
+@pytest.mark.parametrize("g,T", [(1, 3), (8, 6), (10, 6), (16, 6), (16, 7), (8, 64)])
+@pytest.mark.parametrize("dim,page", [(64, 16), (128, 48), (192, 32), (256, 16)])
+@pytest.mark.parametrize("bound", [256, SPLIT])
+def test_short_sequences(g, T, dim, page, bound):
+    lens = [0, 1, 33, 128, 250, T]
+    attend(100 + g, T, 2 * g, 2, dim, page, lens, nodes=[T, 1, T, T - 1, 0, T], tree=True, max_len=bound)
+    attend(101 + g, T, g, 1, dim, page, lens, max_len=bound)
+
+
+@pytest.mark.parametrize("T,hq,hkv,dim,lens", [
+    (1, 8, 1, 128, [20000]), (1, 2, 1, 64, [30000, 0]), (15, 4, 1, 128, [9000]), (13, 10, 1, 64, [7001, 5]),
+    (5, 32, 1, 256, [3001, 64]), (6, 28, 1, 192, [2500])])
+def test_runs_of_several_units(T, hq, hkv, dim, lens):
+    attend(120, T, hq, hkv, dim, 64, lens, tree=T > 1)
+
+
+@pytest.mark.parametrize("g", [12, 40])
+def test_scores_that_move_the_reference(g):
+    attend(130, 6, g, 1, 128, 32, [700, 64], scale=4.0)
+    attend(131, 6, g, 1, 64, 32, [700, 64], scale=-5.0, tree=True)
+
+
+@pytest.mark.parametrize("bound", [128, SPLIT])
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+def test_absent_pages_of_many_rows(dim, bound):
+    def table(pages, n):
+        pages[0, 1], pages[1, 0], pages[2, :] = -1, n, 2 ** 30
+    for g in (16, 40):
+        attend(140, 6, g, 1, dim, 16, [100, 50, 40], table=table, tree=True, max_len=bound)
+
+
+@pytest.mark.parametrize("bound", [128, SPLIT])
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+def test_nonfinite_leftovers_with_many_rows(dim, bound):
+    def spoil(cache, K, V, pages):
+        for t in (cache.kq, cache.vq):
+            t[int(pages[0, 2]), :, 8:] = 0xFF                    # positions 40.. of sequence 0 (41 long): node 5 and the rest
+        cache.ks[int(pages[1, 0]), :, 14] = 255                  # position 14 of sequence 1: its node 2 of 4
+        cache.vs[int(pages[1, 0]), :, 14] = 255
+        for x in (K, V):
+            x[int(pages[0, 2]) * 16 + 8: int(pages[0, 2]) * 16 + 16] = np.nan
+            x[int(pages[1, 0]) * 16 + 14] = np.nan
+    for g in (14, 40):
+        out = attend(150, 6, g, 1, dim, 16, [41, 16], nodes=[6, 4], spoil=spoil, max_len=bound)
+        assert out[0, 5].isnan().all() and not out[0, :5].isnan().any()
+        assert out[1, 2:4].isnan().all() and not out[1, :2].isnan().any() and not out[1, 4:].any()
+
+
+@pytest.mark.parametrize("bound", [64, SPLIT])
+@pytest.mark.parametrize("g", [1, 40])
+def test_values_that_pass_bf16(g, bound):
+    """A scale byte of 254 makes codes of 448 infinite in bf16: rows that do not see the token stay finite, those that do
+    get the infinity, and NaN where infinities of both signs meet."""
+    T, dim, page, n = 4, 128, 16, 20
+    r = np.random.default_rng(160)
+    cache, _, _ = cache_of(r, 2, 1, page, dim, special=False)
+    cache.vq[1, 0, 2:4] = 0x7E                                   # positions 18 and 19 of 20: nodes 2 and 3, codes of 448
+    cache.vs[1, 0, 2:4] = 254
+    cache.vq[1, 0, 3, 64:] = 0xFE                                # the second half of node 3's are negative
+    q, _ = bf16(r, (1, T, g, dim), 0.1)
+    pages, lens = torch.tensor([[0, 1]], dtype=torch.int32).cuda(), torch.tensor([n], dtype=torch.int32).cuda()
+    out = B.bsfp8_tree_attention(q, cache, pages, lens, max_len=bound)
+    assert out[0, :2].isfinite().all()
+    assert (out[0, 2:, :, :64] == float("inf")).all() and (out[0, 2, :, 64:] == float("inf")).all()
+    assert out[0, 3, :, 64:].isnan().all()
