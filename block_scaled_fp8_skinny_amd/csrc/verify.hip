@@ -38,9 +38,10 @@ struct VerifyParams {
   const float *temperature, *u, *u_sample;
   int* counters;                                    // [B], zero between calls
   Pair* pairs;                                      // [rows][pieces]: the target's rows, then the draft's
-  double* rest;                                     // [B][pieces][vectors]: residual sums of a refused row; a tree's sampled tokens [B][T]
+  double* rest;                                     // [B][pieces][vectors]: sums of a refused row; a tree's tokens [B][T]
   int32_t *out_tokens, *path, *n_accepted;
   int B, T, V, pieces;
+  int share;                                        // vectors of a refused row that a wave sums: 1, or a whole piece's
 };
 
 // The element type's 16-byte vectors, and how many a piece has per lane.
@@ -540,19 +541,21 @@ __global__ void __launch_bounds__(256, 4) verify_chain_kernel(VerifyParams p) {
     const Residual<T> res(p, prow, (int64_t)b * D + n, tp, totals[p.T + n], it, powers);
     constexpr int E = Vec<T>::E, N = Vec<T>::N;
     double* rest = p.rest + (int64_t)b * p.pieces * N;   // a sum for every vector
-    const int piece = blockIdx.y * 4 + wave;
+    const int at0 = (blockIdx.y * 4 + wave) * p.share, piece = at0 / N, v0 = at0 % N;
     if (piece < p.pieces) {
       u32x4_t a[N], c[N];
 #pragma unroll
-      for (int v = 0; v < N; ++v) res.load(piece, lane, v, a[v], c[v]);
+      for (int v = 0; v < N; ++v)
+        if (v < p.share) res.load(piece, lane, v0 + v, a[v], c[v]);
 #pragma unroll
       for (int v = 0; v < N; ++v) {
+        if (v >= p.share) break;
         double w[E], s = 0;
-        res.get(a[v], c[v], piece, lane, v, w);
+        res.get(a[v], c[v], piece, lane, v0 + v, w);
 #pragma unroll
         for (int i = 0; i < E; ++i) s += w[i];
         s = wave_sum(s);
-        if (lane == 0) __hip_atomic_store(rest + piece * N + v, s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (lane == 0) __hip_atomic_store(rest + at0 + v, s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
     }
     if (!last_to_arrive(p.counters + b, gridDim.y, &shared_last) || wave != 0) return;
@@ -699,6 +702,12 @@ int launch_verify(const VerifyArgs& a, bool tree, hipStream_t stream) {
   p.pairs = reinterpret_cast<Pair*>(ws);
   ws += align256((size_t)a.B * (2 * a.T - 1) * p.pieces * sizeof(Pair));
   p.rest = reinterpret_cast<double*>(ws);
+  // A refused row's second look by a wave for each vector while that keeps every workgroup in one round of the GPU (four
+  // per CU): one chain over 32768 columns 11.7 us, by a wave for each piece 13.4; else a piece, since every workgroup
+  // repeats the acceptance tests.
+  const int vectors = a.f32 ? Vec<float>::N : Vec<uint16_t>::N;
+  p.share = (int64_t)a.B * ((p.pieces * vectors + 3) / 4) <= 1024 ? 1 : vectors;
+  const unsigned shares = (unsigned)((p.pieces * (vectors / p.share) + 3) / 4);
   const unsigned blocks = (unsigned)((p.pieces + 3) / 4);
   const unsigned rows = (unsigned)(tree ? a.B * a.T : a.B * (2 * a.T - 1));
   if (a.f32)
@@ -711,9 +720,9 @@ int launch_verify(const VerifyArgs& a, bool tree, hipStream_t stream) {
   else if (tree)
     hipLaunchKernelGGL(verify_tree_kernel<uint16_t>, dim3((unsigned)a.B, (unsigned)((a.T + 3) / 4)), dim3(256), 0, stream, p);
   else if (a.f32)
-    hipLaunchKernelGGL(verify_chain_kernel<float>, dim3((unsigned)a.B, blocks), dim3(256), 0, stream, p);
+    hipLaunchKernelGGL(verify_chain_kernel<float>, dim3((unsigned)a.B, shares), dim3(256), 0, stream, p);
   else
-    hipLaunchKernelGGL(verify_chain_kernel<uint16_t>, dim3((unsigned)a.B, blocks), dim3(256), 0, stream, p);
+    hipLaunchKernelGGL(verify_chain_kernel<uint16_t>, dim3((unsigned)a.B, shares), dim3(256), 0, stream, p);
   return hip_status(hipGetLastError());
 }
 
