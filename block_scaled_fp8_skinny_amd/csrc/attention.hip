@@ -1263,9 +1263,9 @@ AttnPlan attention_plan(const AttentionArgs& a) {
   const int64_t grid = p.wide ? 256 : ring_grid((int)a.cache.dim, p.mt);
   const int64_t items = a.B * a.cache.heads * p.mblocks;
   // short contexts: a workgroup for each item, nothing to join (one sequence, 16 heads over 2 of dim 64: at 128 positions
-  // 7.7 against 10.0 us, at 1023 13.0 against 11.0; 59 nodes, 14 heads over 2 of dim 128: at 128 positions 16.4 against
-  // 19.6, at 512 29.6 against 22.0)
-  p.direct = a.max_len <= (small ? 512 : 256) / (p.wide ? 2 : 1);
+  // 6.8 against 9.2 us, at 1024 11.5 against 10.2; 40 nodes, 16 heads over 4 of dim 128: at 128 positions 14.9 against
+  // 17.6, at 256 19.3 against 17.8)
+  p.direct = a.max_len <= (p.wide ? (a.cache.dim == 64 ? 256 : 128) : small ? 512 : 256);
   if (p.direct) {
     p.nwg = (int)items;
     p.start_cost = 0;
