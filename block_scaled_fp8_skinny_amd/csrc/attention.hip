@@ -967,10 +967,13 @@ __global__ void __launch_bounds__(64 * WW, 2) attention_wide_kernel(AttnParams p
       auto issue = [&](int i) {
         uint8_t* st = ring + (i % STAGES) * W::STAGE;
         const int* en = table + (i - uc) * W::GROUPS;
+        int entry[MY];                              // read together, before the loads that each needs one
+#pragma unroll
+        for (int k = 0; k < MY; ++k) entry[k] = en[my[k].group < W::GROUPS ? my[k].group : 0];
 #pragma unroll
         for (int k = 0; k < MY; ++k) {
           if (wave + k * WW >= W::LOADS) break;
-          const int64_t at = max(__builtin_amdgcn_readfirstlane(en[my[k].group]), 0);   // absent: some group, not used
+          const int64_t at = max(__builtin_amdgcn_readfirstlane(entry[k]), 0);   // absent: some group, not used
           if (k < W::CL / WW || wave + k * WW < W::CL)
             gload_lds16<1>(my[k].base + at * (16 * D), &my[k].off, lds_addr(st + my[k].lds));
           else if (lane < D / 8)
