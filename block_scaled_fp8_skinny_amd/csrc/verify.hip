@@ -69,18 +69,25 @@ constexpr float NEG_INF = -__builtin_inff();
 // A wave's view of one row of V elements. Rows start anywhere, so the row is addressed in 16-byte
 // words from the word that holds its first element: word w, element i is row element w * E + i - lead,
 // and elements outside [0, V) (the neighbouring rows') read as -inf. The descriptor ends with the
-// row's last 4-byte word, so nothing past it is read.
+// row's last whole 4-byte word, so nothing past the row is read; a bf16 row's last element in half a word
+// is read by itself.
 template <typename T>
 struct Row {
   static constexpr int E = Vec<T>::E, N = Vec<T>::N;
   __amdgpu_buffer_rsrc_t r;
   int lead, V;
-  __device__ __forceinline__ Row(const void* base, int64_t row, int V_) : V(V_) {
+  bool half;
+  float last;
+  __device__ __forceinline__ Row(const void* base, int64_t row, int V_) : V(V_), half(false), last(0.f) {
     const int64_t first = row * V_;
+    const T* const at = reinterpret_cast<const T*>(base) + first;
     lead = (int)(first & (E - 1));
-    const int64_t bytes = ((int64_t)(lead + V_) * (int64_t)sizeof(T) + 3) & ~(int64_t)3;
-    r = __builtin_amdgcn_make_buffer_rsrc((void*)(reinterpret_cast<const T*>(base) + (first - lead)), 0, (int)bytes,
-                                          RSRC_WORD3);
+    const int64_t bytes = (int64_t)(lead + V_) * (int64_t)sizeof(T) & ~(int64_t)3;
+    r = __builtin_amdgcn_make_buffer_rsrc((void*)(at - lead), 0, (int)bytes, RSRC_WORD3);
+    if constexpr (sizeof(T) == 2) {
+      half = (lead + V_) & 1;
+      if (half) last = __uint_as_float((uint32_t)at[V_ - 1] << 16);
+    }
   }
   __device__ __forceinline__ u32x4_t load(int piece, int lane, int v) const {
     return __builtin_amdgcn_raw_buffer_load_b128(r, (piece * (PIECE / E) + v * 64 + lane) * 16, 0, 0);
@@ -98,7 +105,7 @@ struct Row {
     if (piece * PIECE < lead || (piece + 1) * PIECE > V + lead) {   // the row's ends (uniform)
       const int at = index(piece, lane, v, 0);
 #pragma unroll
-      for (int i = 0; i < E; ++i) x[i] = (unsigned)(at + i) < (unsigned)V ? x[i] : NEG_INF;
+      for (int i = 0; i < E; ++i) x[i] = half && at + i == V - 1 ? last : (unsigned)(at + i) < (unsigned)V ? x[i] : NEG_INF;
     }
   }
   __device__ __forceinline__ void get(const u32x4_t (&w)[N], int piece, int lane, float (&x)[N][E]) const {

@@ -427,7 +427,6 @@ BSFP8_API size_t bsfp8_verify_workspace_bytes(int64_t B, int64_t T, int64_t V);
  * p_{T-1} when all were accepted. With t = 0 (greedy; also t < 0 or NaN) x_i is accepted if it is
  * the lowest index of the largest logit of row i, and the next token is that of row n.
  *   logits : [B][T][V], draft : [B][T-1][V], of `dtype` (bsfp8_logits), contiguous, 16-byte aligned.
- *            bf16 rows of an odd total are read to the end of their last 4-byte word.
  *   tokens : int32_t [B][T-1]; one outside [0, V) is refused. temperature: float [B]; u: float
  *            [B][T-1]; u_sample: float [B], uniform in [0, 1) (all device; the draft arrays may be NULL
  *            when T = 1).

@@ -79,3 +79,24 @@ def test_values_that_pass_bf16(g, bound):
     assert out[0, :2].isfinite().all()
     assert (out[0, 2:, :, :64] == float("inf")).all() and (out[0, 2, :, 64:] == float("inf")).all()
     assert out[0, 3, :, 64:].isnan().all()
+
+
+def test_verify_reads_nothing_past_an_odd_bf16_tensor():
+    """Logits of an odd number of bf16 values whose neighbour in memory would win every row: it is not read, and the row's
+    last element, alone in its 4-byte word, is."""
+    for Bn, T, V in ((1, 3, 1001), (3, 1, 5), (1, 1, 2049)):
+        n = Bn * T * V
+        room = torch.zeros(n + 1, dtype=torch.bfloat16, device="cuda")
+        room[n] = 1000
+        lg = room[:n].view(Bn, T, V)
+        for last in (0, 7):
+            lg[-1, -1, -1] = last
+            u = torch.full((Bn, T), 0.5, device="cuda")
+            t = torch.zeros(Bn, device="cuda")
+            tok = torch.zeros(Bn, T, dtype=torch.int32, device="cuda")
+            par = torch.arange(-1, T - 1, device="cuda").to(torch.int32).expand(Bn, T).contiguous()
+            out, path, k = B.bsfp8_verify_tree(lg, tok, par, t, u)
+            assert (out[:-1] == 0).all() and (out[-1, :-1] == 0).all() and int(out[-1, -1]) == (V - 1 if last else 0)
+            if T == 1:
+                out, k = B.bsfp8_verify_chain(lg, None, None, t, None, u[:, 0].contiguous())
+                assert (out[:-1] == 0).all() and int(out[-1, 0]) == (V - 1 if last else 0)
