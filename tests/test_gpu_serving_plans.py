@@ -100,3 +100,27 @@ def test_verify_reads_nothing_past_an_odd_bf16_tensor():
             if T == 1:
                 out, k = B.bsfp8_verify_chain(lg, None, None, t, None, u[:, 0].contiguous())
                 assert (out[:-1] == 0).all() and int(out[-1, 0]) == (V - 1 if last else 0)
+
+
+def test_cache_past_4_gib():
+    """Offsets inside a cache of 4.6 GB of codes: its last pages give bit for bit what a small cache of theirs gives, in the
+    write, the read and both attention kernels."""
+    heads, page, dim, n = 8, 64, 128, 70000
+    big, small = B.KVCache.empty(n, heads, page, dim), B.KVCache.empty(4, heads, page, dim)
+    r = np.random.default_rng(170)
+    k, _ = bf16(r, (200, heads * dim))
+    v, _ = bf16(r, (200, heads * dim))
+    at = torch.arange(200, device="cuda")
+    B.bsfp8_cache_write(small, at, k, v)
+    B.bsfp8_cache_write(big, at + (n - 4) * page, k, v)
+    for a, b in ((big.kq, small.kq), (big.ks, small.ks), (big.vq, small.vq), (big.vs, small.vs)):
+        assert torch.equal(a[-4:], b)
+    for a, b in zip(B.bsfp8_cache_read(big, at + (n - 4) * page), B.bsfp8_cache_read(small, at)):
+        assert torch.equal(a, b)
+    pages = torch.arange(4, device="cuda", dtype=torch.int32)[None]
+    lens = torch.tensor([200], dtype=torch.int32).cuda()
+    for T, g, bound in ((1, 1, 256), (6, 8, SPLIT), (20, 8, SPLIT)):
+        q, _ = bf16(r, (1, T, heads * g, dim))
+        a = B.bsfp8_tree_attention(q, big, pages + (n - 4), lens, max_len=bound)
+        b = B.bsfp8_tree_attention(q, small, pages, lens, max_len=bound)
+        assert torch.equal(a, b) and a.abs().sum() > 0
