@@ -1265,15 +1265,6 @@ AttnPlan attention_plan(const AttentionArgs& a) {
   const int64_t units = a.B * a.cache.heads * p.mblocks * ((a.max_len + (1 << p.unit_shift) - 1) >> p.unit_shift);
   const int64_t grid = p.wide ? 256 : ring_grid((int)a.cache.dim, p.mt);
   const int64_t items = a.B * a.cache.heads * p.mblocks;
-  // short contexts: a workgroup for each item, nothing to join (one sequence, 16 heads over 2 of dim 64: at 128 positions
-  // 6.8 against 9.2 us, at 1024 11.5 against 10.2; 40 nodes, 16 heads over 4 of dim 128: at 128 positions 14.9 against
-  // 17.6, at 256 19.3 against 17.8)
-  p.direct = a.max_len <= (p.wide ? (a.cache.dim == 64 ? 256 : 128) : small ? 512 : 256);
-  if (p.direct) {
-    p.nwg = (int)items;
-    p.start_cost = 0;
-    return p;
-  }
   // Units of a run: with n workgroups it costs about t units / n (t = 1 us, wide 2) to compute them, and to write and
   // read back n partial results at 4 TB/s and 35 ns for each of an item's in the join; the least sum. (One token over
   // 131072 positions, 8 heads over 1: 25 us, with runs of one unit 40; 59 nodes over 1024, 14 heads over 2: 24 against 30.)
@@ -1282,6 +1273,17 @@ AttnPlan attention_plan(const AttentionArgs& a) {
   const double least = __builtin_sqrt(joined / (p.wide ? 2. : 1.));
   const int64_t run = least < 1.5 ? 1 : (int64_t)(least + 0.5), runs = (units + run - 1) / run;
   p.nwg = (int)(runs < 1 ? 1 : runs > grid ? grid : runs);
+  // short contexts: a workgroup for each item, nothing to join (one sequence, 16 heads over 2 of dim 64: at 128 positions
+  // 6.8 against 9.2 us, at 1024 11.5 against 10.2; 40 nodes, 16 heads over 4 of dim 128: at 128 positions 14.9 against
+  // 17.6, at 256 19.3 against 17.8); longer ones where runs are longer than a unit, up to four (28 sequences of 275
+  // positions, 53 nodes, 56 heads over 8 of dim 64: 27 against 52 us)
+  const int64_t bound = p.wide ? (a.cache.dim == 64 ? 256 : 128) : small ? 512 : 256;
+  p.direct = a.max_len <= bound + ((run < 4 ? run : 4) - 1) * ((int64_t)1 << p.unit_shift);
+  if (p.direct) {
+    p.nwg = (int)items;
+    p.start_cost = 0;
+    return p;
+  }
   // beginning an item costs about as long as four units (32 chains of 6, ragged, 64 heads over 8 of dim 128: 77 us, with 0
   // 96, with 8 81; 16 single tokens of dim 64: 26, 28 and 27; 24 x 3 nodes of dim 192: 56, 68 and - with 2 - 60); with few
   // units a workgroup has no second item

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import block_scaled_fp8_skinny_amd as B
+import test_gpu_serving as base
 from test_gpu_serving import attend, bf16, cache_of
 
 pytestmark = pytest.mark.gpu
@@ -100,6 +101,14 @@ def test_verify_reads_nothing_past_an_odd_bf16_tensor():
             if T == 1:
                 out, k = B.bsfp8_verify_chain(lg, None, None, t, None, u[:, 0].contiguous())
                 assert (out[:-1] == 0).all() and int(out[-1, 0]) == (V - 1 if last else 0)
+
+
+# tokens of few heads that share a workgroup, the last workgroup not full: rows, hq, hkv, dim, page, norm, rot, interleaved
+@pytest.mark.parametrize("case", [(2051, 3, 1, 64, 16, True, 64, False), (2050, 1, 2, 128, 48, True, 32, True),
+                                  (2049, 0, 1, 192, 16, True, 96, False), (2053, 2, 1, 256, 32, False, 256, True),
+                                  (2047, 3, 1, 64, 16, True, 64, False)], ids=str)
+def test_write_of_few_heads(case):
+    base.test_write(case)
 
 
 def test_cache_past_4_gib():
