@@ -1,6 +1,6 @@
 // Attention of drafted tokens over the paged MXFP8 cache for gfx950 (MI355X).
 //
-// One kernel for decoding (one token a sequence), chains and trees. The rows of one key/value head
+// Decoding (one token a sequence), chains and trees alike. The rows of one key/value head
 // are its (node, query head) pairs, g * T of them (g query heads share it). With s = q . k * scale in
 // base 2 (scale * log2 e), a running reference m per row, and weights w = 2^(s - m):
 //   l = sum w,  O = sum w V,  out = O / l,
@@ -20,7 +20,7 @@
 //   ring  up to 96 rows (64 above dim 128): a workgroup's waves share 16 to 48 rows and split their tokens in tiles of 32,
 //         each wave with a ring of NS tiles in LDS that the LDS mode of global loads fills (codes are contiguous per 16
 //         tokens of a page and head); waves only wait for their own loads, and are joined through LDS at an item's end.
-//         Bound by HBM: the loop of a chain of 6 over 131072 positions (64 heads over 8 of dim 128) streams 6.2 TB/s; 75 us
+//         Bound by HBM: the loop of a chain of 6 over 131072 positions (64 heads over 8 of dim 128) streams 6.2 TB/s; 71 us
 //         in all, of which 5 go before the first tile is asked for, 10 to the waves' skew and join, 5 to the joining kernel.
 //   wide  more rows: the waves split the rows and share the tokens, which are rebuilt once per workgroup (see there).
 // Work is cut evenly over the grid: the units (the tokens that a workgroup's waves take in one step, of one head and row
@@ -860,7 +860,7 @@ __global__ void __launch_bounds__(256) attention_join_kernel(AttnParams p, int j
 // into operand order, also in LDS (a fragment of one MFMA is 64 lanes x 16 bytes, read back without bank
 // conflicts), two buffers deep: while a tile is computed, the next one is rebuilt, a unit of K and one of V
 // by each wave. The operand order of V is value c * 64 + x * 4 + k for column x of 16-row tile 4c + k.
-// Trees of 64 nodes over 16384 positions of 4 sequences, 64 heads over 8 of dim 128 (137 GFLOP): 177 us, 0.78 PFLOP/s.
+// Trees of 64 nodes over 16384 positions of 4 sequences, 64 heads over 8 of dim 128 (137 GFLOP): 176 us, 0.78 PFLOP/s.
 // Counters: matrix cores busy 33% of the time, vector ALUs 45%, LDS 28%; two waves a SIMD overlap them little (all the
 // registers are taken at 32 rows a wave). Taking turns by halves, products against softmax with a barrier after each
 // phase, was slower (217 us), as was rebuilding V in half the waves and K in the others (180).

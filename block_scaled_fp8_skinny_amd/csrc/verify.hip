@@ -16,8 +16,8 @@
 //           sequence, left at zero) picks the token. Otherwise the sequence's first workgroup picks.
 //   tree    one wave per node samples its token; the sequence's last workgroup walks down.
 // Times: 32 chains of 6 over 131072 columns, 36 us for the pairs (184 MB at 5.1 TB/s, the vector ALUs 81% busy with the
-// exponentials) and 18 for the rest, of which 10 are its chain of dependent loads (a single chain takes as long) and the
-// others the second look at the refused rows; 16 trees of 32 nodes over 32768 columns 15 and 6.7 us.
+// exponentials) and 18 for the rest, of which 8 are its chain of dependent loads (a single chain's 8.6) and the others
+// the second look at the refused rows; 16 trees of 32 nodes over 32768 columns 15 and 6.7 us.
 #include "device.h"
 
 namespace bsfp8 {
