@@ -827,8 +827,8 @@ def bsfp8_verify_workspace_bytes(B, T, V):
 
 
 def workspace_verify(B, T, V, device="cuda"):
-    """A zero-filled workspace tensor for the verification calls with these sizes."""
-    return torch.zeros(bsfp8_verify_workspace_bytes(B, T, V), dtype=torch.uint8, device=device)
+    """A workspace tensor for the verification calls with these sizes or smaller ones (its contents need no clearing)."""
+    return torch.empty(bsfp8_verify_workspace_bytes(B, T, V), dtype=torch.uint8, device=device)
 
 
 def _verify_args(logits, ws, out_tokens, n_accepted):

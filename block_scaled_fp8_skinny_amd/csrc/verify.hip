@@ -13,7 +13,7 @@
 // Two launches, the second starting from the pairs:
 //   chain   every workgroup of a sequence repeats the few acceptance tests; after a refusal each wave
 //           sums max(p - q, 0) over its piece, and the workgroup that arrives last (a counter per
-//           sequence, left at zero) picks the token. Otherwise the sequence's first workgroup picks.
+//           sequence, zeroed by the first launch) picks the token. Otherwise the sequence's first workgroup picks.
 //   tree    one wave per node samples its token; the sequence's last workgroup walks down.
 // Times: 32 chains of 6 over 131072 columns, 36 us for the pairs (184 MB at 5.1 TB/s, the vector ALUs 81% busy with the
 // exponentials) and 18 for the rest, of which 8 are its chain of dependent loads (a single chain's 8.6) and the others
@@ -36,7 +36,7 @@ struct VerifyParams {
   const void *logits, *draft;
   const int32_t *tokens, *parents;
   const float *temperature, *u, *u_sample;
-  int* counters;                                    // [B], zero between calls
+  int* counters;                                    // [B]: workgroups of the second launch that have arrived
   Pair* pairs;                                      // [rows][pieces]: the target's rows, then the draft's
   double* rest;                                     // [B][pieces][vectors]: sums of a refused row; a tree's tokens [B][T]
   int32_t *out_tokens, *path, *n_accepted;
@@ -230,6 +230,8 @@ __global__ void __launch_bounds__(256) verify_pairs_kernel(VerifyParams p) {
   const int lane = threadIdx.x & 63;
   const int piece = blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row = blockIdx.x, targets = p.B * p.T;
+  // (not left at zero by the last call instead: where they lie depends on its sizes)
+  if (row < p.B && blockIdx.y == 0 && threadIdx.x == 0) p.counters[row] = 0;
   const bool is_draft = row >= targets;
   const int local = is_draft ? row - targets : row;
   const Row<T> r(is_draft ? p.draft : p.logits, local, p.V);
@@ -453,18 +455,15 @@ struct Residual {
 };
 
 // The arrival of a workgroup at a sequence's counter: true for the last of `n`, which sees what the others
-// stored before theirs, and leaves the counter at zero (whole workgroup). What is handed over is stored and
+// stored before theirs (whole workgroup). What is handed over is stored and
 // loaded by relaxed device-scope atomics only, which pass the XCDs' L2s by, so it is enough that each wave
 // waits for its stores' completion before the count: a release fence would also write back the whole L2 of
 // the XCD, once per workgroup (32 sequences' chains over 131072 columns took 57 us with it).
 __device__ __forceinline__ bool last_to_arrive(int* counter, int n, int* shared) {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
-  if (threadIdx.x == 0) {
-    const int last = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == n - 1;
-    if (last) __hip_atomic_store(counter, 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    *shared = last;
-  }
+  if (threadIdx.x == 0)
+    *shared = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == n - 1;
   __syncthreads();
   return *shared != 0;
 }

@@ -414,9 +414,9 @@ typedef enum bsfp8_logits {
   BSFP8_LOGITS_F32 = 1
 } bsfp8_logits;
 
-/* Workspace bytes of the verification calls (0 for sizes they refuse). ZERO-FILLED once after
- * allocation; every call leaves its counters at zero. Not for two calls that can run at the same
- * time. */
+/* Workspace bytes of the verification calls (0 for sizes they refuse; never more for smaller sizes). The
+ * contents need no clearing: calls of any sizes may use it one after another. Not for two calls that can
+ * run at the same time. */
 BSFP8_API size_t bsfp8_verify_workspace_bytes(int64_t B, int64_t T, int64_t V);
 
 /* Verification of a chain of T - 1 drafted tokens per sequence. With p_i = softmax(logits[b][i] / t)

@@ -1,0 +1,55 @@
+"""Verification of drafts where a batch, a row's place in memory or a row's values are out of the ordinary. Equality with
+oracle/serving.py throughout."""
+import numpy as np
+import pytest
+import torch
+
+import block_scaled_fp8_skinny_amd as B
+import oracle.serving as SV
+from test_gpu_serving import _check_chain, _logits, f64
+
+pytestmark = pytest.mark.gpu
+
+TYPES = pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+
+
+def check_tree(lg, tok, par, t, u, ws=None):
+    print("tree", tuple(lg.shape), lg.dtype, flush=True)
+    dev = lambda a, d: torch.from_numpy(np.ascontiguousarray(a, d)).cuda()
+    out, path, n = B.bsfp8_verify_tree(lg, dev(tok, np.int32), dev(par, np.int32), dev(t, np.float32), dev(u, np.float32), ws=ws)
+    for b in range(lg.shape[0]):
+        wo, wp, wn = SV.verify_tree(f64(lg[b]), tok[b], par[b], float(np.float32(t[b])), np.float32(u[b]).astype(np.float64))
+        assert int(n[b]) == wn and np.array_equal(path[b].cpu().numpy(), wp) and np.array_equal(out[b].cpu().numpy(), wo), b
+    return out, path, n
+
+
+def random_tree(r, lg, t, u):
+    """Parents, and tokens of which half are what their parents sample."""
+    Bn, T, V = lg.shape
+    par, tok = np.full((Bn, T), -1), np.zeros((Bn, T), np.int64)
+    for b in range(Bn):
+        for i in range(1, T):
+            p = par[b, i] = r.integers(0, i)
+            own = SV.pick(SV.probabilities(f64(lg[b, p]), float(np.float32(t[b]))), float(np.float32(u[b, p])))
+            tok[b, i] = own if r.random() < 0.5 else r.integers(0, V)
+    return tok, par
+
+
+# ------------------------------------------------------------------------------------------------
+# one workspace, many batches
+# ------------------------------------------------------------------------------------------------
+@pytest.mark.parametrize("V", [1001, 4096])
+def test_one_workspace_serves_every_batch(V):
+    """A workspace of the largest size, its contents whatever they were, through calls of small and large batches."""
+    r = np.random.default_rng(V)
+    T, most = 4, 100
+    ws = torch.full((B.bsfp8_verify_workspace_bytes(most, T, V),), 0xFF, dtype=torch.uint8, device="cuda")
+    for Bn in (8, most, 65, 8, most):
+        lg, dr = _logits(r, (Bn, T, V), torch.float32), _logits(r, (Bn, T - 1, V), torch.float32)
+        t = r.uniform(0.5, 1.3, Bn)
+        tok = r.integers(0, V, (Bn, T - 1))
+        _, n = _check_chain(lg, dr, tok, t, r.random((Bn, T - 1)), r.random(Bn), ws)
+        assert int((n < T - 1).sum()) > 0                        # refusals, which the counters serve
+        u = r.random((Bn, T))
+        tok, par = random_tree(r, lg, t, u)
+        check_tree(lg, tok, par, t, u, ws)

@@ -1,0 +1,14 @@
+"""CPU checks of the verify step's sizes: workspaces that serve smaller calls, and limits at the ends of 32-bit counts. No
+kernel is launched."""
+import block_scaled_fp8_skinny_amd as B
+from test_serving_abi import lib  # noqa: F401
+
+
+def test_a_verification_workspace_serves_smaller_calls(lib):
+    size = B.bsfp8_verify_workspace_bytes
+    for most in ((100, 8, 5000), (9, 64, 300), (65, 2, 131073)):
+        for b in range(1, most[0] + 1, 7):
+            for t in range(1, most[1] + 1):
+                for v in (1, 31, 1025, most[2] // 2, most[2]):
+                    if v <= most[2]:
+                        assert 0 < size(b, t, v) <= size(*most), (b, t, v, most)
