@@ -66,49 +66,68 @@ template <> struct Vec<uint16_t> {
 
 constexpr float NEG_INF = -__builtin_inff();
 
-// A wave's view of one row of V elements. Rows start anywhere, so the row is addressed in 16-byte
-// words from the word that holds its first element: word w, element i is row element w * E + i - lead,
-// and elements outside [0, V) (the neighbouring rows') read as -inf. The descriptor ends with the
-// row's last whole 4-byte word, so nothing past the row is read; a bf16 row's last element in half a word
-// is read by itself.
+// What a lane loads of a vector: its 16 bytes and, in a bf16 row that starts in the middle of a 4-byte word, the word
+// after them.
+struct Words {
+  u32x4_t w;
+  uint32_t next;
+};
+
+// A wave's view of one row of V elements: word w, element i is row element w * E + i wherever the row starts in memory, so
+// that rows of equal logits are summed in the same order and their probabilities cancel. Buffer loads need 4-byte
+// addresses; a bf16 row of an odd start is read from the element before it and shifted by half a word. Elements
+// past the row's end (the neighbouring row's) read as -inf. The descriptor ends with the row's last whole 4-byte word, so
+// nothing past the row is read; a bf16 row's last element in half a word is read by itself.
 template <typename T>
 struct Row {
   static constexpr int E = Vec<T>::E, N = Vec<T>::N;
   __amdgpu_buffer_rsrc_t r;
-  int lead, V;
-  bool half;
+  int V;
+  bool odd, half;
   float last;
-  __device__ __forceinline__ Row(const void* base, int64_t row, int V_) : V(V_), half(false), last(0.f) {
+  __device__ __forceinline__ Row(const void* base, int64_t row, int V_) : V(V_), odd(false), half(false), last(0.f) {
     const int64_t first = row * V_;
     const T* const at = reinterpret_cast<const T*>(base) + first;
-    lead = (int)(first & (E - 1));
-    const int64_t bytes = (int64_t)(lead + V_) * (int64_t)sizeof(T) & ~(int64_t)3;
-    r = __builtin_amdgcn_make_buffer_rsrc((void*)(at - lead), 0, (int)bytes, RSRC_WORD3);
     if constexpr (sizeof(T) == 2) {
-      half = (lead + V_) & 1;
+      odd = first & 1;
+      half = (odd + V_) & 1;
       if (half) last = __uint_as_float((uint32_t)at[V_ - 1] << 16);
     }
+    r = __builtin_amdgcn_make_buffer_rsrc((void*)(at - odd), 0, (odd + V_) * (int)sizeof(T) & ~3, RSRC_WORD3);
   }
-  __device__ __forceinline__ u32x4_t load(int piece, int lane, int v) const {
-    return __builtin_amdgcn_raw_buffer_load_b128(r, (piece * (PIECE / E) + v * 64 + lane) * 16, 0, 0);
+  __device__ __forceinline__ Words load(int piece, int lane, int v) const {
+    const int at = index(piece, lane, v, 0) * (int)sizeof(T);
+    Words w;
+    w.w = __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0);
+    w.next = 0;
+    if constexpr (sizeof(T) == 2)
+      if (odd) w.next = __builtin_amdgcn_raw_buffer_load_b32(r, at + 16, 0, 0);   // uniform
+    return w;
   }
-  __device__ __forceinline__ void load(int piece, int lane, u32x4_t (&w)[N]) const {
+  __device__ __forceinline__ void load(int piece, int lane, Words (&w)[N]) const {
 #pragma unroll
     for (int v = 0; v < N; ++v) w[v] = load(piece, lane, v);
   }
   __device__ __forceinline__ int index(int piece, int lane, int v, int i) const {
-    return (piece * (PIECE / E) + v * 64 + lane) * E + i - lead;
+    return (piece * (PIECE / E) + v * 64 + lane) * E + i;
   }
   // A vector's elements; outside the row: -inf. NaN stays (it loses every maximum, and weighs nothing).
-  __device__ __forceinline__ void get(const u32x4_t& w, int piece, int lane, int v, float (&x)[E]) const {
+  __device__ __forceinline__ void get(const Words& from, int piece, int lane, int v, float (&x)[E]) const {
+    u32x4_t w = from.w;
+    if constexpr (sizeof(T) == 2) {
+      if (odd) {                                    // uniform
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __builtin_amdgcn_alignbit(i < 3 ? from.w[i + 1] : from.next, from.w[i], 16);
+      }
+    }
     Vec<T>::get(w, x);
-    if (piece * PIECE < lead || (piece + 1) * PIECE > V + lead) {   // the row's ends (uniform)
+    if ((piece + 1) * PIECE > V) {                  // the row's end (uniform)
       const int at = index(piece, lane, v, 0);
 #pragma unroll
-      for (int i = 0; i < E; ++i) x[i] = half && at + i == V - 1 ? last : (unsigned)(at + i) < (unsigned)V ? x[i] : NEG_INF;
+      for (int i = 0; i < E; ++i) x[i] = half && at + i == V - 1 ? last : at + i < V ? x[i] : NEG_INF;
     }
   }
-  __device__ __forceinline__ void get(const u32x4_t (&w)[N], int piece, int lane, float (&x)[N][E]) const {
+  __device__ __forceinline__ void get(const Words (&w)[N], int piece, int lane, float (&x)[N][E]) const {
 #pragma unroll
     for (int v = 0; v < N; ++v) get(w[v], piece, lane, v, x[v]);
   }
@@ -235,7 +254,7 @@ __global__ void __launch_bounds__(256) verify_pairs_kernel(VerifyParams p) {
   const bool is_draft = row >= targets;
   const int local = is_draft ? row - targets : row;
   const Row<T> r(is_draft ? p.draft : p.logits, local, p.V);
-  u32x4_t w[N];
+  Words w[N];
   r.load(piece, lane, w);                           // (past the row's end: nothing is read)
   load_powers(powers);
   const int b = is_draft ? local / (p.T - 1) : local / p.T;
@@ -367,7 +386,7 @@ __device__ __forceinline__ int pick_greedy(const Row<T>& r, const Pair* pr, int 
       break;
     }
   }
-  u32x4_t w[N];
+  Words w[N];
   r.load(piece, lane, w);
   float x[N][E];
   r.get(w, piece, lane, x);
@@ -395,7 +414,7 @@ __device__ __forceinline__ int pick_row(const Row<T>& r, const Pair* pr, int pie
   const double target = (double)u * t.S;
   double before;
   const int piece = pick_piece(pieces, lane, target, before, [&](int i) { return pr[i].s * f(pr[i].m); });
-  u32x4_t raw[N];
+  Words raw[N];
   r.load(piece, lane, raw);
   float x[N][E];
   r.get(raw, piece, lane, x);
@@ -408,43 +427,27 @@ __device__ __forceinline__ int pick_row(const Row<T>& r, const Pair* pr, int pie
   return at < 0 ? 0 : r.index(piece, 0, 0, 0) + at;
 }
 
-// max(p - q, 0) of the lane's elements of a piece, in the target row's layout. The draft's row may
-// start at another place in its 16-byte words (an odd V): its elements are then read one by one.
+// max(p - q, 0) of the lane's elements of a piece.
 template <typename T>
 struct Residual {
   static constexpr int E = Vec<T>::E, N = Vec<T>::N;
   Row<T> rp, rq;
-  __amdgpu_buffer_rsrc_t q_row;                     // the draft's row from its first element
   Weights fp, fq;
   double ip, iq;                                    // 1 / S
   __device__ __forceinline__ Residual(const VerifyParams& p, int64_t prow, int64_t qrow, const Total& tp, const Total& tq,
                                       double it, const double* powers)
       : rp(p.logits, prow, p.V), rq(p.draft, qrow, p.V), fp(tp.M, it, powers), fq(tq.M, it, powers) {
-    q_row = __builtin_amdgcn_make_buffer_rsrc((void*)(reinterpret_cast<const T*>(p.draft) + qrow * p.V), 0,
-                                              (int)(p.V * (int)sizeof(T)), RSRC_WORD3);
     ip = 1.0 / tp.S;
     iq = tq.S > 0 ? 1.0 / tq.S : 0.0;
   }
-  // vector v of a piece: (a, b) = its words of both rows (b unused where the rows lie differently)
-  __device__ __forceinline__ void load(int piece, int lane, int v, u32x4_t& a, u32x4_t& b) const {
+  // vector v of a piece: (a, b) = its words of both rows
+  __device__ __forceinline__ void load(int piece, int lane, int v, Words& a, Words& b) const {
     a = rp.load(piece, lane, v);
-    b = rp.lead == rq.lead ? rq.load(piece, lane, v) : u32x4_t{0, 0, 0, 0};
+    b = rq.load(piece, lane, v);
   }
-  __device__ __forceinline__ void get(const u32x4_t& a, const u32x4_t& b, int piece, int lane, int v, double (&w)[E]) const {
+  __device__ __forceinline__ void get(const Words& a, const Words& b, int piece, int lane, int v, double (&w)[E]) const {
     float x[E], y[E];
-    if (rp.lead == rq.lead) {                       // uniform
-      rq.get(b, piece, lane, v, y);
-    } else {
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const int j = rp.index(piece, lane, v, i);     // (outside the row nothing is read)
-        if constexpr (sizeof(T) == 4)
-          y[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(q_row, j * 4, 0, 0));
-        else
-          y[i] = __uint_as_float((uint32_t)__builtin_amdgcn_raw_buffer_load_b16(q_row, j * 2, 0, 0) << 16);
-        y[i] = (unsigned)j < (unsigned)rp.V ? y[i] : NEG_INF;
-      }
-    }
+    rq.get(b, piece, lane, v, y);
     rp.get(a, piece, lane, v, x);
 #pragma unroll
     for (int i = 0; i < E; ++i) {
@@ -549,7 +552,7 @@ __global__ void __launch_bounds__(256, 4) verify_chain_kernel(VerifyParams p) {
     double* rest = p.rest + (int64_t)b * p.pieces * N;   // a sum for every vector
     const int at0 = (blockIdx.y * 4 + wave) * p.share, piece = at0 / N, v0 = at0 % N;
     if (piece < p.pieces) {
-      u32x4_t a[N], c[N];
+      Words a[N], c[N];
 #pragma unroll
       for (int v = 0; v < N; ++v)
         if (v < p.share) res.load(piece, lane, v0 + v, a[v], c[v]);
@@ -609,7 +612,7 @@ __global__ void __launch_bounds__(256, 4) verify_chain_kernel(VerifyParams p) {
           left -= s;
         }
       }
-      u32x4_t a, c;
+      Words a, c;
       double w[1][E];
       res.load(at, lane, v, a, c);
       res.get(a, c, at, lane, v, w[0]);
@@ -674,8 +677,7 @@ __global__ void __launch_bounds__(256) verify_tree_kernel(VerifyParams p) {
   if (lane == 0) p.n_accepted[b] = n;
 }
 
-// Pieces of a row; one whose length is not whole 16-byte words may start up to seven elements into its first.
-inline int pieces_of(int64_t V) { return (int)((V + (V % 8 ? 7 : 0) + PIECE - 1) / PIECE); }
+inline int pieces_of(int64_t V) { return (int)((V + PIECE - 1) / PIECE); }
 inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 }  // namespace

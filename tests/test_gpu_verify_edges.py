@@ -53,3 +53,23 @@ def test_one_workspace_serves_every_batch(V):
         u = r.random((Bn, T))
         tok, par = random_tree(r, lg, t, u)
         check_tree(lg, tok, par, t, u, ws)
+
+
+# ------------------------------------------------------------------------------------------------
+# equal rows of target and draft
+# ------------------------------------------------------------------------------------------------
+@TYPES
+@pytest.mark.parametrize("V", [301, 2041, 8197])
+def test_a_refusal_on_equal_rows_draws_from_the_target(V, dt):
+    """max(p - q, 0) is zero everywhere where both rows hold the same logits, wherever they lie in memory (rows of these
+    lengths start at different places in their 16-byte words): the token comes from p."""
+    r = np.random.default_rng(V)
+    Bn, T = 64, 3
+    lg = _logits(r, (Bn, T, V), dt)
+    dr = lg[:, : T - 1].clone()
+    tok = r.integers(0, V, (Bn, T - 1))
+    tok[::2, 0], tok[1::2, 1] = V, -1                            # outside the vocabulary: refused
+    t = r.uniform(0.5, 1.3, Bn)
+    for rep in range(4):
+        _, n = _check_chain(lg, dr, tok, t, 0.9 * r.random((Bn, T - 1)), r.random(Bn))
+        assert n.cpu().tolist() == [0, 1] * (Bn // 2)
