@@ -237,8 +237,9 @@ __device__ __forceinline__ double wave_scan(double v) {                 // inclu
 }
 __device__ __forceinline__ double wave_sum(double v) { return from_lane(wave_scan(v), 63); }
 
-// 1 / t, or 0 for a greedy row (t = 0, negative or NaN).
-__device__ __forceinline__ double inv_temperature(float t) { return t > 0.f ? 1.0 / (double)t : 0.0; }
+// 1 / t (0 for an infinite one: equal weights), or -1 for a greedy row (t = 0, negative or NaN).
+__device__ __forceinline__ double inv_temperature(float t) { return t > 0.f ? 1.0 / (double)t : -1.0; }
+__device__ __forceinline__ bool is_greedy(double it) { return it < 0; }
 
 // The pairs of every piece of every row (blockIdx.x; rows of sequence b: the target's b * T + i, then the
 // draft's B * T + b * (T - 1) + i).
@@ -270,7 +271,7 @@ __global__ void __launch_bounds__(256) verify_pairs_kernel(VerifyParams p) {
     for (int i = 0; i < E; ++i) m = fmaxf(m, x[v][i]);
   m = wave_max(m);
   double s = 0;
-  if (it > 0 && m > NEG_INF) {
+  if (!is_greedy(it) && m > NEG_INF) {
     if (m < -NEG_INF) {
       const Weights f(m, it, powers);
 #pragma unroll
@@ -307,7 +308,7 @@ __device__ __forceinline__ Total row_total(const Pair* pr, const Pairs& first, i
   for (int i = lane + 128; i < pieces; i += 64) M = fmaxf(M, pr[i].m);
   M = wave_max(M);
   double S = 0;
-  if (it > 0 && M > NEG_INF) {
+  if (!is_greedy(it) && M > NEG_INF) {
     const Weights f(M, it, powers);
     S = first.a.s * f(first.a.m) + first.b.s * f(first.b.m);
     for (int i = lane + 128; i < pieces; i += 64) S += pr[i].s * f(pr[i].m);
@@ -408,7 +409,7 @@ template <typename T>
 __device__ __forceinline__ int pick_row(const Row<T>& r, const Pair* pr, int pieces, int lane, const Total& t, double it,
                                         float u, const double* powers) {
   constexpr int E = Row<T>::E, N = Row<T>::N;
-  if (!(it > 0)) return pick_greedy(r, pr, pieces, lane, t.M);
+  if (is_greedy(it)) return pick_greedy(r, pr, pieces, lane, t.M);
   if (!(t.M > NEG_INF)) return 0;
   const Weights f(t.M, it, powers);
   const double target = (double)u * t.S;
@@ -479,7 +480,7 @@ __global__ void __launch_bounds__(256, 4) verify_chain_kernel(VerifyParams p) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int b = blockIdx.x, D = p.T - 1;
   const double it = inv_temperature(p.temperature[b]);
-  const bool greedy = !(it > 0);
+  const bool greedy = is_greedy(it);
   const Pair* target_pairs = p.pairs + (int64_t)b * p.T * p.pieces;
   const Pair* draft_pairs = p.pairs + ((int64_t)p.B * p.T + (int64_t)b * D) * p.pieces;
   // draft i on lane i of wave 0: its logits in both rows, asked for before the totals

@@ -425,7 +425,8 @@ BSFP8_API size_t bsfp8_verify_workspace_bytes(int64_t B, int64_t T, int64_t V);
  * token is the first index whose running sum of the weights passes u_sample[b] times their total,
  * the weights being max(p_n - q_n, 0) after a refusal (p_n where that is zero everywhere) and
  * p_{T-1} when all were accepted. With t = 0 (greedy; also t < 0 or NaN) x_i is accepted if it is
- * the lowest index of the largest logit of row i, and the next token is that of row n.
+ * the lowest index of the largest logit of row i, and the next token is that of row n. An infinite t gives
+ * every logit but -inf and NaN the same probability.
  *   logits : [B][T][V], draft : [B][T-1][V], of `dtype` (bsfp8_logits), contiguous, 16-byte aligned.
  *   tokens : int32_t [B][T-1]; one outside [0, V) is refused. temperature: float [B]; u: float
  *            [B][T-1]; u_sample: float [B], uniform in [0, 1) (all device; the draft arrays may be NULL

@@ -71,7 +71,8 @@ def attention(q, K, V, see, scale):
 
 
 def probabilities(logits, t):
-    """softmax(logits / t) of one row; t = 0: all on the lowest index of the largest. NaN counts as -inf."""
+    """softmax(logits / t) of one row; t = 0: all on the lowest index of the largest. NaN counts as -inf, which has
+    probability 0 at an infinite t too."""
     x = np.where(np.isnan(logits), -np.inf, np.asarray(logits, np.float64))
     p = np.zeros_like(x)
     if not np.isfinite(x.max()):
@@ -79,8 +80,9 @@ def probabilities(logits, t):
     if not t > 0:
         p[int(x.argmax())] = 1.0
         return p
-    e = np.exp((x - x.max()) / t)
-    return e / e.sum()
+    live = x > -np.inf
+    p[live] = np.exp((x[live] - x.max()) / t)
+    return p / p.sum()
 
 
 def pick(w, u):

@@ -73,3 +73,25 @@ def test_a_refusal_on_equal_rows_draws_from_the_target(V, dt):
     for rep in range(4):
         _, n = _check_chain(lg, dr, tok, t, 0.9 * r.random((Bn, T - 1)), r.random(Bn))
         assert n.cpu().tolist() == [0, 1] * (Bn // 2)
+
+
+# ------------------------------------------------------------------------------------------------
+# infinite temperatures
+# ------------------------------------------------------------------------------------------------
+@TYPES
+@pytest.mark.parametrize("V", [7, 1000, 3001])
+def test_infinite_temperature_is_uniform(V, dt):
+    """softmax(logits / t) with t infinite: the same probability for every logit that is not -inf or NaN."""
+    r = np.random.default_rng(V)
+    Bn, T = 12, 4
+    lg, dr = _logits(r, (Bn, T, V), dt), _logits(r, (Bn, T - 1, V), dt)
+    lg[1, :, ::2], lg[2, :, 3:5] = -float("inf"), float("nan")
+    dr[3, :, 1::2] = -float("inf")
+    t = np.full(Bn, np.inf)
+    t[5], t[6] = 0, 1
+    u = r.random((Bn, T))
+    out, n = _check_chain(lg, dr, r.integers(0, V, (Bn, T - 1)), t, u[:, 1:], r.random(Bn))
+    tok, par = random_tree(r, lg, t, u)
+    out, _, _ = check_tree(lg, tok, par, t, u)
+    if V > 100:
+        assert len(set(out[7:, 0].tolist())) > 1                 # not the largest logit of each
