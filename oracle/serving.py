@@ -72,16 +72,16 @@ def attention(q, K, V, see, scale):
 
 def probabilities(logits, t):
     """softmax(logits / t) of one row; t = 0: all on the lowest index of the largest. NaN counts as -inf, which has
-    probability 0 at an infinite t too."""
+    probability 0 at an infinite t too; logits of +inf share the row."""
     x = np.where(np.isnan(logits), -np.inf, np.asarray(logits, np.float64))
-    p = np.zeros_like(x)
-    if not np.isfinite(x.max()):
+    p, top = np.zeros_like(x), x.max()
+    if top == -np.inf:
         return p
     if not t > 0:
         p[int(x.argmax())] = 1.0
         return p
-    live = x > -np.inf
-    p[live] = np.exp((x[live] - x.max()) / t)
+    live = x == top if top == np.inf else x > -np.inf
+    p[live] = 1.0 if top == np.inf else np.exp((x[live] - top) / t)
     return p / p.sum()
 
 

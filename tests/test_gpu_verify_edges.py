@@ -76,7 +76,7 @@ def test_a_refusal_on_equal_rows_draws_from_the_target(V, dt):
 
 
 # ------------------------------------------------------------------------------------------------
-# infinite temperatures
+# infinite temperatures and logits
 # ------------------------------------------------------------------------------------------------
 @TYPES
 @pytest.mark.parametrize("V", [7, 1000, 3001])
@@ -95,3 +95,28 @@ def test_infinite_temperature_is_uniform(V, dt):
     out, _, _ = check_tree(lg, tok, par, t, u)
     if V > 100:
         assert len(set(out[7:, 0].tolist())) > 1                 # not the largest logit of each
+
+
+@TYPES
+@pytest.mark.parametrize("V", [40, 2051])
+def test_infinite_logits_share_their_row(V, dt):
+    r = np.random.default_rng(V)
+    Bn, T = 10, 3
+    lg, dr = _logits(r, (Bn, T, V), dt), _logits(r, (Bn, T - 1, V), dt)
+    inf = float("inf")
+    for b in range(Bn):
+        for i in range(T):
+            lg[b, i, torch.from_numpy(r.integers(0, V, 1 + b % 4)).cuda()] = inf
+    dr[2, :, 5] = dr[3, :, 6] = inf
+    dr[4, 0] = lg[4, 0]
+    lg[5, 0], lg[6, :, 1] = inf, float("nan")
+    t = r.uniform(0.5, 1.3, Bn)
+    t[::5], t[7] = 0, np.inf
+    first = lambda b, i: int((lg[b, i] == inf).nonzero()[0, 0])
+    for rep in range(3):
+        u = r.random((Bn, T))
+        tok = np.array([[first(b, i) if r.random() < 0.8 else r.integers(0, V) for i in range(T - 1)] for b in range(Bn)])
+        tok[4, 0] = V
+        _, n = _check_chain(lg, dr, tok, t, u[:, 1:], r.random(Bn))
+        tok, par = random_tree(r, lg, t, u)
+        check_tree(lg, tok, par, t, u)
