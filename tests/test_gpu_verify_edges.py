@@ -120,3 +120,24 @@ def test_infinite_logits_share_their_row(V, dt):
         _, n = _check_chain(lg, dr, tok, t, u[:, 1:], r.random(Bn))
         tok, par = random_tree(r, lg, t, u)
         check_tree(lg, tok, par, t, u)
+
+
+# ------------------------------------------------------------------------------------------------
+# rows of more than 128 pieces
+# ------------------------------------------------------------------------------------------------
+@TYPES
+@pytest.mark.parametrize("V", [131073, 300001, 262144])
+def test_long_rows(V, dt):
+    r = np.random.default_rng(V)
+    Bn, T = 5, 3
+    lg = _logits(r, (Bn, T, V), dt)
+    dr = (0.8 * lg[:, : T - 1].float() + 0.6 * _logits(r, (Bn, T - 1, V), torch.float32)).to(dt)
+    lg[3, :, -1] = lg[4, :, V - 300] = 60.0                      # all the weight behind the first 128 pieces
+    t = np.array([1.0, 0.7, 0.0, 1.0, 0.0])
+    tok = np.array([[SV.pick(SV.probabilities(f64(dr[b, i]), t[b]), r.random()) for i in range(T - 1)] for b in range(Bn)])
+    tok[1, 0], tok[3, 0], tok[4] = -1, V - 1, V - 300
+    for us in (0.02, 0.5, 0.999):
+        _check_chain(lg, dr, tok, t, r.random((Bn, T - 1)), np.full(Bn, us))
+    u = r.random((Bn, T))
+    tok, par = random_tree(r, lg, t, u)
+    check_tree(lg, tok, par, t, u)
