@@ -851,7 +851,8 @@ def _verify_args(logits, ws, out_tokens, n_accepted):
 def bsfp8_verify_chain(logits, draft, tokens, temperature, u, u_sample, ws=None, out_tokens=None, n_accepted=None):
     """Verify a chain of T - 1 drafted tokens a sequence: logits [B, T, V] of the target and draft [B, T-1, V] of the
     drafter (fp32 or bf16, alike), tokens int32 [B, T-1], temperature fp32 [B] (0: greedy), u fp32 [B, T-1] and u_sample
-    fp32 [B] uniform in [0, 1). With T = 1 there are no drafts: draft, tokens and u may be None.
+    fp32 [B] uniform in [0, 1). With T = 1 there are no drafts: draft, tokens and u may be None. A sequence of fewer drafts
+    fills up with tokens -1 and, at the first of them, a draft row of -inf.
     -> (out_tokens int32 [B, T]: accepted tokens, the next one, -1s; n_accepted int32 [B])."""
     B, T, V, dev, dt, ws, (pl, pw, po, pn), out_tokens, n_accepted = _verify_args(logits, ws, out_tokens, n_accepted)
     pd = _vec(draft, logits.dtype, "draft", (B, T - 1, V), dev) if T > 1 else 0

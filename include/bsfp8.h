@@ -432,6 +432,9 @@ BSFP8_API size_t bsfp8_verify_workspace_bytes(int64_t B, int64_t T, int64_t V);
  *            [B][T-1]; u_sample: float [B], uniform in [0, 1) (all device; the draft arrays may be NULL
  *            when T = 1).
  *   out_tokens : int32_t [B][T]: the n accepted tokens, the next one, then -1. n_accepted: int32_t [B].
+ * A sequence of fewer drafts than T - 1 fills up with tokens -1 and draft rows of -inf: the first of them is refused, and
+ * since its draft row has no probability the next token comes from p_n. (A refused token with any other draft row draws from
+ * max(p_n - q_n, 0).) What lies behind the first refusal takes no part.
  * 1 <= T <= 64, 1 <= V <= 2^24, B * (2 T - 1) < 2^24. Probabilities and running sums are 64-bit, so that neighbouring
  * sums are told apart. -inf logits have probability 0; a NaN logit counts as -inf; +inf ones share
  * the row. A row of nothing but -inf or NaN gives index 0. */

@@ -123,7 +123,7 @@ def test_infinite_logits_share_their_row(V, dt):
 
 
 # ------------------------------------------------------------------------------------------------
-# rows of more than 128 pieces
+# rows of more than 128 pieces; chains of different lengths
 # ------------------------------------------------------------------------------------------------
 @TYPES
 @pytest.mark.parametrize("V", [131073, 300001, 262144])
@@ -141,3 +141,27 @@ def test_long_rows(V, dt):
     u = r.random((Bn, T))
     tok, par = random_tree(r, lg, t, u)
     check_tree(lg, tok, par, t, u)
+
+
+@TYPES
+def test_shorter_chains_are_padded_with_refused_tokens(dt):
+    """A sequence of fewer drafts: tokens -1 and draft rows of -inf after them give what the shorter chain gives."""
+    r = np.random.default_rng(11)
+    Bn, T, V = 12, 5, 1203
+    lg = _logits(r, (Bn, T, V), dt)
+    dr = (0.9 * lg[:, : T - 1].float() + 0.3 * _logits(r, (Bn, T - 1, V), torch.float32)).to(dt)
+    t = r.uniform(0.5, 1.3, Bn)
+    t[::4] = 0
+    tok = np.array([[SV.pick(SV.probabilities(f64(dr[b, i]), t[b]), r.random()) for i in range(T - 1)] for b in range(Bn)])
+    u, us = r.random((Bn, T - 1)), r.random(Bn)
+    for b in range(Bn):
+        tok[b, b % T:] = -1
+        dr[b, b % T:] = -float("inf")
+    out, n = _check_chain(lg, dr, tok, t, u, us)
+    dev = lambda a, d: torch.from_numpy(np.ascontiguousarray(a, d)).cuda()
+    for b in range(Bn):
+        k = b % T                                                # its drafts
+        one = slice(b, b + 1)
+        short, m = B.bsfp8_verify_chain(lg[one, : k + 1].clone(), dr[one, :k].clone(), dev(tok[one, :k], np.int32),
+                                        dev(t[one], np.float32), dev(u[one, :k], np.float32), dev(us[one], np.float32))
+        assert int(m[0]) == int(n[b]) and torch.equal(short[0], out[b, : k + 1]) and (out[b, k + 1:] == -1).all()
