@@ -190,7 +190,8 @@ int check_attention_sizes(int64_t B, int64_t T, int64_t hq, int64_t hkv, int64_t
   if (dim != 64 && dim != 128 && dim != 192 && dim != 256) return BSFP8_ESHAPE;
   if (B < 0 || T < 1 || hkv < 1 || hkv > 65536 || hq < hkv || hq % hkv || hq > 64 * hkv || max_len < 0) return BSFP8_ESHAPE;
   const int64_t lim = (int64_t)1 << 31;
-  if (max_len >= lim || B >= lim || T >= lim || B * T >= lim || B * T * hq >= lim) return BSFP8_ESHAPE;
+  // the kernels count positions past a length in 32 bits, up to the end of a table's stretch (8064)
+  if (max_len > lim - (1 << 14) || B >= lim || T >= lim || B * T >= lim || B * T * hq >= lim) return BSFP8_ESHAPE;
   // units of at least 32 positions (and the cost of a start) of a head and a block of at least 16 rows are
   // counted in 32 bits
   const int64_t blocks = (T * (hq / hkv) + 15) / 16, units = max_len / 32 + 10;

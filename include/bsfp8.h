@@ -394,6 +394,7 @@ BSFP8_API size_t bsfp8_attention_workspace_bytes(int64_t B, int64_t T, int64_t h
  *   lens  : int32_t [B] (device), the nodes included; cut to [0, min(max_len, ld_pages * page)].
  *   nodes : int32_t [B] (device), cut to [0, T]; NULL: T everywhere. Rows t >= nodes[b] are zeros.
  *   mask  : int64_t [B][T] (device) or NULL; with a mask T <= 64.
+ *   max_len : 0 to 2^31 - 2^14, a bound of lens.
  *   scale : finite (BSFP8_EINVAL).
  *   out   : bf16 [B][T][hq][dim] (contiguous, 16-byte aligned). A node that sees nothing gets zeros.
  * Values of positions that a node does not see never reach it, also when they are NaN or infinite

@@ -1,7 +1,7 @@
 """CPU checks of the verify step's sizes: workspaces that serve smaller calls, and limits at the ends of 32-bit counts. No
 kernel is launched."""
 import block_scaled_fp8_skinny_amd as B
-from test_serving_abi import lib  # noqa: F401
+from test_serving_abi import NULL, P, attn, cache, lib  # noqa: F401
 
 
 def test_a_verification_workspace_serves_smaller_calls(lib):
@@ -12,3 +12,12 @@ def test_a_verification_workspace_serves_smaller_calls(lib):
                 for v in (1, 31, 1025, most[2] // 2, most[2]):
                     if v <= most[2]:
                         assert 0 < size(b, t, v) <= size(*most), (b, t, v, most)
+
+
+def test_lengths_whose_ends_pass_32_bits_are_refused(lib):
+    """The kernels look up to a table's stretch of 8064 positions past a length, in 32 bits: max_len ends at 2^31 - 2^14."""
+    top = (1 << 31) - (1 << 14)
+    assert B.bsfp8_attention_workspace_bytes(1, 1, 1, 1, 64, top) > 0
+    for bad in (top + 1, (1 << 31) - 1, 1 << 31):
+        assert B.bsfp8_attention_workspace_bytes(1, 1, 1, 1, 64, bad) == 0
+        assert attn(lib, cache(heads=1), ldq=64, Bn=1, T=1, hq=1, mask=NULL, max_len=bad) == B.ESHAPE
