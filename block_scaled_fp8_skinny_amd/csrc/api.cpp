@@ -655,7 +655,7 @@ int bsfp8_cache_read(const bsfp8_kv_cache* cache, const int64_t* slots, int64_t 
   const int st = check_cache(cache);
   if (st != BSFP8_OK) return st;
   if (R < 0 || R >= ((int64_t)1 << 31) || R * cache->heads >= ((int64_t)1 << 31)) return BSFP8_ESHAPE;
-  if (R * cache->heads * (cache->dim / 16) >= MAX_BLOCKS * 256) return BSFP8_ESHAPE;
+  if (R * cache->heads * (cache->dim / 16) > (MAX_BLOCKS - 1) * 256) return BSFP8_ESHAPE;
   if (R == 0) return BSFP8_OK;
   if (!slots || !k_out || !v_out) return BSFP8_EINVAL;
   if (!aligned16(k_out) || !aligned16(v_out)) return BSFP8_ESTRIDE;

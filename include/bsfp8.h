@@ -372,7 +372,7 @@ BSFP8_API int bsfp8_cache_write(const bsfp8_kv_cache* cache, const int64_t* slot
 /* Rows of the cache as bf16: k_out, v_out [R][heads][dim] (contiguous, 16-byte aligned), each value
  * e4m3(code) * 2^(byte-127) rounded once to bf16 (exact unless it falls below the bf16 normals;
  * scale byte 255 and NaN codes give NaN). A slot outside the cache gives zeros. R * heads < 2^31 and
- * R * heads * dim < 2^36. */
+ * R * heads * dim <= 2^36 - 4096. */
 BSFP8_API int bsfp8_cache_read(const bsfp8_kv_cache* cache, const int64_t* slots, int64_t R,
                                uint16_t* k_out, uint16_t* v_out, void* stream);
 

@@ -21,3 +21,11 @@ def test_lengths_whose_ends_pass_32_bits_are_refused(lib):
     for bad in (top + 1, (1 << 31) - 1, 1 << 31):
         assert B.bsfp8_attention_workspace_bytes(1, 1, 1, 1, 64, bad) == 0
         assert attn(lib, cache(heads=1), ldq=64, Bn=1, T=1, hq=1, mask=NULL, max_len=bad) == B.ESHAPE
+
+
+def test_reads_of_more_lanes_than_a_launch_counts_are_refused(lib):
+    """2^24 workgroups of 256 lanes of 16 codes are one too many: 2^36 - 4096 values are the most."""
+    c = lambda: cache(pages=1, heads=1)
+    far = [P(i << 12) for i in (1, 2, 3)]
+    for rows in ((1 << 30) - 63, (1 << 30) - 1, 1 << 30):
+        assert lib.bsfp8_cache_read(c(), far[0], rows, far[1], far[2], NULL) == B.ESHAPE
