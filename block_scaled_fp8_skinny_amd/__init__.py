@@ -773,7 +773,8 @@ def bsfp8_attention_workspace_bytes(B, T, hq, hkv, dim, max_len):
 
 
 def workspace_attention(B, T, hq, hkv, dim, max_len, device="cuda"):
-    """A workspace tensor for bsfp8_tree_attention with these sizes (its contents need no clearing)."""
+    """A workspace tensor for bsfp8_tree_attention with these sizes, or a smaller B, T or max_len (its contents need no
+    clearing)."""
     return torch.empty(bsfp8_attention_workspace_bytes(B, T, hq, hkv, dim, max_len), dtype=torch.uint8, device=device)
 
 

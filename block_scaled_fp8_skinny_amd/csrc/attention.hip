@@ -28,6 +28,8 @@
 // idle; a head that falls into several runs leaves partial (m, l, O) in the workspace for a joining kernel. Short contexts
 // are not cut: a workgroup for each head and row block, one launch. A launch is as short as its code: the instruction
 // cache starts cold, and 5 KB of straight code took 3 us (masks by single comparisons, sums unrolled per row block).
+#include <initializer_list>
+
 #include "device.h"
 
 namespace bsfp8 {
@@ -1243,27 +1245,38 @@ __global__ void __launch_bounds__(64 * WW, 2) attention_wide_kernel(AttnParams p
   }
 }
 
+// The two kernels' row blocks (mt steps of rows, at most `most`), units and grids.
+struct AttnKernel {
+  bool wide;
+  int dim;
+  int64_t step() const { return wide ? WW * 16 : 16; }
+  int64_t most() const { return wide ? (dim == 64 ? 3 : dim == 128 ? 2 : 1) : dim <= 128 ? 3 : 2; }
+  int64_t blocks(int64_t rows) const { return (rows + step() * most() - 1) / (step() * most()); }
+  int unit_shift(int mt) const { return !wide ? (ring_waves(dim, mt) == 8 ? 8 : 7) : dim == 64 ? 7 : dim == 128 ? 6 : 5; }
+  int64_t grid(int mt) const { return wide ? 256 : ring_grid(dim, mt); }
+  int64_t unsplit() const { return wide ? (dim == 64 ? 256 : 128) : dim <= 128 ? 512 : 256; }   // (see attention_plan)
+};
+// The ring kernel takes up to two of its blocks of rows, though it reads keys and values twice then: 16 sequences of
+// 4096 positions, 4 heads, 64 rows: 26 against 33 us at dim 64, 38 against 45 at 128, 58 against 62 at 192, 71 against
+// 77 at 256 (three blocks, 96 rows at dim 256: 99 against 79; 144 rows at dim 64: 38 against 45)
+inline int64_t ring_rows(int dim) { return AttnKernel{false, dim}.most() * 16 * 2; }
+
 struct AttnPlan {
   int wide, mt, br, unit_shift, start_cost, mblocks, nwg, direct;
 };
 // Rows of a block and the grid: every unit its own workgroup up to one workgroup per CU.
 AttnPlan attention_plan(const AttentionArgs& a) {
   const int64_t rows = a.T * (a.hq / a.cache.heads);
-  const bool small = a.cache.dim <= 128;
   AttnPlan p;
-  const int narrow = small ? 3 : 2;                 // blocks of 16 rows that a wave of the ring kernel holds
-  // the ring kernel takes up to two of its blocks of rows, though it reads keys and values twice then: 16 sequences of
-  // 4096 positions, 4 heads, 64 rows: 26 against 33 us at dim 64, 38 against 45 at 128, 58 against 62 at 192, 71 against
-  // 77 at 256 (three blocks, 96 rows at dim 256: 99 against 79; 144 rows at dim 64: 38 against 45)
-  p.wide = rows > narrow * 16 * 2;
-  const int64_t step = p.wide ? WW * 16 : 16, most = p.wide ? (a.cache.dim == 64 ? 3 : small ? 2 : 1) : narrow;
-  const int64_t blocks = (rows + step * most - 1) / (step * most);
+  p.wide = rows > ring_rows((int)a.cache.dim);
+  const AttnKernel k{p.wide != 0, (int)a.cache.dim};
+  const int64_t step = k.step(), blocks = k.blocks(rows);
   p.mt = (int)((rows + step * blocks - 1) / (step * blocks));
   p.br = (int)(p.mt * step);
   p.mblocks = (int)((rows + p.br - 1) / p.br);
-  p.unit_shift = !p.wide ? (ring_waves((int)a.cache.dim, p.mt) == 8 ? 8 : 7) : a.cache.dim == 64 ? 7 : a.cache.dim == 128 ? 6 : 5;
+  p.unit_shift = k.unit_shift(p.mt);
   const int64_t units = a.B * a.cache.heads * p.mblocks * ((a.max_len + (1 << p.unit_shift) - 1) >> p.unit_shift);
-  const int64_t grid = p.wide ? 256 : ring_grid((int)a.cache.dim, p.mt);
+  const int64_t grid = k.grid(p.mt);
   const int64_t items = a.B * a.cache.heads * p.mblocks;
   // Units of a run: with n workgroups it costs about t units / n (t = 1 us, wide 2) to compute them, and to write and
   // read back n partial results at 4 TB/s and 35 ns for each of an item's in the join; the least sum. (One token over
@@ -1277,8 +1290,7 @@ AttnPlan attention_plan(const AttentionArgs& a) {
   // 6.8 against 9.2 us, at 1024 11.5 against 10.2; 40 nodes, 16 heads over 4 of dim 128: at 128 positions 14.9 against
   // 17.6, at 256 19.3 against 17.8); longer ones where runs are longer than a unit, up to four (28 sequences of 275
   // positions, 53 nodes, 56 heads over 8 of dim 64: 27 against 52 us)
-  const int64_t bound = p.wide ? (a.cache.dim == 64 ? 256 : 128) : small ? 512 : 256;
-  p.direct = a.max_len <= bound + ((run < 4 ? run : 4) - 1) * ((int64_t)1 << p.unit_shift);
+  p.direct = a.max_len <= k.unsplit() + ((run < 4 ? run : 4) - 1) * ((int64_t)1 << p.unit_shift);
   if (p.direct) {
     p.nwg = (int)items;
     p.start_cost = 0;
@@ -1319,12 +1331,30 @@ inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 }  // namespace
 
+// The most that a plan of these sizes or of a smaller batch, fewer nodes or a smaller max_len uses (a plan itself may use
+// less for larger ones: short contexts of many sequences are not cut), so that one workspace serves a program's calls.
 size_t attention_ws_bytes(const AttentionArgs& a) {
-  const AttnPlan pl = attention_plan(a);
-  if (pl.direct) return 256;                        // (not read)
-  const size_t rows = (size_t)pl.nwg * 2 * pl.br;
-  return align256((size_t)a.B * a.cache.heads * pl.mblocks * sizeof(int2)) + align256(rows * sizeof(float2)) +
-         rows * (size_t)a.cache.dim * 4;
+  const int dim = (int)a.cache.dim;
+  const int64_t most_rows = a.T * (a.hq / a.cache.heads);
+  int64_t part_rows = 0, mblocks = 1;
+  bool split = false;
+  for (const bool wide : {false, true}) {
+    if (wide && most_rows <= ring_rows(dim)) break;
+    const AttnKernel k{wide, dim};
+    const int64_t rows = wide || most_rows < ring_rows(dim) ? most_rows : ring_rows(dim), blocks = k.blocks(rows);
+    if (blocks > mblocks) mblocks = blocks;
+    if (a.max_len > k.unsplit()) split = true;
+    for (int mt = 1; mt <= k.most() && (mt - 1) * k.step() < rows; ++mt) {
+      const int64_t tokens = (int64_t)1 << k.unit_shift(mt);
+      const int64_t units = a.B * a.cache.heads * blocks * ((a.max_len + tokens - 1) / tokens);
+      const int64_t held = k.step() * mt * (units < k.grid(mt) ? units : k.grid(mt));
+      if (held > part_rows) part_rows = held;
+    }
+  }
+  if (!split) return 256;                           // (not read)
+  const size_t rows = (size_t)part_rows * 2;
+  return align256((size_t)(a.B * a.cache.heads * mblocks) * sizeof(int2)) + align256(rows * sizeof(float2)) +
+         rows * (size_t)dim * 4;
 }
 
 int launch_tree_attention(const AttentionArgs& a, hipStream_t stream) {

@@ -376,8 +376,9 @@ BSFP8_API int bsfp8_cache_write(const bsfp8_kv_cache* cache, const int64_t* slot
 BSFP8_API int bsfp8_cache_read(const bsfp8_kv_cache* cache, const int64_t* slots, int64_t R,
                                uint16_t* k_out, uint16_t* v_out, void* stream);
 
-/* Workspace bytes of bsfp8_tree_attention for these sizes (0 for sizes it refuses). The contents
- * need no clearing; one workspace must not be used by two calls that can run at the same time. */
+/* Workspace bytes of bsfp8_tree_attention for these sizes (0 for sizes it refuses; never more for a smaller B, T or
+ * max_len of the same heads and dim: the largest call's workspace serves them all). The contents need no clearing; one
+ * workspace must not be used by two calls that can run at the same time. */
 BSFP8_API size_t bsfp8_attention_workspace_bytes(int64_t B, int64_t T, int64_t hq, int64_t hkv, int64_t dim,
                                                  int64_t max_len);
 

@@ -29,3 +29,16 @@ def test_reads_of_more_lanes_than_a_launch_counts_are_refused(lib):
     far = [P(i << 12) for i in (1, 2, 3)]
     for rows in ((1 << 30) - 63, (1 << 30) - 1, 1 << 30):
         assert lib.bsfp8_cache_read(c(), far[0], rows, far[1], far[2], NULL) == B.ESHAPE
+
+
+def test_an_attention_workspace_serves_smaller_calls(lib):
+    size = B.bsfp8_attention_workspace_bytes
+    for hq, hkv, dim in ((64, 8, 128), (32, 4, 64), (56, 8, 64), (48, 1, 192), (16, 2, 256)):
+        for most in ((64, 8, 1200), (28, 53, 300), (128, 6, 1024), (64, 64, 600), (3, 7, 100000)):
+            top = size(most[0], most[1], hq, hkv, dim, most[2])
+            lens = sorted({1, 128, 129, 256, 257, 512, 513, 640, 768, 1024, most[2] // 3, most[2]})
+            for b in sorted({1, 2, 8, 16, 37, most[0]}):
+                for t in sorted({1, 2, 4, 6, 8, 16, 33, most[1]}):
+                    for n in lens:
+                        if b <= most[0] and t <= most[1] and n <= most[2]:
+                            assert 0 < size(b, t, hq, hkv, dim, n) <= top, (b, t, hq, hkv, dim, n, most)
