@@ -43,7 +43,7 @@ constexpr int TILE = 32;                            // tokens of a wave's tile
 constexpr int ring_waves(int dim, int mt) { return dim == 128 && mt >= 2 ? 8 : 4; }
 constexpr int ring_grid(int dim, int mt) { return dim <= 128 && ring_waves(dim, mt) == 4 ? 512 : 256; }
 constexpr float HEADROOM = 8.f;                     // weights are at most 2^8
-constexpr float M_NONE = -1e30f;                    // reference of a row that has seen nothing
+constexpr float M_NONE = -3.4028234664e38f;         // reference of a row that has seen nothing: no finite score is below it
 
 struct AttnParams {
   const uint16_t* q;

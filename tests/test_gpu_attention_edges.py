@@ -1,4 +1,4 @@
-"""Attention of drafted tokens with the largest call's workspace."""
+"""Attention of drafted tokens with the largest call's workspace, and for scores far below zero."""
 import numpy as np
 import pytest
 import torch
@@ -24,3 +24,44 @@ def test_one_workspace_serves_smaller_calls(dim):
         lens = [most] + [int(x) for x in r.integers(0, most + 1, n - 1)]
         attend(180 + T, T, hq, hkv, dim, 32, lens, tree=T > 1, max_len=most, launch=launch)
         assert (room[need:] == 0xFF).all()
+
+
+PLANS = [pytest.mark.parametrize("bound", [256, 6000]), pytest.mark.parametrize("g", [1, 8, 40]),
+         pytest.mark.parametrize("dim", [64, 128, 192, 256])]
+
+
+def plans(f):
+    for p in PLANS:
+        f = p(f)
+    return f
+
+
+def mean_of_values(dim, g, n, each, scale, bound):
+    """All keys ones in the first 64 values, all queries `each` there and zeros after: every score is 64 * each * scale, every
+    weight of a row is alike, and the output is the mean of the values that the row sees."""
+    T, page = 3, 16
+    cache = B.KVCache.empty(3, 1, page, dim)
+    cache.kq.fill_(0x38)
+    cache.ks.fill_(127)
+    r = np.random.default_rng(dim + g)
+    codes = torch.from_numpy(r.integers(0x30, 0x48, (3, 1, page, dim), dtype=np.uint8)).cuda()
+    cache.vq.copy_(codes)
+    cache.vs.fill_(127)
+    q = torch.zeros((1, T, g, dim), dtype=torch.bfloat16, device="cuda")
+    q[..., :64] = each
+    pages, lens = torch.arange(3, dtype=torch.int32, device="cuda")[None], torch.tensor([n], dtype=torch.int32, device="cuda")
+    print("equal scores", dim, g, n, each, scale, bound, flush=True)
+    out = B.bsfp8_tree_attention(q, cache, pages, lens, scale=scale, max_len=bound).double().cpu()
+    v = codes.cpu().view(torch.float8_e4m3fn).double().transpose(1, 2).reshape(3 * page, dim)
+    for t in range(T):
+        seen = v[: n - T + t + 1]
+        want, mag = seen.mean(0), seen.abs().mean(0)
+        # a rounding of the result and of the weights to bf16, and the fp32 sums
+        tol = 2.0 ** -8 * want.abs() + (2.0 ** -8 + (n + 8) * 2.0 ** -24) * mag
+        assert ((out[0, t] - want).abs() <= tol).all(), (t, out[0, t, 0, :4], want[:4])
+
+
+@plans
+def test_scores_far_below_zero(dim, g, bound):
+    """-2^109 for each position (the products with powers of two are exact): a low score is not a masked one."""
+    mean_of_values(dim, g, 40, -1.0, 2.0 ** 103, bound)
