@@ -396,8 +396,13 @@ __device__ __forceinline__ void weights(const f32x4_t (&s)[2][MT], float scale2,
       mref[mt] = m;
       l[mt] *= f;
       rescale(mt, f);
+      // the product rounded as the reference's was: fused, half a unit in the last place of a score of 2^32 is
+      // left over, and 2 to that power may be infinite or leave nothing of the row
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[mt][e] = fmaf(s[e >> 2][mt][e & 3], scale2, -m);
+      for (int e = 0; e < 8; ++e) {
+#pragma clang fp contract(off)
+        x[mt][e] = s[e >> 2][mt][e & 3] * scale2 - m;
+      }
     }
   }
 #pragma unroll

@@ -1,4 +1,4 @@
-"""Attention of drafted tokens with the largest call's workspace, and for scores far below zero."""
+"""Attention of drafted tokens with the largest call's workspace, and for scores far below and far from zero."""
 import numpy as np
 import pytest
 import torch
@@ -65,3 +65,12 @@ def mean_of_values(dim, g, n, each, scale, bound):
 def test_scores_far_below_zero(dim, g, bound):
     """-2^109 for each position (the products with powers of two are exact): a low score is not a masked one."""
     mean_of_values(dim, g, 40, -1.0, 2.0 ** 103, bound)
+
+
+@plans
+def test_scores_whose_last_place_is_large(dim, g, bound):
+    """Scores of 2^32 and of 2^68 of both signs, whose product with log2 e is rounded by many powers of two: the largest
+    still weighs 1."""
+    for each in (3.0, -3.0, 5.0, -5.0, 11.0, -11.0):
+        for scale in (2.0 ** 25, 2.0 ** 60):
+            mean_of_values(dim, g, 20, each, scale, bound)
