@@ -1,4 +1,5 @@
-"""Attention of drafted tokens with the largest call's workspace, and for scores far below and far from zero."""
+"""Attention of drafted tokens with the largest call's workspace, and at the ends of its numbers: scores far below and far
+from zero, scales of keys and values over most of their range."""
 import numpy as np
 import pytest
 import torch
@@ -74,3 +75,35 @@ def test_scores_whose_last_place_is_large(dim, g, bound):
     for each in (3.0, -3.0, 5.0, -5.0, 11.0, -11.0):
         for scale in (2.0 ** 25, 2.0 ** 60):
             mean_of_values(dim, g, 20, each, scale, bound)
+
+
+def rescale(scales, x, lo, hi, seed):
+    """New random scale bytes lo .. hi - 1 in a cache's tensor, and the values x [slots, heads, dim] with them."""
+    new = np.random.default_rng(seed).integers(lo, hi, scales.shape, dtype=np.uint8)
+    up = (new.astype(np.int64) - scales.cpu().numpy()).transpose(0, 2, 1, 3).reshape(x.shape[0], x.shape[1], -1)
+    x *= np.exp2(np.repeat(up, 32, -1))                          # exact: powers of two
+    scales.copy_(torch.from_numpy(new))
+
+
+RANGES = [pytest.mark.parametrize("g,T", [(1, 1), (8, 6), (16, 5), (40, 6)]), pytest.mark.parametrize("dim", [64, 128, 192, 256])]
+
+
+def ranges(f):
+    for p in RANGES:
+        f = p(f)
+    return f
+
+
+@ranges
+def test_scales_of_values_over_their_range(dim, g, T):
+    """2^-87 to 2^63 side by side. (Scores of a few units: no weight falls below the fp32 normals, which a large value would
+    show.)"""
+    attend(200 + g, T, 2 * g, 2, dim, 32, [T, 77, 300], tree=T > 1, scale=0.01,
+           spoil=lambda cache, K, V, pages: rescale(cache.vs, V, 40, 191, dim))
+
+
+@ranges
+def test_scales_of_keys_over_their_range(dim, g, T):
+    """2^-77 to 2^-1 side by side."""
+    attend(210 + g, T, 2 * g, 2, dim, 32, [T, 77, 300], tree=T > 1,
+           spoil=lambda cache, K, V, pages: rescale(cache.ks, K, 50, 127, dim))
