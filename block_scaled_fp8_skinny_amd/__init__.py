@@ -716,8 +716,9 @@ def bsfp8_cache_write(cache, slots, k, v, q=None, q_out=None, q_weight=None, k_w
                       positions=None, interleaved=False):
     """Write tokens into the cache, normalising and rotating queries and keys on the way.
 
-    k, v: bf16 [R, heads, dim] (or [R, heads * dim]), any row stride; q likewise, or None. slots: int64 [R]. q_weight,
-    k_weight: bf16 [dim] norm weights or None. cos_sin: fp32 [n_positions, rot] with positions int64 [R], or None.
+    k, v: bf16 [R, heads, dim] (or [R, heads * dim]), any row stride; q likewise, or None. slots: int64 [R], each in the
+    cache at most once. q_weight, k_weight: bf16 [dim] norm weights or None. cos_sin: fp32 [n_positions, rot] with
+    positions int64 [R], or None (positions are not looked at then).
     Returns q_out (bf16 [R, hq, dim], allocated when None), or None without q."""
     c = _cache(cache)
     dev, D = c.device, c.dim

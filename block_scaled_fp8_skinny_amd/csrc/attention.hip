@@ -20,8 +20,9 @@
 //   ring  up to 96 rows (64 above dim 128): a workgroup's waves share 16 to 48 rows and split their tokens in tiles of 32,
 //         each wave with a ring of NS tiles in LDS that the LDS mode of global loads fills (codes are contiguous per 16
 //         tokens of a page and head); waves only wait for their own loads, and are joined through LDS at an item's end.
-//         Bound by HBM: the loop of a chain of 6 over 131072 positions (64 heads over 8 of dim 128) streams 6.2 TB/s; 71 us
-//         in all, of which 5 go before the first tile is asked for, 10 to the waves' skew and join, 5 to the joining kernel.
+//         Bound by HBM: the loop of a chain of 6 over 131072 positions (64 heads over 8 of dim 128) streams 6.2 TB/s by the
+//         clock read in the kernel (a plain read of as much 6.2 to 6.6); 71 us in all (62 in a graph), of which 5 go before the
+//         first tile is asked for, 10 to the waves' skew and join, 6 to the joining kernel.
 //   wide  more rows: the waves split the rows and share the tokens, which are rebuilt once per workgroup (see there).
 // Work is cut evenly over the grid: the units (the tokens that a workgroup's waves take in one step, of one head and row
 // block) of all sequences, in order, are divided into equal runs, one per workgroup, so that ragged lengths leave nobody
@@ -868,8 +869,9 @@ __global__ void __launch_bounds__(256) attention_join_kernel(AttnParams p, int j
 // conflicts), two buffers deep: while a tile is computed, the next one is rebuilt, a unit of K and one of V
 // by each wave. The operand order of V is value c * 64 + x * 4 + k for column x of 16-row tile 4c + k.
 // Trees of 64 nodes over 16384 positions of 4 sequences, 64 heads over 8 of dim 128 (137 GFLOP): 176 us, 0.78 PFLOP/s.
-// Counters: matrix cores busy 33% of the time, vector ALUs 45%, LDS 28%; two waves a SIMD overlap them little (all the
-// registers are taken at 32 rows a wave). Taking turns by halves, products against softmax with a barrier after each
+// Counters: matrix cores busy 35% of the time, vector ALUs 47%, LDS 29%; two waves a SIMD overlap them little (all the
+// registers are taken at 32 rows a wave). The instances of 32 rows of dim 128 and of dim 256 keep two and four vector registers
+// in scratch, read once an item; every instance of both kernels keeps 110 to 290 scalars in lanes of vector registers. Taking turns by halves, products against softmax with a barrier after each
 // phase, was slower (217 us), as was rebuilding V in half the waves and K in the others (180).
 // ------------------------------------------------------------------------------------------------
 constexpr int WW = 8;                               // waves per workgroup

@@ -15,9 +15,9 @@
 //           sums max(p - q, 0) over its piece, and the workgroup that arrives last (a counter per
 //           sequence, zeroed by the first launch) picks the token. Otherwise the sequence's first workgroup picks.
 //   tree    one wave per node samples its token; the sequence's last workgroup walks down.
-// Times: 32 chains of 6 over 131072 columns, 36 us for the pairs (184 MB at 5.1 TB/s, the vector ALUs 81% busy with the
-// exponentials) and 18 for the rest, of which 8 are its chain of dependent loads (a single chain's 8.6) and the others
-// the second look at the refused rows; 16 trees of 32 nodes over 32768 columns 15 and 6.7 us.
+// Times: 32 chains of 6 over 131072 columns, 36 us for the pairs (184 MB at 5.1 TB/s, the vector ALUs 84% busy with the
+// exponentials: bf16 logits take as long) and 18 for the rest, of which 8 are its chain of dependent loads (a single chain's
+// 8.3) and the others the second look at the refused rows; 16 trees of 32 nodes over 32768 columns 15 and 6.5 us.
 #include "device.h"
 
 namespace bsfp8 {

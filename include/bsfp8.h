@@ -352,7 +352,7 @@ typedef struct bsfp8_kv_cache {
  *   bsfp8_quantize_mx, on the fp32 value: keys are not rounded to bf16 in between) into slots[r].
  *   slots     : int64_t [R] (device). A slot outside [0, pages * page) (e.g. -1 for a padding row)
  *               stores no key and value; its query is written all the same. Two rows of one call
- *               with the same slot leave either row's values.
+ *               must not have the same slot: they would leave a mixture of both rows' bytes there.
  *   k, v      : bf16 [R][ldk], [R][ldv], head h at columns [h*dim, (h+1)*dim) (16-byte aligned; row
  *               strides >= heads*dim, multiples of 8: slices of a fused projection).
  *   q, q_out  : bf16 [R][ldq] with hq heads, and [R][hq][dim] contiguous; NULL with hq = 0.
@@ -400,7 +400,9 @@ BSFP8_API size_t bsfp8_attention_workspace_bytes(int64_t B, int64_t T, int64_t h
  *   out   : bf16 [B][T][hq][dim] (contiguous, 16-byte aligned). A node that sees nothing gets zeros.
  * Values of positions that a node does not see never reach it, also when they are NaN or infinite
  * (a rejected draft's leftovers, a page never written); those that it sees have the effect they have in the formula,
- * values whose code times scale passes bf16 counting as infinite. hq is a multiple of cache->heads, at most
+ * values whose code times scale passes bf16 counting as infinite. (In fp32, that is: a weight below 2^-126 of the
+ * row's largest is 0, and may make an infinity or NaN of an infinite value; a row whose scores are all -inf gets
+ * zeros.) hq is a multiple of cache->heads, at most
  * 64 times it; T >= 1; B * T * hq < 2^31, and fewer than 2^24 blocks of 16 rows (B times the key/value
  * heads times T * hq / heads / 16, rounded up). Scores and sums are fp32; the weights of one tile are
  * rounded to bf16 for the product with V (rebuilt exactly from its codes, as K is). The split of
