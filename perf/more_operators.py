@@ -1,0 +1,556 @@
+"""Cases of a serving step's operators: the norms and the gated residual between blocks, page tables and slots from
+request lengths, bounds of the cached keys of a page, attention over the pages that these bounds select, and sampling
+with top-k, top-p and min-p.
+
+`listed()` holds the named cases, `draw(rng)` gives further ones of the same ranges, `prepare(case, seed)`
+makes what a program has in hand before the call, `run(state)` is one pass: in plain torch operations where
+`own` is false, through block_scaled_fp8_skinny_amd where it is true. `work(case)` counts the bytes and
+operations that a pass cannot do without and `exact(case, seed)` gives the outputs in 64 bits.
+"""
+import math
+
+import torch
+
+own = False
+
+DEV = "cuda"
+BLOCK = 32                # values that share one power-of-two scale
+F8 = torch.float8_e4m3fn
+E8 = torch.float8_e8m0fnu
+EPS = 1e-6
+
+
+# ------------------------------------------------------------------------------------------------
+# cases
+# ------------------------------------------------------------------------------------------------
+def _norm(name, rows, width, f32, gate, post, mx):
+    c = dict(op="norm", rows=rows, width=width, f32=f32, gate=gate, post=post, mx=mx)
+    return dict(c, name=name) if name else c
+
+
+def _tables(name, batch, length, page, fresh, drafts):
+    c = dict(op="tables", batch=batch, length=length, page=page, fresh=fresh, drafts=drafts)
+    return dict(c, name=name) if name else c
+
+
+def _bounds(name, batch, length, added, hkv, dim, page):
+    c = dict(op="bounds", batch=batch, length=length, added=added, hkv=hkv, dim=dim, page=page)
+    return dict(c, name=name) if name else c
+
+
+def _sparse(name, batch, nodes, length, count, hq, hkv, dim, page, ragged):
+    c = dict(op="sparse", batch=batch, nodes=nodes, length=length, count=count, hq=hq, hkv=hkv, dim=dim, page=page,
+             ragged=ragged)
+    return dict(c, name=name) if name else c
+
+
+def _sample(name, rows, vocab, bf16, rules, filtered):
+    c = dict(op="sample", rows=rows, vocab=vocab, bf16=bf16, rules=rules, filtered=filtered)
+    return dict(c, name=name) if name else c
+
+
+def listed():
+    return [
+        # one sequence's verify step: six rows between two blocks, a gate for each channel
+        _norm("norm_step6", 6, 5120, False, "channel", True, False),
+        # a prompt's chunk of an odd number of rows, its residual in fp32, MXFP8 out for the fp8 x fp8 products
+        _norm("norm_prompt", 8191, 5120, True, "none", True, True),
+        # a decode step of a full batch: one token each
+        _tables("tables_decode", 256, 8192, 64, 0.0, 1),
+        # requests coming, going, growing by drafts and shrinking by refused ones, in one step
+        _tables("tables_prompts", 96, 16384, 16, 0.25, 6),
+        # a decode step of a batch: each sequence's last page anew
+        _bounds("bounds_decode", 32, 8192, 1, 8, 128, 64),
+        # a long prompt's keys, just written
+        _bounds("bounds_prompt", 1, 65536, 65536, 8, 128, 64),
+        # one token over a long context, 2048 positions of it for each key head
+        _sparse("sparse_b1", 1, 1, 131072, 32, 64, 8, 128, 64, False),
+        # chains of drafts for a batch, ragged lengths
+        _sparse("sparse_chain_b16", 16, 4, 16384, 32, 64, 8, 128, 64, True),
+        # plain decode of a batch, 64-wide heads without sharing, small pages
+        _sparse("sparse_b16_mha64", 16, 1, 4099, 16, 16, 16, 64, 16, True),
+        # one request's next token from one rank's share of the vocabulary
+        _sample("sample_b1", 1, 32768, False, "p", False),
+        # a batch of requests, each with its own rules
+        _sample("sample_b64", 64, 131072, False, "mixed", False),
+        # drafted tokens' rows filtered for the verification
+        _sample("filter_b48", 48, 32768, True, "mixed", True),
+    ]
+
+
+def _log(rng, lo, hi):
+    return min(hi, max(lo, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(["norm", "tables", "bounds", "sparse", "sparse", "sparse", "sample", "sample"])
+    if op == "norm":
+        mx = rng.random() < 0.4
+        step = 32 if mx else 8
+        width = step * _log(rng, 64 // step, 16384 // step)
+        f32 = rng.random() < 0.4
+        gate = rng.choice(["none", "channel", "row"])
+        each = 10 if f32 else 8
+        return _norm(None, _log(rng, 1, 8191 * 5120 * 7 // (width * each)), width, f32, gate, rng.random() < 0.6, mx)
+    page = rng.choice([16, 32, 48, 64, 128])
+    if op == "tables":
+        batch = _log(rng, 1, 96)
+        return _tables(None, batch, _log(rng, 64, 16384), page, rng.choice([0.0, 0.05, 0.25]), rng.randint(1, 8))
+    dim = rng.choice([64, 128, 128, 192, 256])
+    hkv = rng.choice([1, 2, 4, 8])
+    if op == "bounds":
+        most = 65536 * 8 * 128 // (hkv * dim)
+        batch = _log(rng, 1, 64)
+        length = _log(rng, 16, max(16, min(131072, most // batch)))
+        return _bounds(None, batch, length, rng.choice([1, rng.randint(1, 8), _log(rng, 1, length)]), hkv, dim, page)
+    if op == "sparse":
+        g = rng.choice([1, 2, 3, 4, 7, 8, 16])
+        nodes = _log(rng, 1, 8)
+        batch = _log(rng, 1, 32)
+        count = _log(rng, 3, 64)
+        # no more bytes read, and no more scores, than the chains of the batch
+        most = 16 * 4 * 32 * 64 * 8 * 128 // (hkv * dim)
+        batch = max(1, min(batch, most // (nodes * count * page)))
+        rows = batch * nodes * g * hkv
+        most = min(131072, 16 * 4 * 64 * 256 * 128 * page // (rows * dim), 16 * 16384 * 8 * 128 // (batch * hkv * dim))
+        length = _log(rng, max(nodes, 64), max(nodes, 64, most))
+        return _sparse(None, batch, nodes, length, count, g * hkv, hkv, dim, page, rng.random() < 0.6)
+    vocab = _log(rng, 1000, 131072)
+    rows = _log(rng, 1, max(1, min(256, 64 * 131072 // (2 * vocab))))
+    return _sample(None, rows, vocab, rng.random() < 0.4, rng.choice(["k", "p", "min", "mixed", "mixed"]), rng.random() < 0.4)
+
+
+# ------------------------------------------------------------------------------------------------
+# inputs
+# ------------------------------------------------------------------------------------------------
+def _gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def _quantize(x):
+    """fp32 [..., D] -> (e4m3 codes [..., D], scale bytes [..., D/32]): 2^s with s = floor(log2 amax) - 8
+    per 32 values, values rounded to nearest even and saturated at 448."""
+    b = x.unflatten(-1, (-1, BLOCK))
+    amax = b.abs().amax(-1)
+    s = torch.where(amax > 0, torch.frexp(amax).exponent - 9, torch.full_like(amax, -127, dtype=torch.int32)).clamp(-127, 127)
+    q = torch.ldexp(b, -s.unsqueeze(-1)).clamp(-448, 448).to(torch.float32).to(F8)
+    return q.flatten(-2).view(torch.uint8), (s + 127).to(torch.uint8)
+
+
+def _dequantize(codes, scales):
+    f = torch.ldexp(torch.ones((), device=DEV), scales.to(torch.int32) - 127)
+    return (codes.view(F8).float().unflatten(-1, (-1, BLOCK)) * f.unsqueeze(-1)).flatten(-2)
+
+
+def _random_cache(g, pages, heads, page, dim):
+    """A cache that has been in use: every slot holds some token's values."""
+    out = []
+    for scale in (1.0, 0.7):
+        x = torch.randn(pages, heads, page, dim, generator=g, device=DEV, dtype=torch.bfloat16).float() * scale
+        out += _quantize(x)
+        del x
+    return out
+
+
+def _bf16(g, *shape, scale=1.0, at=0.0):
+    return (at + scale * torch.randn(*shape, generator=g, device=DEV)).to(torch.bfloat16)
+
+
+def _prepare_norm(c, g):
+    R, W = c["rows"], c["width"]
+    s = dict(h=4 * torch.randn(R, W, generator=g, device=DEV), y=_bf16(g, R, W))
+    if not c["f32"]:
+        s["h"] = s["h"].to(torch.bfloat16)
+    s["weight"] = _bf16(g, W, scale=0.1, at=1.0)
+    s["post"] = _bf16(g, W, scale=0.1, at=1.0) if c["post"] else None
+    s["gate"] = None if c["gate"] == "none" else _bf16(g, *((W,) if c["gate"] == "channel" else (R, W)), scale=0.3, at=0.5)
+    s["scale"] = 0.22
+    s["h_out"] = torch.empty_like(s["h"])
+    if c["mx"]:
+        s["x"] = [torch.empty(R, w, dtype=torch.uint8, device=DEV) for w in (W, W // BLOCK)]
+    else:
+        s["x"] = torch.empty(R, W, dtype=torch.bfloat16, device=DEV)
+    return s
+
+
+def _prepare_tables(c, g):
+    B, L, page = c["batch"], c["length"], c["page"]
+    rand = lambda lo, hi: torch.randint(lo, hi + 1, (B,), generator=g, device=DEV)
+    kind = torch.randperm(B, generator=g, device=DEV) / B
+    old = rand(max(1, L // 4), L)
+    new = old + rand(1, c["drafts"])                                        # decode, or a verify step's nodes
+    if c["drafts"] > 1:
+        new = torch.where(kind > 0.8, (old - rand(1, c["drafts"])).clamp(min=0), new)   # refused drafts
+    f = c["fresh"]
+    new = torch.where(kind < f, old, new)                                   # a prompt
+    old = torch.where(kind < f, 0, old)
+    new = torch.where((kind >= f) & (kind < 1.5 * f), 0, new)               # an end
+    width = (L + c["drafts"] + page - 1) // page
+    n = B * width
+    perm = torch.randperm(n, generator=g, device=DEV).to(torch.int32)
+    held = (old + page - 1) // page
+    at = torch.arange(width, device=DEV)
+    has = at[None] < held[:, None]
+    rank = has.flatten().cumsum(0).view(B, width) - 1
+    s = dict(lens=old.to(torch.int32), new_lens=new.to(torch.int32), width=width)
+    s["pages"] = torch.where(has, perm[rank.clamp(min=0)], -1).to(torch.int32)
+    total = has.sum()
+    s["free"] = torch.full((n,), -1, dtype=torch.int32, device=DEV)
+    left = torch.arange(n, device=DEV)
+    s["free"] = torch.where(left < n - total, perm[(left + total).clamp(max=n - 1)], s["free"])
+    s["n_free"] = (n - total).to(torch.int32).view(1)
+    s["rows"] = (math.ceil(f * B) * L + B * c["drafts"] + 63) // 64 * 64    # a program's token buffer, for the most there can be
+    i32 = lambda *k: torch.empty(*k, dtype=torch.int32, device=DEV)
+    s["out"] = dict(n_free_out=i32(1), slots=torch.empty(s["rows"], dtype=torch.int64, device=DEV),
+                    positions=torch.empty(s["rows"], dtype=torch.int64, device=DEV), seqs=i32(s["rows"]), starts=i32(B + 1),
+                    held=i32(B), counts=i32(4))
+    return s
+
+
+def _table(g, lens, width, page):
+    """A page table [B, width] over a cache of the same number of pages and one more, in random order."""
+    n = lens.shape[0] * width + 1
+    return torch.randperm(n, generator=g, device=DEV)[: n - 1].view(-1, width).to(torch.int32), n
+
+
+def _prepare_bounds(c, g):
+    B, L, page = c["batch"], c["length"], c["page"]
+    lens = torch.randint(max(1, L // 2), L + 1, (B,), generator=g, device=DEV, dtype=torch.int32)
+    lens[0] = L
+    s = dict(lens=lens, first=(lens - c["added"]).clamp(min=0))
+    s["pages"], n = _table(g, lens, (L + page - 1) // page, page)
+    s["cache"] = _random_cache(g, n, c["hkv"], page, c["dim"])
+    s["bounds"] = torch.zeros(n, c["hkv"], 2, c["dim"], dtype=torch.bfloat16, device=DEV)
+    return s
+
+
+def _prepare_sparse(c, g):
+    B, T, L, page = c["batch"], c["nodes"], c["length"], c["page"]
+    if c["ragged"]:
+        lens = torch.randint(min(L, max(T, L // 8)), L + 1, (B,), generator=g, device=DEV, dtype=torch.int32)
+        lens[0] = L
+        nodes = torch.randint(max(1, T - 2), T + 1, (B,), generator=g, device=DEV, dtype=torch.int32)
+    else:
+        lens, nodes = torch.full((B,), L, dtype=torch.int32, device=DEV), None
+    s = dict(lens=lens, nodes=nodes, scale=c["dim"] ** -0.5, sinks=1, recent=2)
+    s["pages"], n = _table(g, lens, (L + page - 1) // page, page)
+    s["cache"] = _random_cache(g, n, c["hkv"], page, c["dim"])
+    k = _dequantize(*s["cache"][:2]).to(torch.bfloat16)          # bounds of whole pages, as they are once written
+    s["bounds"] = torch.stack([k.amin(2), k.amax(2)], 2)
+    s["q"] = _bf16(g, B, T, c["hq"], c["dim"])
+    i32 = lambda *k: torch.empty(*k, dtype=torch.int32, device=DEV)
+    s["selected"], s["held"] = i32(B * T, c["hkv"], c["count"]), i32(B * T)
+    s["out"] = torch.empty_like(s["q"])
+    return s
+
+
+def _prepare_sample(c, g):
+    R, V = c["rows"], c["vocab"]
+    x = 2 * torch.randn(R, V, generator=g, device=DEV) - 1.5 * torch.rand(R, V, generator=g, device=DEV).log()
+    rand = lambda: torch.rand(R, generator=g, device=DEV)
+    rules, which = c["rules"], rand()
+    s = dict(logits=x.to(torch.bfloat16 if c["bf16"] else torch.float32), u=rand())
+    s["temperature"] = 0.5 + rand()
+    k = torch.exp(rand() * math.log(200)).to(torch.int32)        # 1 .. 200
+    p, m = 0.5 + 0.48 * rand(), 0.3 * rand() ** 2 + 1e-3
+    on = lambda name, lo, hi: torch.full_like(which, rules == name, dtype=torch.bool) if rules != "mixed" else (which > lo) & (which < hi)
+    s["top_k"] = torch.where(on("k", 0.0, 0.4), k, 0).to(torch.int32)
+    s["top_p"] = torch.where(on("p", 0.2, 0.7), p, 1.0)
+    s["min_p"] = torch.where(on("min", 0.6, 0.9), m, 0.0)
+    if rules == "mixed":
+        s["temperature"] = torch.where(which > 0.95, 0.0, s["temperature"])   # some requests decode greedily
+    s["tokens"] = torch.empty(R, dtype=torch.int32, device=DEV)
+    s["filtered"] = torch.empty_like(s["logits"]) if c["filtered"] else None
+    return s
+
+
+def prepare(case, seed):
+    s = {"norm": _prepare_norm, "tables": _prepare_tables, "bounds": _prepare_bounds, "sparse": _prepare_sparse,
+         "sample": _prepare_sample}[case["op"]](case, _gen(seed))
+    s["case"] = c = case
+    if own:   # the handle and the workspaces that a program keeps beside its tensors
+        import block_scaled_fp8_skinny_amd as L
+        s["lib"] = L
+        if "cache" in s:
+            s["handle"] = L.KVCache(*s["cache"])
+        if c["op"] == "sparse":
+            s["ws_select"] = L.workspace_select(c["batch"], c["nodes"], c["hkv"], s["pages"].shape[1])
+            s["ws"] = L.workspace_attention(c["batch"] * c["nodes"], 1, c["hq"], c["hkv"], c["dim"], c["count"] * c["page"])
+        elif c["op"] == "sample":
+            s["ws"] = L.workspace_sample(c["rows"], c["vocab"])
+    return s
+
+
+# ------------------------------------------------------------------------------------------------
+# one pass
+# ------------------------------------------------------------------------------------------------
+def _run_norm(s):
+    c = s["case"]
+    if own:
+        out = dict(mx_out=s["x"]) if c["mx"] else dict(x_out=s["x"])
+        h, x = s["lib"].bsfp8_residual_norm(s["h"], s["y"], weight=s["weight"], post_weight=s["post"], gate=s["gate"],
+                                            scale=s["scale"], eps=EPS, h_out=s["h_out"], **out)
+    else:
+        z = s["y"].float()
+        if s["post"] is not None:
+            z = z * torch.rsqrt(z.square().mean(-1, keepdim=True) + EPS) * s["post"].float()
+        if s["gate"] is not None:
+            z = z * s["gate"].float()
+        h = s["h"].float() + s["scale"] * z
+        x = h * torch.rsqrt(h.square().mean(-1, keepdim=True) + EPS) * s["weight"].float()
+        h, x = h.to(s["h"].dtype), _quantize(x) if c["mx"] else x.to(torch.bfloat16)
+    return [h, x[0].view(F8), x[1].view(E8)] if c["mx"] else [h, x]
+
+
+def _run_tables(s):
+    c, o = s["case"], s["out"]
+    names = ("slots", "positions", "seqs", "starts", "held", "counts")
+    if own:
+        got = s["lib"].bsfp8_step_tables(s["pages"], s["lens"], s["new_lens"], s["free"], s["n_free"], c["page"], s["rows"], **o)
+        return [getattr(got, n) for n in names] + [s["pages"], s["free"], o["n_free_out"]]
+    page, W, B, R = c["page"], s["width"], c["batch"], s["rows"]
+    old, new = s["lens"].clamp(min=0).long(), s["new_lens"].clamp(min=0).long()
+    had, want = (old + page - 1) // page, (new + page - 1) // page
+    at = torch.arange(W, device=DEV)[None]
+    gives = (at >= want[:, None]) & (at < had[:, None])
+    takes = (at >= had[:, None]) & (at < want[:, None])
+    given, wanted = gives.sum(), (want - had).clamp(min=0).sum()
+    # the stack of free pages with those given back on top, in the requests' order
+    stack = torch.cat([s["free"], torch.zeros(W * B, dtype=torch.int32, device=DEV)])
+    place = s["n_free"].long() + gives.flatten().cumsum(0).view(B, W) - 1
+    stack = stack.scatter(0, torch.where(gives, place, stack.shape[0] - 1).flatten(), s["pages"].flatten())
+    top = s["n_free"].long() + given - 1
+    rank = top - (takes.flatten().cumsum(0).view(B, W) - 1)
+    s["pages"].copy_(torch.where(takes, torch.where(rank >= 0, stack[rank.clamp(min=0)], -1), s["pages"]))
+    s["free"].copy_(torch.where(torch.arange(s["free"].shape[0], device=DEV) <= top, stack[: s["free"].shape[0]], s["free"]))
+    got = (takes & (rank >= 0)).sum(1)
+    held = torch.where(new > old, torch.minimum(new, (had + got) * page), new)
+    starts = torch.cat([torch.zeros(1, dtype=torch.long, device=DEV), (new - old).clamp(min=0).cumsum(0)])
+    row = torch.arange(R, device=DEV)
+    seq = torch.searchsorted(starts[1:].contiguous(), row, right=True)
+    live = row < starts[-1]
+    b = seq.clamp(max=B - 1)
+    pos = torch.where(live, old[b] + row - starts[b], 0)
+    entry = s["pages"][b, (pos // page).clamp(max=W - 1)].long()
+    slots = torch.where(live & (entry >= 0), entry * page + pos % page, -1)
+    taken = got.sum()
+    i32 = torch.int32
+    return [slots, pos, torch.where(live, seq, -1).to(i32), starts.to(i32), held.to(i32),
+            torch.stack([starts[-1], taken, given, wanted - taken]).to(i32), s["pages"], s["free"],
+            (s["n_free"].long() + given - taken).to(i32)]
+
+
+def _run_bounds(s):
+    c = s["case"]
+    if own:
+        s["lib"].bsfp8_cache_bounds(s["handle"], s["pages"], s["lens"], s["bounds"], first=s["first"], max_new=c["added"])
+        return s["bounds"]
+    page, D = c["page"], c["dim"]
+    at = torch.arange(s["pages"].shape[1], device=DEV)[None]
+    touched = (at >= s["first"][:, None] // page) & (at * page < s["lens"][:, None])
+    b, j = touched.nonzero(as_tuple=True)
+    ids = s["pages"][b, j].long()
+    kq, ks, _, _ = s["cache"]
+    x = _dequantize(kq[ids], ks[ids])                                       # [n, heads, page, D]
+    there = (j * page)[:, None] + torch.arange(page, device=DEV) < s["lens"][b][:, None]
+    there = there[:, None, :, None]
+    lo, hi = torch.where(there, x, math.inf).amin(2), torch.where(there, x, -math.inf).amax(2)
+    s["bounds"][ids] = torch.stack([lo, hi], 2).to(torch.bfloat16)
+    return s["bounds"]
+
+
+def _seen(s):
+    """Positions [B * T] that each query row sees: its own and those before it."""
+    c = s["case"]
+    T = c["nodes"]
+    t = torch.arange(T, device=DEV)
+    here = s["nodes"].long() if s["nodes"] is not None else torch.full((c["batch"],), T, device=DEV)
+    return torch.where(t < here[:, None], s["lens"].long()[:, None] - here[:, None] + t + 1, 0).flatten()
+
+
+def _run_sparse(s):
+    c = s["case"]
+    B, T, H, D, page, n = c["batch"], c["nodes"], c["hkv"], c["dim"], c["page"], c["count"]
+    if own:
+        sel, held = s["lib"].bsfp8_select_pages(s["q"], s["bounds"], s["pages"], s["lens"], n, page, nodes=s["nodes"],
+                                                sinks=s["sinks"], recent=s["recent"], ws=s["ws_select"],
+                                                selected=s["selected"], held=s["held"])
+        out = s["lib"].bsfp8_sparse_attention(s["q"].view(B * T, c["hq"], D), s["handle"], sel, held, scale=s["scale"],
+                                              ws=s["ws"], out=s["out"].view(B * T, c["hq"], D))
+        return [sel, held, out]
+    R, W = B * T, s["pages"].shape[1]
+    seen = _seen(s)
+    N = (seen + page - 1) // page
+    # which of two pages has the larger score is decided in 64 bits
+    k = s["bounds"][s["pages"].long()].double()                             # [B, W, H, 2, D]
+    q = s["q"].double().view(B, T, H, -1, D).permute(0, 2, 1, 3, 4).flatten(2, 3)            # [B, H, T*g, D]
+    lo, hi = (k[:, :, :, i].permute(0, 2, 3, 1).contiguous() for i in (0, 1))                # [B, H, D, W]
+    u = (q.clamp(max=0) @ lo + q.clamp(min=0) @ hi).unflatten(2, (T, -1)).amax(3)            # [B, H, T, W]
+    u = u.transpose(1, 2).reshape(R, H, W)
+    at = torch.arange(W, device=DEV)
+    there = at < N[:, None]
+    forced = there & ((at < s["sinks"]) | (at >= N[:, None] - s["recent"]))
+    u = torch.where(forced[:, None], math.inf, torch.where(there[:, None], u, -math.inf))
+    best = torch.sort(u, dim=-1, descending=True, stable=True).indices
+    best = torch.nn.functional.pad(best, (0, max(0, n - W)))[..., :n]
+    m = N.clamp(max=n)
+    mine = torch.arange(n, device=DEV) < m[:, None, None]
+    best = torch.where(mine, best, W).sort(-1).values                       # ascending, the unused ones last
+    ids = s["pages"].repeat_interleave(T, 0)[torch.arange(R, device=DEV)[:, None, None], best.clamp(max=W - 1)]
+    sel = torch.where(mine, ids, -1)
+    held = torch.where(seen > 0, (m - 1) * page + seen - (N - 1) * page, 0)
+    # attention over them
+    head = torch.arange(H, device=DEV)[None, :, None]
+    kq, ks, vq, vs = (t[sel.clamp(min=0).long(), head].flatten(2, 3) for t in s["cache"])    # [R, H, n * page, *]
+    pos = (best[..., None] * page + torch.arange(page, device=DEV)).flatten(2)
+    live = (pos < seen[:, None, None])[:, :, None]
+    q = s["q"].float().view(R, H, -1, D)
+    x = (q @ _dequantize(kq, ks).transpose(2, 3).contiguous() * s["scale"]).masked_fill(~live, -math.inf)
+    x = torch.exp(x - x.amax(-1, keepdim=True).clamp(min=-1e30))
+    total = x.sum(-1, keepdim=True)
+    o = x @ _dequantize(vq, vs) / torch.where(total > 0, total, 1)
+    return [sel, held.to(torch.int32), o.reshape(R, -1, D).to(torch.bfloat16)]
+
+
+def _run_sample(s):
+    if own:
+        tokens = s["lib"].bsfp8_sample(s["logits"], s["temperature"], s["u"], top_k=s["top_k"], top_p=s["top_p"], min_p=s["min_p"],
+                                       filtered=s["filtered"], ws=s["ws"], tokens=s["tokens"])
+        return [tokens] if s["filtered"] is None else [tokens, s["filtered"]]
+    V = s["case"]["vocab"]
+    # in 64 bits, since the decisions below compare neighbouring sums
+    x, order = torch.sort(s["logits"].double(), dim=-1, descending=True, stable=True)
+    t = s["temperature"].double()[:, None]
+    w = torch.exp((x - x[:, :1]) / torch.where(t > 0, t, 1))
+    n = torch.arange(V, device=DEV)
+    k = torch.where((s["top_k"] > 0) & (s["top_k"] < V), s["top_k"], V)[:, None]
+    k = torch.where(t > 0, k, 1)
+    w = torch.where(n < k, w, 0)
+    before = w.cumsum(-1) - w
+    p = s["top_p"].double()[:, None]
+    keep = (n < k) & ((p >= 1) | (before < p * w.sum(-1, keepdim=True))) & (w >= s["min_p"].double()[:, None])
+    keep = torch.zeros_like(keep).scatter(1, order, keep)
+    w = torch.where(keep, torch.zeros_like(w).scatter(1, order, w), 0)
+    c = w.cumsum(-1)
+    tokens = ((c > s["u"].double()[:, None] * c[:, -1:]) & keep).to(torch.int32).argmax(-1).to(torch.int32)
+    return [tokens] if s["filtered"] is None else [tokens, torch.where(keep, s["logits"], -math.inf)]
+
+
+def run(state):
+    return {"norm": _run_norm, "tables": _run_tables, "bounds": _run_bounds, "sparse": _run_sparse,
+            "sample": _run_sample}[state["case"]["op"]](state)
+
+
+# ------------------------------------------------------------------------------------------------
+# what a pass cannot do without
+# ------------------------------------------------------------------------------------------------
+def work(case):
+    c = case
+    if c["op"] == "norm":
+        R, W = c["rows"], c["width"]
+        each = 2 * (4 if c["f32"] else 2) + 2 + (33 / 32 if c["mx"] else 2) + (2 if c["gate"] == "row" else 0)
+        return dict(bytes=R * W * each + 2 * W * (1 + c["post"] + (c["gate"] == "channel")), flops=12 * R * W)
+    if c["op"] == "tables":
+        B, L = c["batch"], c["length"]
+        rows = math.ceil(c["fresh"] * B) * L + B * c["drafts"]              # the buffer's padding is written too
+        return dict(bytes=20 * B + 20 * rows + 12 * rows / c["page"], flops=rows)
+    if c["op"] == "bounds":
+        pages = c["batch"] * max(1, c["added"] // c["page"])
+        values = pages * c["page"] * c["hkv"] * c["dim"]
+        return dict(bytes=values * 33 / 32 + 4 * pages * c["hkv"] * c["dim"], flops=3 * values)
+    if c["op"] == "sparse":
+        B, T, L, H, D, page = c["batch"], c["nodes"], c["length"], c["hkv"], c["dim"], c["page"]
+        L = L * 9 // 16 if c["ragged"] else L                               # the mean
+        N = -(-L // page)
+        n = min(c["count"], N)
+        union = N * (1 - (1 - n / N) ** T)                                  # of a sequence's rows, were they independent
+        bytes_ = B * N * H * D * 4 + B * union * page * H * D * 2 * 33 / 32 + B * T * c["hq"] * D * 4 + B * T * H * n * 4
+        return dict(bytes=bytes_, flops=B * T * c["hq"] * D * (4 * N + 4 * n * page))
+    R, V = c["rows"], c["vocab"]
+    size = 2 if c["bf16"] else 4
+    return dict(bytes=R * V * size * (2 if c["filtered"] else 1), flops=R * V * 25)
+
+
+# ------------------------------------------------------------------------------------------------
+# the outputs in 64 bits, from the definitions
+# ------------------------------------------------------------------------------------------------
+def _exact_codes(x):
+    """64-bit values -> the values of the nearest e4m3 codes and of the scale bytes."""
+    b = x.reshape(*x.shape[:-1], -1, BLOCK)
+    top = b.abs().amax(-1, keepdim=True)
+    s = torch.where(top > 0, torch.floor(torch.log2(torch.where(top > 0, top, 1))) - 8, -127.0).clamp(-127, 127)
+    y = b * torch.pow(2.0, -s)
+    step = torch.pow(2.0, torch.floor(torch.log2(y.abs().clamp(min=2.0 ** -6))) - 3)
+    return (torch.round(y / step) * step).clamp(-448, 448).reshape(x.shape), torch.pow(2.0, s).squeeze(-1)
+
+
+def _values(codes, scales):
+    return (codes.view(F8).double().unflatten(-1, (-1, BLOCK)) * torch.pow(2.0, scales.double() - 127).unsqueeze(-1)).flatten(-2)
+
+
+def exact(case, seed):
+    c = case
+    if c["op"] == "tables":
+        return None                                   # whole numbers
+    s = prepare(case, seed)
+    if c["op"] == "norm":
+        h, z = s["h"].double(), s["y"].double()
+        if s["post"] is not None:
+            z = z / torch.sqrt((z * z).sum(-1, keepdim=True) / c["width"] + EPS) * s["post"].double()
+        if s["gate"] is not None:
+            z = z * s["gate"].double()
+        h = h + s["scale"] * z
+        x = h / torch.sqrt((h * h).sum(-1, keepdim=True) / c["width"] + EPS) * s["weight"].double()
+        return [h, *_exact_codes(x)] if c["mx"] else [h, x]
+    if c["op"] == "bounds":
+        out = s["bounds"].double()
+        for b in range(c["batch"]):
+            n, j = int(s["lens"][b]), int(s["first"][b]) // c["page"]
+            ids = s["pages"][b, j: -(-n // c["page"])].long()
+            x = _values(s["cache"][0][ids], s["cache"][1][ids])
+            last = n - (j + len(ids) - 1) * c["page"]
+            if len(ids) > 1:
+                out[ids[:-1]] = torch.stack([x[:-1].min(2).values, x[:-1].max(2).values], 2)
+            out[ids[-1]] = torch.stack([x[-1, :, :last].min(1).values, x[-1, :, :last].max(1).values], 1)
+        return out
+    if c["op"] == "sample":
+        if not c["filtered"]:
+            return None                               # tokens
+        out = torch.full((c["rows"], c["vocab"]), -math.inf, dtype=torch.float64, device=DEV)
+        for r in range(c["rows"]):
+            x, t = s["logits"][r].double(), float(s["temperature"][r])
+            order = torch.argsort(x, descending=True, stable=True)
+            k = int(s["top_k"][r])
+            order = order[:1] if t <= 0 else order[:k] if k > 0 else order
+            w = torch.exp((x[order] - x[order[0]]) / (t if t > 0 else 1))
+            if float(s["top_p"][r]) < 1:
+                order = order[: int((w.cumsum(0) < float(s["top_p"][r]) * w.sum()).sum()) + 1]
+            order = order[w[: len(order)] >= float(s["min_p"][r])]
+            out[r, order] = x[order]
+        return [None, out]
+    R, T, D, H, page = c["batch"] * c["nodes"], c["nodes"], c["dim"], c["hkv"], c["page"]
+    if R * H * c["count"] > 1 << 15:
+        return None
+    g, seen = c["hq"] // H, _seen(s).tolist()
+    out = torch.zeros(R, c["hq"], D, dtype=torch.float64, device=DEV)
+    kq, ks, vq, vs = s["cache"]
+    q = s["q"].double().view(R, H, g, D)
+    for r in range(R):
+        n = seen[r]
+        N = -(-n // page)
+        if not N:
+            continue
+        row = s["pages"][r // T, :N].long()
+        b = s["bounds"][row].double()                                       # [N, H, 2, D]
+        for h in range(H):
+            u = torch.maximum(q[r, h][None] * b[:, None, h, 0], q[r, h][None] * b[:, None, h, 1]).sum(-1).amax(1)
+            u[: s["sinks"]] = math.inf
+            u[max(0, N - s["recent"]):] = math.inf
+            j = torch.argsort(u, descending=True, stable=True)[: c["count"]].sort().values
+            k, v = (_values(x[row[j], h], y[row[j], h]).reshape(-1, D) for x, y in ((kq, ks), (vq, vs)))
+            held = (len(j) - 1) * page + n - (N - 1) * page
+            p = torch.softmax(q[r, h] @ k[:held].T * s["scale"], -1)
+            out[r, h * g: h * g + g] = p @ v[:held]
+    return [None, None, out]
