@@ -68,6 +68,14 @@ _SIGS = {
     "bsfp8_verify_workspace_bytes": (_SZ, [_I64] * 3),
     "bsfp8_verify_chain": (_I, [_P, _P, _I, _I64, _I64, _I64, _P, _P, _P, _P, _P, _SZ, _P, _P, _P]),
     "bsfp8_verify_tree": (_I, [_P, _I, _I64, _I64, _I64, _P, _P, _P, _P, _P, _SZ, _P, _P, _P, _P]),
+    "bsfp8_residual_norm": (_I, [_P, _I64, _I, _P, _I64, _P, _I64, _P, _P, ctypes.c_float, ctypes.c_float, _I64, _I64, _P,
+                                 _I64, _P, _P, _P, _P]),
+    "bsfp8_step_tables": (_I, [_P, _P, _I64, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _I64, _P, _P, _P, _P, _P, _P, _P]),
+    "bsfp8_cache_bounds": (_I, [_P, _P, _I64, _P, _P, _I64, _I64, _P, _P]),
+    "bsfp8_select_workspace_bytes": (_SZ, [_I64] * 4),
+    "bsfp8_select_pages": (_I, [_P, _I64, _I64, _I64, _I64, _P, _I64, _I64, _I64, _I64, _P, _I64, _P, _P, _I64, _I64, _I64, _I64,
+                                _P, _SZ, _P, _P, _P]),
+    "bsfp8_sparse_attention": (_I, [_P, _I64, _I64, _I64, _P, _P, _I64, _P, ctypes.c_float, _P, _SZ, _P, _P]),
     "bsfp8_gemm_mxfp8_config": (_I, [_P, _I64, _I64, _I64, _I64, _I64, _P, _P, _I, _I, _P, _SZ, _P, _P, _P]),
 }
 
@@ -882,3 +890,200 @@ def bsfp8_verify_tree(logits, tokens, parents, temperature, u, ws=None, out_toke
     st = lib().bsfp8_verify_tree(pl, dt, B, T, V, pt, pr, pe, pu, pw, ws.numel(), po, pp, pn, _stream(logits))
     _check(st, "bsfp8_verify_tree")
     return out_tokens, path, n_accepted
+
+
+# ------------------------------------------------------------------------------------------------
+# the serving step around them: norms and gated residual, page tables, attention over selected pages
+# ------------------------------------------------------------------------------------------------
+def _rows(x, dtype, name, R, W, device):
+    """[R, W] rows of any stride, their values contiguous -> (pointer, row stride)."""
+    if not isinstance(x, torch.Tensor) or x.dtype is not dtype:
+        raise TypeError(f"{name} must be a {dtype} tensor")
+    if x.device != device:
+        raise ValueError(f"{name} is on {x.device}, expected {device}")
+    shape, stride = x.shape, x.stride()
+    if len(shape) != 2 or shape[0] != R or shape[1] != W or (W > 1 and stride[1] != 1):
+        raise ValueError(f"{name} must be [{R}, {W}] with contiguous rows, got {list(shape)}, {list(stride)}")
+    return x.data_ptr(), stride[0] if R > 1 else W
+
+
+def bsfp8_residual_norm(h, y=None, weight=None, post_weight=None, gate=None, scale=1.0, eps=1e-6, h_out=None, x_out=None,
+                        mx_out=None, mx=False):
+    """The norms before and after a block with its gate and residual scale: z = norm(y) * post_weight (y itself without
+    one), h' = h + scale * gate * z, x = norm(h') * weight.
+
+    h: bf16 or fp32 [R, W], any row stride; y: bf16 [R, W] or None (h' = h); gate: bf16 [W], [R, W] or None; weight,
+    post_weight: bf16 [W] or None. h_out: where h' goes, of h's type (h itself: in place; allocated when None, and h itself
+    is returned without y). x_out: bf16 [R, W], contiguous; mx_out: (codes uint8 [R, W], scale bytes uint8 [R, W/32]).
+    -> (h', x): x as given, allocated when neither is: MXFP8 with mx=True, else bf16; (x_out, mx_out) when both are given."""
+    if not isinstance(h, torch.Tensor) or h.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("h must be a bf16 or fp32 tensor")
+    if h.dim() != 2 or not h.is_cuda:
+        raise ValueError("h must be a GPU tensor [R, W]")
+    R, W = h.shape
+    dev, dtype = h.device, h.dtype
+    ph, ldh = _rows(h, dtype, "h", R, W, dev)
+    py, ldy = _rows(y, torch.bfloat16, "y", R, W, dev) if y is not None else (0, 0)
+    pg = ldg = 0
+    if gate is not None:
+        if isinstance(gate, torch.Tensor) and gate.dim() == 1:
+            pg = _vec(gate, torch.bfloat16, "gate", (W,), dev)
+        else:
+            pg, ldg = _rows(gate, torch.bfloat16, "gate", R, W, dev)
+    pp = _vec(post_weight, torch.bfloat16, "post_weight", (W,), dev) if post_weight is not None else 0
+    pw = _vec(weight, torch.bfloat16, "weight", (W,), dev) if weight is not None else 0
+    if h_out is None and y is not None:
+        h_out = torch.empty((R, W), dtype=dtype, device=dev)
+    po, ldo = _rows(h_out, dtype, "h_out", R, W, dev) if h_out is not None else (0, 0)
+    if x_out is None and mx_out is None:
+        if mx:
+            mx_out = (torch.empty((R, W), dtype=torch.uint8, device=dev), torch.empty((R, W // 32), dtype=torch.uint8, device=dev))
+        else:
+            x_out = torch.empty((R, W), dtype=torch.bfloat16, device=dev)
+    px = _vec(x_out, torch.bfloat16, "x_out", (R, W), dev) if x_out is not None else 0
+    pq = ps = 0
+    if mx_out is not None:
+        pq, ps = _vec(mx_out[0], torch.uint8, "mx_out[0]", (R, W), dev), _vec(mx_out[1], torch.uint8, "mx_out[1]", (R, W // 32), dev)
+    st = lib().bsfp8_residual_norm(ph, ldh, 1 if dtype is torch.float32 else 0, py, ldy, pg, ldg, pp, pw, scale, eps, R, W, po, ldo,
+                                   px, pq, ps, _stream(h))
+    _check(st, "bsfp8_residual_norm")
+    return (h if h_out is None else h_out), (x_out if mx_out is None else mx_out if x_out is None else (x_out, mx_out))
+
+
+StepTables = namedtuple("StepTables", "slots positions seqs starts held counts")
+
+
+def bsfp8_step_tables(pages, lens, new_lens, free_pages, n_free, page, rows, per_seq=0, n_free_out=None, slots=None,
+                      positions=None, seqs=None, starts=None, held=None, counts=None):
+    """Page table, slots and positions of a step's tokens from the lengths before and after it.
+
+    pages: int32 [B, W], updated; lens, new_lens: int32 [B]; free_pages: int32 [capacity], the stack of free pages, updated;
+    n_free: int32 [1], its height, updated in place (or left, with n_free_out int32 [1]). page: tokens per page. rows:
+    how many rows the outputs have (a bound of the tokens added); per_seq: rows of a request, or 0: packed.
+    -> StepTables(slots int64 [rows], positions int64 [rows], seqs int32 [rows], starts int32 [B + 1], held int32 [B],
+    counts int32 [4]: tokens added, pages taken, given back, lacking). held is the next call's lens."""
+    if not isinstance(pages, torch.Tensor) or pages.dim() != 2 or not pages.is_cuda:
+        raise ValueError("pages must be a GPU tensor [B, W]")
+    dev, (B, W), i32, i64 = pages.device, pages.shape, torch.int32, torch.int64
+    if not isinstance(free_pages, torch.Tensor) or free_pages.dim() != 1:
+        raise ValueError("free_pages must be [capacity]")
+    new = lambda t, n, dtype: torch.empty((n,), dtype=dtype, device=dev) if t is None else t
+    slots, positions, seqs = new(slots, rows, i64), new(positions, rows, i64), new(seqs, rows, i32)
+    starts, held, counts = new(starts, B + 1, i32), new(held, B, i32), new(counts, 4, i32)
+    st = lib().bsfp8_step_tables(
+        _vec(lens, i32, "lens", (B,), dev), _vec(new_lens, i32, "new_lens", (B,), dev), B, page,
+        _vec(pages, i32, "pages", (B, W), dev), W, _vec(free_pages, i32, "free_pages", free_pages.shape, dev), free_pages.shape[0],
+        _vec(n_free, i32, "n_free", (1,), dev), _vec(n_free_out, i32, "n_free_out", (1,), dev) if n_free_out is not None else 0,
+        rows, per_seq, _vec(slots, i64, "slots", (rows,), dev), _vec(positions, i64, "positions", (rows,), dev),
+        _vec(seqs, i32, "seqs", (rows,), dev), _vec(starts, i32, "starts", (B + 1,), dev), _vec(held, i32, "held", (B,), dev),
+        _vec(counts, i32, "counts", (4,), dev), _stream(pages))
+    _check(st, "bsfp8_step_tables")
+    return StepTables(slots, positions, seqs, starts, held, counts)
+
+
+def _table(pages):
+    if not isinstance(pages, torch.Tensor) or pages.dim() != 2:
+        raise ValueError("pages must be [B, W]")
+    return pages.shape
+
+
+def bsfp8_cache_bounds(cache, pages, lens, bounds=None, first=None, max_new=None):
+    """Bounds of the keys of the pages that hold the positions first .. lens - 1 of each sequence (all without `first`):
+    bounds bf16 [pages, heads, 2, dim] (zeros when None), the least and the largest value of each key dimension.
+
+    pages: int32 [B, W] page table; lens, first: int32 [B]; max_new: a bound of lens - first (None: W * page)."""
+    c = _cache(cache)
+    dev = c.device
+    B, W = _table(pages)
+    shape = (c.pages, c.heads, 2, c.dim)
+    if bounds is None:
+        bounds = torch.zeros(shape, dtype=torch.bfloat16, device=dev)
+    pb = _vec(bounds, torch.bfloat16, "bounds", shape, dev)
+    pf = _vec(first, torch.int32, "first", (B,), dev) if first is not None else 0
+    st = lib().bsfp8_cache_bounds(c._ref, _vec(pages, torch.int32, "pages", (B, W), dev), W, _vec(lens, torch.int32, "lens", (B,), dev),
+                                  pf, B, W * c.page if max_new is None else max_new, pb, _stream(bounds))
+    _check(st, "bsfp8_cache_bounds")
+    return bounds
+
+
+def bsfp8_select_workspace_bytes(B, T, hkv, width):
+    return int(lib().bsfp8_select_workspace_bytes(B, T, hkv, width))
+
+
+def workspace_select(B, T, hkv, width, device="cuda"):
+    """A workspace tensor for bsfp8_select_pages with these sizes or smaller ones (its contents need no clearing)."""
+    return torch.empty(bsfp8_select_workspace_bytes(B, T, hkv, width), dtype=torch.uint8, device=device)
+
+
+def _tokens_view(q, dim, dev):
+    """bf16 queries [B, T, hq, dim] with contiguous heads and one stride between tokens -> that stride."""
+    if not isinstance(q, torch.Tensor) or q.dtype is not torch.bfloat16:
+        raise TypeError("q must be a bf16 tensor")
+    if q.device != dev:
+        raise ValueError(f"q is on {q.device}, expected {dev}")
+    shape = q.shape
+    if len(shape) != 4 or shape[3] != dim:
+        raise ValueError(f"q must be [B, T, hq, {dim}], got {list(shape)}")
+    B, T, hq, D = shape
+    if q.is_contiguous():
+        return hq * D
+    sb, stt, sh, sd = q.stride()
+    if sd != 1 or (hq > 1 and sh != D) or (B > 1 and T > 1 and sb != T * stt):
+        raise ValueError("q must have contiguous heads and one stride between tokens")
+    return stt if T > 1 else sb if B > 1 else hq * D
+
+
+def bsfp8_select_pages(q, bounds, pages, lens, count, page, nodes=None, sinks=1, recent=1, max_len=None, ws=None, selected=None,
+                       held=None):
+    """The `count` pages that each token of q bf16 [B, T, hq, dim] attends to for each key/value head: the first `sinks`, the
+    last `recent` (its own among them) and those whose bounds (bf16 [pages, heads, 2, dim]) allow the largest scores.
+
+    pages: int32 [B, W] page table; lens: int32 [B] tokens held, the new ones last; nodes: int32 [B] new tokens (None: T
+    each); page: tokens per page. -> (selected int32 [B * T, heads, count], held int32 [B * T]), as bsfp8_sparse_attention
+    takes them."""
+    if not isinstance(bounds, torch.Tensor) or bounds.dim() != 4 or bounds.shape[2] != 2 or not bounds.is_cuda:
+        raise ValueError("bounds must be a GPU tensor [pages, heads, 2, dim]")
+    dev = bounds.device
+    n_pages, heads, _, D = bounds.shape
+    ldq = _tokens_view(q, D, dev)
+    B, T, hq, _ = q.shape
+    W = _table(pages)[1]
+    max_len = W * page if max_len is None else max_len
+    if ws is None:
+        ws = workspace_select(B, T, heads, W, device=dev)
+    if selected is None:
+        selected = torch.empty((B * T, heads, count), dtype=torch.int32, device=dev)
+    if held is None:
+        held = torch.empty((B * T,), dtype=torch.int32, device=dev)
+    st = lib().bsfp8_select_pages(
+        q.data_ptr(), ldq, B, T, hq, _vec(bounds, torch.bfloat16, "bounds", bounds.shape, dev), n_pages, heads, page, D,
+        _vec(pages, torch.int32, "pages", (B, W), dev), W, _vec(lens, torch.int32, "lens", (B,), dev),
+        _vec(nodes, torch.int32, "nodes", (B,), dev) if nodes is not None else 0, max_len, count, sinks, recent,
+        _vec(ws, torch.uint8, "ws", ws.shape, dev), ws.numel(), _vec(selected, torch.int32, "selected", (B * T, heads, count), dev),
+        _vec(held, torch.int32, "held", (B * T,), dev), _stream(q))
+    _check(st, "bsfp8_select_pages")
+    return selected, held
+
+
+def bsfp8_sparse_attention(q, cache, selected, held, scale=None, ws=None, out=None):
+    """Attention of the tokens q bf16 [R, hq, dim] (any stride between tokens), each over the first held[r] positions of its
+    own pages selected[r] (int32 [R, heads, count], of bsfp8_select_pages) -> bf16 [R, hq, dim]."""
+    c = _cache(cache)
+    dev = c.device
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError(f"q must be a tensor [R, hq, {c.dim}]")
+    if not isinstance(selected, torch.Tensor) or selected.dim() != 3:
+        raise ValueError("selected must be [R, heads, count]")
+    R, hq, D = q.shape
+    ldq = _tokens_view(q.unsqueeze(1), c.dim, dev)
+    count = selected.shape[2]
+    if ws is None:
+        ws = workspace_attention(R, 1, hq, c.heads, D, count * c.page, device=dev)
+    if out is None:
+        out = torch.empty((R, hq, D), dtype=torch.bfloat16, device=dev)
+    st = lib().bsfp8_sparse_attention(q.data_ptr(), ldq, R, hq, c._ref, _vec(selected, torch.int32, "selected", (R, c.heads, count), dev),
+                                      count, _vec(held, torch.int32, "held", (R,), dev), D ** -0.5 if scale is None else scale,
+                                      _vec(ws, torch.uint8, "ws", ws.shape, dev), ws.numel(),
+                                      _vec(out, torch.bfloat16, "out", (R, hq, D), dev), _stream(q))
+    _check(st, "bsfp8_sparse_attention")
+    return out

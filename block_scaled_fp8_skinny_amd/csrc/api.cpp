@@ -221,6 +221,15 @@ int check_verify(const VerifyArgs& a, int dtype, size_t ws_bytes) {
   return BSFP8_OK;
 }
 
+// Sizes of a selection of pages: rows B * T, a table of `width` pages.
+int check_select_sizes(int64_t B, int64_t T, int64_t hkv, int64_t width) {
+  const int64_t lim = (int64_t)1 << 31;
+  if (B < 0 || T < 1 || hkv < 1 || hkv > 65536 || width < 0 || B >= lim || T >= lim || B * T >= lim) return BSFP8_ESHAPE;
+  // workgroups of up to 1024 threads, counted in 32 bits; 64 pages a workgroup along a grid's second axis
+  if (B * T * hkv >= (MAX_BLOCKS >> 2) || width > (int64_t)65535 * 64) return BSFP8_ESHAPE;
+  return BSFP8_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -691,7 +700,7 @@ int bsfp8_tree_attention(const uint16_t* q, int64_t ldq, int64_t B, int64_t T, i
   const int64_t D = cache->dim;
   if (!q || !out || !lens || (ld_pages > 0 && !pages) || !(scale - scale == 0.f)) return BSFP8_EINVAL;
   if (ldq < hq * D || ldq % 8 || !aligned16(q) || !aligned16(out)) return BSFP8_ESTRIDE;
-  const AttentionArgs a{q, ldq, B, T, hq, *cache, pages, ld_pages, lens, nodes, mask, scale, max_len, ws, out};
+  const AttentionArgs a{q, ldq, B, T, hq, *cache, pages, ld_pages, 0, lens, nodes, mask, scale, max_len, ws, out};
   if (!ws || ws_bytes < attention_ws_bytes(a) || !aligned16(ws)) return BSFP8_EWORKSPACE;
   const size_t codes = cache_codes(cache);
   if (outputs_alias({{out, (size_t)B * T * hq * D * 2}, {ws, ws_bytes}},
@@ -727,6 +736,131 @@ int bsfp8_verify_tree(const void* logits, int dtype, int64_t B, int64_t T, int64
   if (st != BSFP8_OK || B == 0) return st;
   if (!u || !path || (T > 1 && (!tokens || !parents))) return BSFP8_EINVAL;
   return launch_verify(a, true, as_stream(stream));
+}
+
+int bsfp8_residual_norm(const void* h, int64_t ldh, int h_dtype, const uint16_t* y, int64_t ldy, const uint16_t* gate,
+                        int64_t ldg, const uint16_t* post_weight, const uint16_t* weight, float scale, float eps, int64_t R,
+                        int64_t W, void* h_out, int64_t ldo, uint16_t* x_out, uint8_t* xq, uint8_t* xs, void* stream) {
+  if (h_dtype != BSFP8_OUT_BF16 && h_dtype != BSFP8_OUT_F32) return BSFP8_EINVAL;
+  if (R < 0 || R >= ((int64_t)1 << 31) || W < 8 || W % 8 || W > 32768) return BSFP8_ESHAPE;
+  if ((xq || xs) && W % 32) return BSFP8_ESHAPE;
+  if (!(eps >= 0.f) || eps > 3.4e38f || !(scale - scale == 0.f)) return BSFP8_EINVAL;
+  if ((xq != nullptr) != (xs != nullptr) || (!h_out && !x_out && !xq) || (!y && (gate || post_weight))) return BSFP8_EINVAL;
+  if (R == 0) return BSFP8_OK;
+  if (!h) return BSFP8_EINVAL;
+  const int f32 = h_dtype == BSFP8_OUT_F32;
+  const int64_t size = f32 ? 4 : 2, unit = 16 / size;
+  if (ldh < W || ldh % unit || !aligned16(h) || (h_out && (ldo < W || ldo % unit || !aligned16(h_out)))) return BSFP8_ESTRIDE;
+  if (y && (ldy < W || ldy % 8 || !aligned16(y))) return BSFP8_ESTRIDE;
+  if (gate && (ldg < 0 || (ldg > 0 && ldg < W) || ldg % 8 || !aligned16(gate))) return BSFP8_ESTRIDE;
+  if (!aligned16(post_weight) || !aligned16(weight) || !aligned16(x_out) || !aligned16(xq)) return BSFP8_ESTRIDE;
+  // h_out may be h itself (a row is read before it is written, and by its workgroup alone)
+  const bool in_place = h_out == h && ldo == ldh;
+  const size_t w = (size_t)W * 2, n = (size_t)R * W;
+  if (outputs_alias({{h_out, h_out ? ((size_t)(R - 1) * ldo + W) * size : 0}, {x_out, n * 2}, {xq, n}, {xs, n / 32}},
+                    {{in_place ? nullptr : h, ((size_t)(R - 1) * ldh + W) * size}, {y, y ? rows_span(R, ldy, W) : 0},
+                     {gate, gate ? rows_span(ldg ? R : 1, ldg, W) : 0}, {post_weight, w}, {weight, w}}))
+    return BSFP8_EINVAL;
+  const ResidualNormArgs a{h, f32, ldh, y, ldy, gate, ldg, post_weight, weight, scale, eps, R, W, h_out, ldo, x_out, xq, xs};
+  return launch_residual_norm(a, as_stream(stream));
+}
+
+int bsfp8_step_tables(const int32_t* lens, const int32_t* new_lens, int64_t B, int64_t page, int32_t* pages, int64_t ld_pages,
+                      int32_t* free_pages, int64_t capacity, int32_t* n_free, int32_t* n_free_out, int64_t R, int64_t per_seq,
+                      int64_t* slots, int64_t* positions, int32_t* seqs, int32_t* starts, int32_t* held, int32_t* counts,
+                      void* stream) {
+  const int64_t lim = (int64_t)1 << 31;
+  if (B < 0 || B > (1 << 20) || page < 1 || page >= lim || ld_pages < 0 || ld_pages >= lim || capacity < 0 || capacity >= lim)
+    return BSFP8_ESHAPE;
+  if (R < 0 || R >= lim - 4096 || per_seq < 0 || per_seq >= lim || B * ld_pages >= lim) return BSFP8_ESHAPE;
+  if (!n_free || !starts || !counts || (B > 0 && (!lens || !new_lens || !held || (ld_pages > 0 && !pages)))) return BSFP8_EINVAL;
+  if ((capacity > 0 && !free_pages) || (R > 0 && (!slots || !positions || !seqs))) return BSFP8_EINVAL;
+  if (n_free_out == n_free) n_free_out = nullptr;
+  const size_t b = (size_t)B * 4, r = (size_t)R;
+  if (outputs_alias({{pages, (size_t)(B * ld_pages) * 4}, {free_pages, (size_t)capacity * 4}, {n_free_out, 4}, {slots, r * 8},
+                     {positions, r * 8}, {seqs, r * 4}, {starts, b + 4}, {held, b}, {counts, 16}, {n_free, 4}},
+                    {{lens, b}, {new_lens, b}}))
+    return BSFP8_EINVAL;
+  const StepTablesArgs a{lens, new_lens, B, page, pages, ld_pages, free_pages, capacity, n_free, n_free_out, R, per_seq, slots,
+                         positions, seqs, starts, held, counts};
+  return launch_step_tables(a, as_stream(stream));
+}
+
+int bsfp8_cache_bounds(const bsfp8_kv_cache* cache, const int32_t* pages, int64_t ld_pages, const int32_t* lens,
+                       const int32_t* first, int64_t B, int64_t max_new, uint16_t* bounds, void* stream) {
+  const int st = check_cache(cache);
+  if (st != BSFP8_OK) return st;
+  const int64_t lim = (int64_t)1 << 31;
+  if (B < 0 || B >= lim || ld_pages < 0 || ld_pages >= lim || max_new < 0 || max_new >= lim) return BSFP8_ESHAPE;
+  if (B == 0 || max_new == 0 || ld_pages == 0 || cache->pages == 0) return BSFP8_OK;
+  const CacheBoundsArgs a{*cache, pages, ld_pages, lens, first, B, max_new, bounds};
+  const int64_t per = bounds_pages(a);
+  if (B * cache->heads >= lim || B * cache->heads >= MAX_BLOCKS * 4 / per) return BSFP8_ESHAPE;
+  if (!pages || !lens || !bounds) return BSFP8_EINVAL;
+  if (!aligned16(bounds)) return BSFP8_ESTRIDE;
+  const size_t codes = cache_codes(cache), b = (size_t)B * 4;
+  if (outputs_alias({{bounds, codes / cache->page * 4}}, {{cache->kq, codes}, {cache->ks, codes / 32}, {cache->vq, codes},
+                                                          {cache->vs, codes / 32}, {pages, b * ld_pages}, {lens, b}, {first, b}}))
+    return BSFP8_EINVAL;
+  return launch_cache_bounds(a, as_stream(stream));
+}
+
+size_t bsfp8_select_workspace_bytes(int64_t B, int64_t T, int64_t hkv, int64_t width) {
+  if (check_select_sizes(B, T, hkv, width) != BSFP8_OK || B == 0) return 0;
+  return select_ws_bytes(B, T, hkv, width < 1 ? 1 : width);
+}
+
+int bsfp8_select_pages(const uint16_t* q, int64_t ldq, int64_t B, int64_t T, int64_t hq, const uint16_t* bounds, int64_t n_pages,
+                       int64_t heads, int64_t page, int64_t dim, const int32_t* pages, int64_t ld_pages, const int32_t* lens,
+                       const int32_t* nodes, int64_t max_len, int64_t count, int64_t sinks, int64_t recent, void* ws,
+                       size_t ws_bytes, int32_t* selected, int32_t* held, void* stream) {
+  const int64_t lim = (int64_t)1 << 31;
+  if (dim != 64 && dim != 128 && dim != 192 && dim != 256) return BSFP8_ESHAPE;
+  if (page < 16 || page % 16 || page >= lim || n_pages < 0 || n_pages >= lim || n_pages * page >= lim) return BSFP8_ESHAPE;
+  if (heads < 1 || heads > 65536 || n_pages * page / 16 * heads >= lim) return BSFP8_ESHAPE;   // as the cache
+  if (hq < heads || hq % heads || hq > 64 * heads || ld_pages < 0 || ld_pages >= lim) return BSFP8_ESHAPE;
+  if (max_len < 0 || max_len > lim - (1 << 14)) return BSFP8_ESHAPE;
+  if (count < 1 || count >= lim || sinks < 0 || sinks >= lim || recent < 1 || recent >= lim || sinks + recent > count) return BSFP8_ESHAPE;
+  const int64_t bound = (max_len + page - 1) / page, width = bound < ld_pages ? bound : ld_pages;
+  int st = check_select_sizes(B, T, heads, width);
+  if (st != BSFP8_OK) return st;
+  if (count * page > lim - (1 << 14)) return BSFP8_ESHAPE;   // the length of a list, as the attention takes it
+  if (B == 0) return BSFP8_OK;
+  if (!q || (n_pages > 0 && !bounds) || (ld_pages > 0 && !pages) || !lens || !selected || !held) return BSFP8_EINVAL;
+  if (ldq < hq * dim || ldq % 8 || !aligned16(q) || !aligned16(bounds)) return BSFP8_ESTRIDE;
+  if (!ws || ws_bytes < bsfp8_select_workspace_bytes(B, T, heads, width) || !aligned16(ws)) return BSFP8_EWORKSPACE;
+  const size_t b = (size_t)B * 4;
+  if (outputs_alias({{selected, b * T * heads * count}, {held, b * T}, {ws, ws_bytes}},
+                    {{q, rows_span(B * T, ldq, hq * dim)}, {bounds, (size_t)n_pages * heads * dim * 4}, {pages, b * ld_pages},
+                     {lens, b}, {nodes, b}}))
+    return BSFP8_EINVAL;
+  const SelectPagesArgs a{q, ldq, B, T, hq, bounds, n_pages, heads, page, dim, pages, ld_pages, lens, nodes, max_len, count, sinks,
+                          recent, ws, selected, held};
+  return launch_select_pages(a, as_stream(stream));
+}
+
+int bsfp8_sparse_attention(const uint16_t* q, int64_t ldq, int64_t R, int64_t hq, const bsfp8_kv_cache* cache,
+                           const int32_t* selected, int64_t count, const int32_t* held, float scale, void* ws, size_t ws_bytes,
+                           uint16_t* out, void* stream) {
+  int st = check_cache(cache);
+  if (st != BSFP8_OK) return st;
+  const int64_t lim = (int64_t)1 << 31;
+  if (count < 1 || count >= lim || count * cache->page >= lim) return BSFP8_ESHAPE;
+  const int64_t max_len = count * cache->page, D = cache->dim;
+  st = check_attention_sizes(R, 1, hq, cache->heads, D, max_len);
+  if (st != BSFP8_OK) return st;
+  if (R == 0) return BSFP8_OK;
+  if (!q || !out || !held || !selected || !(scale - scale == 0.f)) return BSFP8_EINVAL;
+  if (ldq < hq * D || ldq % 8 || !aligned16(q) || !aligned16(out)) return BSFP8_ESTRIDE;
+  const AttentionArgs a{q, ldq, R, 1, hq, *cache, selected, cache->heads * count, count, held, nullptr, nullptr, scale, max_len,
+                        ws, out};
+  if (!ws || ws_bytes < attention_ws_bytes(a) || !aligned16(ws)) return BSFP8_EWORKSPACE;
+  const size_t codes = cache_codes(cache);
+  if (outputs_alias({{out, (size_t)R * hq * D * 2}, {ws, ws_bytes}},
+                    {{q, rows_span(R, ldq, hq * D)}, {cache->kq, codes}, {cache->ks, codes / 32}, {cache->vq, codes},
+                     {cache->vs, codes / 32}, {selected, (size_t)R * cache->heads * count * 4}, {held, (size_t)R * 4}}))
+    return BSFP8_EINVAL;
+  return launch_tree_attention(a, as_stream(stream));
 }
 
 }  // extern "C"

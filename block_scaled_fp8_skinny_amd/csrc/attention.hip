@@ -55,7 +55,7 @@ struct AttnParams {
   float* part;                                      // [nwg][2][rows of a block][D]
   float2* stat;                                     // [nwg][2][rows of a block]: m, l
   int2* owners;                                     // [items]: the workgroups of an item's first and last unit
-  int64_t ldq, ld_pages, n_pages;
+  int64_t ldq, ld_pages, ld_head, n_pages;          // ld_head: from a head's page table to the next one's (0: one for all)
   float scale2;                                     // |scale| * log2 e (1 for a scale of 0)
   uint32_t q_keep, q_flip;                          // the scale's sign, or a scale of 0, on the queries
   int B, T, hq, hkv, g, rows, mblocks, page, max_len, nwg;
@@ -196,7 +196,7 @@ __device__ __forceinline__ bool fill_table(const AttnParams& p, int b, int h, in
     const int t = t0 + i * 16;
     int entry = -1;
     if (t < len) {
-      const int at = fdiv(t, p.dpage), pg = p.pages[(int64_t)b * p.ld_pages + at];
+      const int at = fdiv(t, p.dpage), pg = p.pages[(int64_t)b * p.ld_pages + h * p.ld_head + at];
       if (pg >= 0 && pg < p.n_pages) entry = (int)((((int64_t)pg * p.hkv + h) * p.page + (t - at * p.page)) >> 4);
       else absent = true;
     }
@@ -1384,6 +1384,7 @@ int launch_tree_attention(const AttentionArgs& a, hipStream_t stream) {
   p.part = reinterpret_cast<float*>(ws + align256((size_t)pl.nwg * 2 * pl.br * sizeof(float2)));
   p.ldq = a.ldq;
   p.ld_pages = a.ld_pages;
+  p.ld_head = a.ld_head;
   p.n_pages = a.cache.pages;
   p.scale2 = a.scale == 0.f ? 1.f : (a.scale < 0.f ? -a.scale : a.scale) * 1.4426950408889634f;
   p.q_keep = a.scale == 0.f ? 0u : ~0u;
@@ -1396,7 +1397,7 @@ int launch_tree_attention(const AttentionArgs& a, hipStream_t stream) {
   p.rows = p.g * p.T;
   p.mblocks = pl.mblocks;
   p.page = (int)a.cache.page;
-  const int64_t held = a.cache.pages == 0 ? 0 : a.ld_pages * a.cache.page;
+  const int64_t held = a.cache.pages == 0 ? 0 : (a.ld_head ? a.ld_head : a.ld_pages) * a.cache.page;
   p.max_len = (int)(a.max_len < held ? a.max_len : held);
   p.nwg = pl.nwg;
   p.br = pl.br;

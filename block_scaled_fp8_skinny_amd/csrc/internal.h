@@ -128,7 +128,7 @@ struct AttentionArgs {
   int64_t ldq, B, T, hq;
   bsfp8_kv_cache cache;
   const int32_t* pages;
-  int64_t ld_pages;
+  int64_t ld_pages, ld_head;             // ld_head: entries of a head's own table (0: one table for all heads)
   const int32_t *lens, *nodes;
   const int64_t* mask;
   float scale;
@@ -151,6 +151,67 @@ struct VerifyArgs {
 };
 size_t verify_ws_bytes(int64_t B, int64_t T, int64_t V);
 int launch_verify(const VerifyArgs& a, bool tree, hipStream_t stream);
+
+// The serving step around them: the norms and the gated residual between blocks (norm.hip), page tables and slots from
+// request lengths (tables.hip), bounds of a page's keys and the selection of pages by them (sparse.hip). Arguments are
+// checked by the caller.
+struct ResidualNormArgs {
+  const void* h;
+  int f32;
+  int64_t ldh;
+  const uint16_t* y;
+  int64_t ldy;
+  const uint16_t* gate;
+  int64_t ldg;
+  const uint16_t *post_weight, *weight;
+  float scale, eps;
+  int64_t R, W;
+  void* h_out;
+  int64_t ldo;
+  uint16_t* x;
+  uint8_t *xq, *xs;
+};
+int launch_residual_norm(const ResidualNormArgs& a, hipStream_t stream);
+
+struct StepTablesArgs {
+  const int32_t *lens, *new_lens;
+  int64_t B, page;
+  int32_t* pages;
+  int64_t ld_pages;
+  int32_t* free_pages;
+  int64_t capacity;
+  int32_t *n_free, *n_free_out;          // n_free_out null: n_free in place
+  int64_t R, per_seq;
+  int64_t *slots, *positions;
+  int32_t *seqs, *starts, *held, *counts;
+};
+int launch_step_tables(const StepTablesArgs& a, hipStream_t stream);
+
+struct CacheBoundsArgs {
+  bsfp8_kv_cache cache;
+  const int32_t* pages;
+  int64_t ld_pages;
+  const int32_t *lens, *first;
+  int64_t B, max_new;
+  uint16_t* bounds;
+};
+int64_t bounds_pages(const CacheBoundsArgs& a);
+int launch_cache_bounds(const CacheBoundsArgs& a, hipStream_t stream);
+
+struct SelectPagesArgs {
+  const uint16_t* q;
+  int64_t ldq, B, T, hq;
+  const uint16_t* bounds;
+  int64_t n_pages, heads, page, dim;
+  const int32_t* pages;
+  int64_t ld_pages;
+  const int32_t *lens, *nodes;
+  int64_t max_len, count, sinks, recent;
+  void* ws;
+  int32_t *selected, *held;
+};
+size_t select_ws_bytes(int64_t B, int64_t T, int64_t hkv, int64_t width);
+int launch_select_pages(const SelectPagesArgs& a, hipStream_t stream);
 
 inline int hip_status(hipError_t err) { return err == hipSuccess ? BSFP8_OK : BSFP8_EHIP; }
 

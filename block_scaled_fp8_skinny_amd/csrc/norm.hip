@@ -1,0 +1,248 @@
+// The norms and the gated residual between two blocks, for gfx950 (MI355X):
+//   z  = y * rsqrt(mean(y^2) + eps) * post     (without `post`: y)
+//   h' = h + scale * gate * z
+//   x  = h' * rsqrt(mean(h'^2) + eps) * weight, as bf16 and as MXFP8
+// in fp32, rounded once where it is stored: x is the norm of h' before its rounding.
+//
+// A row is held in registers by a workgroup (or by one wave, if it is short), so every value is read and written once; the
+// two means are the only exchanges. HBM bounds many rows, the latency of one chain (load, two sums, store) few. A
+// workgroup keeps the weights of its columns for all its rows and asks for the next row before it computes this one.
+
+#include "lanes.h"
+
+namespace bsfp8 {
+namespace {
+
+struct NormParams {
+  const void* h;
+  const uint16_t *y, *gate, *post, *weight;
+  void* h_out;
+  uint16_t* x;
+  uint8_t *xq, *xs;
+  int64_t ldh, ldy, ldg, ldo, R;
+  float scale, eps, inv_w;
+  int W;
+};
+
+__device__ __forceinline__ void unpack8(const u32x4_t& r, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(r[i] << 16);
+    x[2 * i + 1] = __uint_as_float(r[i] & 0xFFFF0000u);
+  }
+}
+
+// Eight values of a row that a thread holds, as they are loaded.
+template <bool F32>
+struct Held {
+  u32x4_t h[F32 ? 2 : 1], y, g;
+};
+
+// V groups of eight values a thread; SHARED: the workgroup is one row's (else each wave has its own).
+template <bool F32, int V, bool SHARED>
+__global__ void __launch_bounds__(SHARED ? 1024 : 256) residual_norm_kernel(NormParams p) {
+  __shared__ float sums[2][16];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int waves = SHARED ? blockDim.x >> 6 : 1, threads = SHARED ? blockDim.x : 64;
+  const int t = SHARED ? threadIdx.x : lane;
+  int64_t r = SHARED ? blockIdx.x : (int64_t)blockIdx.x * 4 + wave;
+  const int64_t step = SHARED ? gridDim.x : (int64_t)gridDim.x * 4;
+  int col[V];
+  bool on[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    col[v] = (v * threads + t) * 8;
+    on[v] = col[v] < p.W;
+  }
+  const u32x4_t none = {0, 0, 0, 0};
+  auto load8 = [&](const uint16_t* src, int v) { return on[v] ? *reinterpret_cast<const u32x4_t*>(src + col[v]) : none; };
+  const bool gates = p.gate != nullptr && p.ldg != 0;   // a row of gates for each row
+  auto load = [&](int64_t row, Held<F32> (&d)[V]) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if constexpr (F32) {
+        const float* src = reinterpret_cast<const float*>(p.h) + row * p.ldh + col[v];
+        d[v].h[0] = on[v] ? *reinterpret_cast<const u32x4_t*>(src) : none;
+        d[v].h[1] = on[v] ? *reinterpret_cast<const u32x4_t*>(src + 4) : none;
+      } else {
+        d[v].h[0] = load8(reinterpret_cast<const uint16_t*>(p.h) + row * p.ldh, v);
+      }
+      d[v].y = p.y ? load8(p.y + row * p.ldy, v) : none;
+      d[v].g = gates ? load8(p.gate + row * p.ldg, v) : none;
+    }
+  };
+  // the sum over the row; a call's slot is free again two calls later, with a barrier of the next one between
+  int turn = 0;
+  auto total = [&](float s) {
+    s = wave_reduce(s, [](float a, float b) { return a + b; });
+    if (!SHARED || waves == 1) return s;
+    turn ^= 1;
+    if (lane == 0) sums[turn][wave] = s;
+    __syncthreads();
+    s = sums[turn][0];
+    for (int w = 1; w < waves; ++w) s += sums[turn][w];
+    return s;
+  };
+
+  Held<F32> now[V];
+  if (r < p.R) load(r, now);
+  u32x4_t wv[V], pv[V], gv[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    wv[v] = p.weight ? load8(p.weight, v) : none;
+    pv[v] = p.post ? load8(p.post, v) : none;
+    gv[v] = p.gate && !gates ? load8(p.gate, v) : none;
+  }
+  for (; r < p.R; r += step) {
+    float h[V][8], z[V][8];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      if constexpr (F32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[v][i] = __uint_as_float(now[v].h[i >> 2][i & 3]);
+      } else {
+        unpack8(now[v].h[0], h[v]);
+      }
+      unpack8(now[v].y, z[v]);
+    }
+    u32x4_t gate[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) gate[v] = gates ? now[v].g : gv[v];
+    if (r + step < p.R) load(r + step, now);
+    if (p.y) {
+      if (p.post) {
+        float s = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s += z[v][i] * z[v][i];
+        const float inv = rsqrtf(total(s) * p.inv_w + p.eps);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          float w[8];
+          unpack8(pv[v], w);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) z[v][i] = z[v][i] * inv * w[i];
+        }
+      }
+      if (p.gate) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          float g[8];
+          unpack8(gate[v], g);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) z[v][i] *= g[i];
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[v][i] = on[v] ? fmaf(p.scale, z[v][i], h[v][i]) : 0.f;
+    }
+    if (p.h_out) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (!on[v]) continue;
+        if constexpr (F32) {
+          f32x4_t* dst = reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(p.h_out) + r * p.ldo + col[v]);
+          dst[0] = f32x4_t{h[v][0], h[v][1], h[v][2], h[v][3]};
+          dst[1] = f32x4_t{h[v][4], h[v][5], h[v][6], h[v][7]};
+        } else {
+          *reinterpret_cast<u32x4_t*>(reinterpret_cast<uint16_t*>(p.h_out) + r * p.ldo + col[v]) =
+              u32x4_t{pack_bf16x2(h[v][0], h[v][1]), pack_bf16x2(h[v][2], h[v][3]), pack_bf16x2(h[v][4], h[v][5]),
+                      pack_bf16x2(h[v][6], h[v][7])};
+        }
+      }
+    }
+    if (!p.x && !p.xq) continue;                    // uniform
+    float s = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s += h[v][i] * h[v][i];
+    const float inv = rsqrtf(total(s) * p.inv_w + p.eps);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float w[8];
+      unpack8(wv[v], w);
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = p.weight ? h[v][i] * inv * w[i] : h[v][i] * inv;
+      if (p.x && on[v])
+        *reinterpret_cast<u32x4_t*>(p.x + r * p.W + col[v]) =
+            u32x4_t{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7])};
+      if (!p.xq) continue;                          // uniform
+      // the rule of quantize_mx_kernel on the fp32 values; a block is four neighbouring lanes (W % 32 == 0)
+      uint32_t amax = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+      amax = max(amax, dpp<XOR1>(amax));
+      amax = max(amax, dpp<XOR2>(amax));
+      const int E = (int)(amax >> 23), e = max(E == 0 ? -127 : E - 135, -127);
+      uint32_t c[2];
+      if (E != 255) {
+        float q[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = fminf(fmaxf(ldexpf(x[i], -e), -448.f), 448.f);
+        c[0] = e4m3x4(q[0], q[1], q[2], q[3]);
+        c[1] = e4m3x4(q[4], q[5], q[6], q[7]);
+      } else {                                      // NaN codes carrying each value's sign
+        c[0] = c[1] = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i >> 2] |= ((__float_as_uint(x[i]) >> 31) ? 0xFFu : 0x7Fu) << (8 * (i & 3));
+      }
+      if (on[v]) {
+        *reinterpret_cast<uint2*>(p.xq + r * p.W + col[v]) = make_uint2(c[0], c[1]);
+        if ((t & 3) == 0) p.xs[r * (p.W / 32) + col[v] / 32] = E != 255 ? (uint8_t)(e + 127) : (uint8_t)255;
+      }
+    }
+  }
+}
+
+template <bool F32>
+int launch(const NormParams& p, hipStream_t stream) {
+  const int groups = p.W / 8;
+  if (groups <= 128) {                              // a wave holds the row: four rows a workgroup
+    const int64_t want = (p.R + 3) / 4;
+    const dim3 grid((unsigned)(want < 2048 ? want : 2048));
+    if (groups <= 64) hipLaunchKernelGGL((residual_norm_kernel<F32, 1, false>), grid, dim3(256), 0, stream, p);
+    else hipLaunchKernelGGL((residual_norm_kernel<F32, 2, false>), grid, dim3(256), 0, stream, p);
+    return hip_status(hipGetLastError());
+  }
+  const int v = groups <= 256 ? 1 : groups <= 2048 ? 2 : 4;
+  const int threads = ((groups + v - 1) / v + 63) / 64 * 64;
+  // as many workgroups as the GPU holds at once (2048 threads a CU, 128 registers each)
+  const int64_t most = 256 * (1024 / threads > 0 ? 1024 / threads : 1);
+  const dim3 grid((unsigned)(p.R < most ? p.R : most));
+  if (v == 1) hipLaunchKernelGGL((residual_norm_kernel<F32, 1, true>), grid, dim3(threads), 0, stream, p);
+  else if (v == 2) hipLaunchKernelGGL((residual_norm_kernel<F32, 2, true>), grid, dim3(threads), 0, stream, p);
+  else hipLaunchKernelGGL((residual_norm_kernel<F32, 4, true>), grid, dim3(threads), 0, stream, p);
+  return hip_status(hipGetLastError());
+}
+
+}  // namespace
+
+int launch_residual_norm(const ResidualNormArgs& a, hipStream_t stream) {
+  NormParams p{};
+  p.h = a.h;
+  p.y = a.y;
+  p.gate = a.gate;
+  p.post = a.post_weight;
+  p.weight = a.weight;
+  p.h_out = a.h_out;
+  p.x = a.x;
+  p.xq = a.xq;
+  p.xs = a.xs;
+  p.ldh = a.ldh;
+  p.ldy = a.ldy;
+  p.ldg = a.ldg;
+  p.ldo = a.ldo;
+  p.R = a.R;
+  p.scale = a.scale;
+  p.eps = a.eps;
+  p.inv_w = (float)(1.0 / (double)a.W);
+  p.W = (int)a.W;
+  return a.f32 ? launch<true>(p, stream) : launch<false>(p, stream);
+}
+
+}  // namespace bsfp8

@@ -18,12 +18,11 @@
 // Times: 32 chains of 6 over 131072 columns, 36 us for the pairs (184 MB at 5.1 TB/s, the vector ALUs 84% busy with the
 // exponentials: bf16 logits take as long) and 18 for the rest, of which 8 are its chain of dependent loads (a single chain's
 // 8.3) and the others the second look at the refused rows; 16 trees of 32 nodes over 32768 columns 15 and 6.5 us.
-#include "device.h"
+#include "logits.h"
 
 namespace bsfp8 {
 namespace {
 
-constexpr int PIECE = 1024;                         // elements a wave holds: 16 per lane
 constexpr int MAX_T = 64;
 
 struct Pair {                                       // one piece of a row: 16 bytes
@@ -44,203 +43,6 @@ struct VerifyParams {
   int share;                                        // vectors of a refused row that a wave sums: 1, or a whole piece's
 };
 
-// The element type's 16-byte vectors, and how many a piece has per lane.
-template <typename T> struct Vec;
-template <> struct Vec<float> {
-  static constexpr int E = 4, N = PIECE / 256;
-  static __device__ __forceinline__ void get(const u32x4_t& r, float (&x)[E]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(r[i]);
-  }
-};
-template <> struct Vec<uint16_t> {
-  static constexpr int E = 8, N = PIECE / 512;
-  static __device__ __forceinline__ void get(const u32x4_t& r, float (&x)[E]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(r[i] << 16);
-      x[2 * i + 1] = __uint_as_float(r[i] & 0xFFFF0000u);
-    }
-  }
-};
-
-constexpr float NEG_INF = -__builtin_inff();
-
-// What a lane loads of a vector: its 16 bytes and, in a bf16 row that starts in the middle of a 4-byte word, the word
-// after them.
-struct Words {
-  u32x4_t w;
-  uint32_t next;
-};
-
-// A wave's view of one row of V elements: word w, element i is row element w * E + i wherever the row starts in memory, so
-// that rows of equal logits are summed in the same order and their probabilities cancel. Buffer loads need 4-byte
-// addresses; a bf16 row of an odd start is read from the element before it and shifted by half a word. Elements
-// past the row's end (the neighbouring row's) read as -inf. The descriptor ends with the row's last whole 4-byte word, so
-// nothing past the row is read; a bf16 row's last element in half a word is read by itself.
-template <typename T>
-struct Row {
-  static constexpr int E = Vec<T>::E, N = Vec<T>::N;
-  __amdgpu_buffer_rsrc_t r;
-  int V;
-  bool odd, half;
-  float last;
-  __device__ __forceinline__ Row(const void* base, int64_t row, int V_) : V(V_), odd(false), half(false), last(0.f) {
-    const int64_t first = row * V_;
-    const T* const at = reinterpret_cast<const T*>(base) + first;
-    if constexpr (sizeof(T) == 2) {
-      odd = first & 1;
-      half = (odd + V_) & 1;
-      if (half) last = __uint_as_float((uint32_t)at[V_ - 1] << 16);
-    }
-    r = __builtin_amdgcn_make_buffer_rsrc((void*)(at - odd), 0, (odd + V_) * (int)sizeof(T) & ~3, RSRC_WORD3);
-  }
-  __device__ __forceinline__ Words load(int piece, int lane, int v) const {
-    const int at = index(piece, lane, v, 0) * (int)sizeof(T);
-    Words w;
-    w.w = __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 0);
-    w.next = 0;
-    if constexpr (sizeof(T) == 2)
-      if (odd) w.next = __builtin_amdgcn_raw_buffer_load_b32(r, at + 16, 0, 0);   // uniform
-    return w;
-  }
-  __device__ __forceinline__ void load(int piece, int lane, Words (&w)[N]) const {
-#pragma unroll
-    for (int v = 0; v < N; ++v) w[v] = load(piece, lane, v);
-  }
-  __device__ __forceinline__ int index(int piece, int lane, int v, int i) const {
-    return (piece * (PIECE / E) + v * 64 + lane) * E + i;
-  }
-  // A vector's elements; outside the row: -inf. NaN stays (it loses every maximum, and weighs nothing).
-  __device__ __forceinline__ void get(const Words& from, int piece, int lane, int v, float (&x)[E]) const {
-    u32x4_t w = from.w;
-    if constexpr (sizeof(T) == 2) {
-      if (odd) {                                    // uniform
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = __builtin_amdgcn_alignbit(i < 3 ? from.w[i + 1] : from.next, from.w[i], 16);
-      }
-    }
-    Vec<T>::get(w, x);
-    if ((piece + 1) * PIECE > V) {                  // the row's end (uniform)
-      const int at = index(piece, lane, v, 0);
-#pragma unroll
-      for (int i = 0; i < E; ++i) x[i] = half && at + i == V - 1 ? last : at + i < V ? x[i] : NEG_INF;
-    }
-  }
-  __device__ __forceinline__ void get(const Words (&w)[N], int piece, int lane, float (&x)[N][E]) const {
-#pragma unroll
-    for (int v = 0; v < N; ++v) get(w[v], piece, lane, v, x[v]);
-  }
-};
-
-template <typename T>
-__device__ __forceinline__ float element(const void* base, int64_t at) {
-  if constexpr (sizeof(T) == 4) return reinterpret_cast<const float*>(base)[at];
-  else return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(base)[at] << 16);
-}
-
-// exp(y) = 2^n 2^(j/64) e^r with y = (64 n + j) ln2 / 64 + r: the table's 64 powers (in LDS) and the Taylor
-// polynomial of degree 5 (|r| <= ln2 / 128, next term below 2^-54). Some 20 instructions, where the
-// library's exp takes three times as many.
-__device__ const double POWERS[64] = {
-    0x1.0000000000000p+0, 0x1.02c9a3e778061p+0, 0x1.059b0d3158574p+0, 0x1.0874518759bc8p+0,
-    0x1.0b5586cf9890fp+0, 0x1.0e3ec32d3d1a2p+0, 0x1.11301d0125b51p+0, 0x1.1429aaea92de0p+0,
-    0x1.172b83c7d517bp+0, 0x1.1a35beb6fcb75p+0, 0x1.1d4873168b9aap+0, 0x1.2063b88628cd6p+0,
-    0x1.2387a6e756238p+0, 0x1.26b4565e27cddp+0, 0x1.29e9df51fdee1p+0, 0x1.2d285a6e4030bp+0,
-    0x1.306fe0a31b715p+0, 0x1.33c08b26416ffp+0, 0x1.371a7373aa9cbp+0, 0x1.3a7db34e59ff7p+0,
-    0x1.3dea64c123422p+0, 0x1.4160a21f72e2ap+0, 0x1.44e086061892dp+0, 0x1.486a2b5c13cd0p+0,
-    0x1.4bfdad5362a27p+0, 0x1.4f9b2769d2ca7p+0, 0x1.5342b569d4f82p+0, 0x1.56f4736b527dap+0,
-    0x1.5ab07dd485429p+0, 0x1.5e76f15ad2148p+0, 0x1.6247eb03a5585p+0, 0x1.6623882552225p+0,
-    0x1.6a09e667f3bcdp+0, 0x1.6dfb23c651a2fp+0, 0x1.71f75e8ec5f74p+0, 0x1.75feb564267c9p+0,
-    0x1.7a11473eb0187p+0, 0x1.7e2f336cf4e62p+0, 0x1.82589994cce13p+0, 0x1.868d99b4492edp+0,
-    0x1.8ace5422aa0dbp+0, 0x1.8f1ae99157736p+0, 0x1.93737b0cdc5e5p+0, 0x1.97d829fde4e50p+0,
-    0x1.9c49182a3f090p+0, 0x1.a0c667b5de565p+0, 0x1.a5503b23e255dp+0, 0x1.a9e6b5579fdbfp+0,
-    0x1.ae89f995ad3adp+0, 0x1.b33a2b84f15fbp+0, 0x1.b7f76f2fb5e47p+0, 0x1.bcc1e904bc1d2p+0,
-    0x1.c199bdd85529cp+0, 0x1.c67f12e57d14bp+0, 0x1.cb720dcef9069p+0, 0x1.d072d4a07897cp+0,
-    0x1.d5818dcfba487p+0, 0x1.da9e603db3285p+0, 0x1.dfc97337b9b5fp+0, 0x1.e502ee78b3ff6p+0,
-    0x1.ea4afa2a490dap+0, 0x1.efa1bee615a27p+0, 0x1.f50765b6e4540p+0, 0x1.fa7c1819e90d8p+0,
-};
-__device__ __forceinline__ void load_powers(double* lds) {
-  if (threadIdx.x < 64) lds[threadIdx.x] = POWERS[threadIdx.x];
-}
-
-// Weights exp((x - M) / t) of one row, for x <= M. it = 1 / t.
-struct Weights {
-  double c;                                         // 64 it / ln2
-  float M;
-  const double* powers;
-  __device__ __forceinline__ Weights(float M_, double it, const double* powers_) : M(M_), powers(powers_) {
-    c = it * 0x1.71547652b82fep+6;                  // 64 / ln 2
-  }
-  // never 0: what is too small (also -inf and NaN) gives 2^-1022, which no sum with a maximum of 1 notices
-  __device__ __forceinline__ double some(float x) const {
-    const double z = fmax(((double)x - (double)M) * c, -1022.0 * 64);
-    const double t = z + 0x1.8p52, r = z - (t - 0x1.8p52);
-    const int n = (int)(uint32_t)__builtin_bit_cast(uint64_t, t);
-    double q = fma(r, 0x1.5d87fe78a6731p-40, 0x1.3b2ab6fba4e77p-31);
-    q = fma(r, q, 0x1.c6b08d704a0c0p-23);
-    q = fma(r, q, 0x1.ebfbdff82c58fp-15);
-    q = fma(r, q, 0x1.62e42fefa39efp-7);
-    const double w = powers[n & 63];
-    const uint64_t b = __builtin_bit_cast(uint64_t, fma(w, r * q, w));
-    return __builtin_bit_cast(double, b + ((uint64_t)(uint32_t)(n >> 6) << 52));
-  }
-  // 0 for -inf, NaN and what falls below 2^-1000; 1 for the maximum itself (also an infinite one)
-  __device__ __forceinline__ double operator()(float x) const {
-    const double w = some(x);
-    return x == M ? 1.0 : w > 0x1p-1000 ? w : 0.0;
-  }
-};
-
-// Lane exchanges in the vector unit (DPP inside a row of 16, then the row swaps): a tenth of the latency of
-// an LDS permute, and these kernels' second launch is one long chain of them.
-template <int CTRL, int ROWS = 0xF>
-__device__ __forceinline__ uint32_t dpp(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
-}
-template <int CTRL, int ROWS = 0xF>
-__device__ __forceinline__ double dpp(double v) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  return __builtin_bit_cast(double, (uint64_t)dpp<CTRL, ROWS>((uint32_t)(b >> 32)) << 32 | dpp<CTRL, ROWS>((uint32_t)b));
-}
-constexpr int XOR1 = 0xB1, XOR2 = 0x4E, HALF_MIRROR = 0x141, MIRROR = 0x140, SHR = 0x110, BCAST15 = 0x142, BCAST31 = 0x143;
-
-// f over all lanes of the wave; f is associative and commutative
-template <typename F>
-__device__ __forceinline__ float wave_reduce(float v, F f) {
-  auto step = [&](uint32_t o) { v = f(v, __uint_as_float(o)); };
-  step(dpp<XOR1>(__float_as_uint(v)));
-  step(dpp<XOR2>(__float_as_uint(v)));
-  step(dpp<HALF_MIRROR>(__float_as_uint(v)));
-  step(dpp<MIRROR>(__float_as_uint(v)));
-  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = f(__uint_as_float(r[0]), __uint_as_float(r[1]));
-  r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return f(__uint_as_float(r[0]), __uint_as_float(r[1]));
-}
-__device__ __forceinline__ float wave_max(float v) {
-  return wave_reduce(v, [](float a, float b) { return fmaxf(a, b); });
-}
-__device__ __forceinline__ double from_lane(double v, int lane) {        // uniform lane
-  const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)b, lane), hi = __builtin_amdgcn_readlane((uint32_t)(b >> 32), lane);
-  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
-__device__ __forceinline__ double wave_scan(double v) {                 // inclusive
-  v += dpp<SHR + 1>(v);
-  v += dpp<SHR + 2>(v);
-  v += dpp<SHR + 4>(v);
-  v += dpp<SHR + 8>(v);
-  v += dpp<BCAST15, 0xA>(v);
-  v += dpp<BCAST31, 0xC>(v);
-  return v;
-}
-__device__ __forceinline__ double wave_sum(double v) { return from_lane(wave_scan(v), 63); }
-
-// 1 / t (0 for an infinite one: equal weights), or -1 for a greedy row (t = 0, negative or NaN).
-__device__ __forceinline__ double inv_temperature(float t) { return t > 0.f ? 1.0 / (double)t : -1.0; }
-__device__ __forceinline__ bool is_greedy(double it) { return it < 0; }
-
 // The pairs of every piece of every row (blockIdx.x; rows of sequence b: the target's b * T + i, then the
 // draft's B * T + b * (T - 1) + i).
 template <typename T>
@@ -254,7 +56,7 @@ __global__ void __launch_bounds__(256) verify_pairs_kernel(VerifyParams p) {
   if (row < p.B && blockIdx.y == 0 && threadIdx.x == 0) p.counters[row] = 0;
   const bool is_draft = row >= targets;
   const int local = is_draft ? row - targets : row;
-  const Row<T> r(is_draft ? p.draft : p.logits, local, p.V);
+  const Row<T> r(is_draft ? p.draft : p.logits, (int64_t)local * p.V, p.V);
   Words w[N];
   r.load(piece, lane, w);                           // (past the row's end: nothing is read)
   load_powers(powers);
@@ -437,7 +239,7 @@ struct Residual {
   double ip, iq;                                    // 1 / S
   __device__ __forceinline__ Residual(const VerifyParams& p, int64_t prow, int64_t qrow, const Total& tp, const Total& tq,
                                       double it, const double* powers)
-      : rp(p.logits, prow, p.V), rq(p.draft, qrow, p.V), fp(tp.M, it, powers), fq(tq.M, it, powers) {
+      : rp(p.logits, prow * p.V, p.V), rq(p.draft, qrow * p.V, p.V), fp(tp.M, it, powers), fq(tq.M, it, powers) {
     ip = 1.0 / tp.S;
     iq = tq.S > 0 ? 1.0 / tq.S : 0.0;
   }
@@ -457,20 +259,6 @@ struct Residual {
     }
   }
 };
-
-// The arrival of a workgroup at a sequence's counter: true for the last of `n`, which sees what the others
-// stored before theirs (whole workgroup). What is handed over is stored and
-// loaded by relaxed device-scope atomics only, which pass the XCDs' L2s by, so it is enough that each wave
-// waits for its stores' completion before the count: a release fence would also write back the whole L2 of
-// the XCD, once per workgroup (32 sequences' chains over 131072 columns took 57 us with it).
-__device__ __forceinline__ bool last_to_arrive(int* counter, int n, int* shared) {
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __syncthreads();
-  if (threadIdx.x == 0)
-    *shared = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == n - 1;
-  __syncthreads();
-  return *shared != 0;
-}
 
 template <typename T>
 __global__ void __launch_bounds__(256, 4) verify_chain_kernel(VerifyParams p) {
@@ -534,7 +322,7 @@ __global__ void __launch_bounds__(256, 4) verify_chain_kernel(VerifyParams p) {
     int n = 0;
     for (; n < D && (oks >> n & 1); ++n) {
       if (greedy) {
-        const Row<T> r(p.logits, (int64_t)b * p.T + n, p.V);
+        const Row<T> r(p.logits, ((int64_t)b * p.T + n) * p.V, p.V);
         if (pick_greedy(r, target_pairs + (int64_t)n * p.pieces, p.pieces, lane, totals[n].M) !=
             __builtin_amdgcn_readlane(x, n))
           break;
@@ -624,7 +412,7 @@ __global__ void __launch_bounds__(256, 4) verify_chain_kernel(VerifyParams p) {
     return;
   }
   if (next < 0)
-    next = pick_row(Row<T>(p.logits, prow, p.V), target_pairs + (int64_t)n * p.pieces, p.pieces, lane, tp, it, p.u_sample[b],
+    next = pick_row(Row<T>(p.logits, prow * p.V, p.V), target_pairs + (int64_t)n * p.pieces, p.pieces, lane, tp, it, p.u_sample[b],
                     powers);
   if (lane < p.T) p.out_tokens[(int64_t)b * p.T + lane] = lane < n ? x : lane == n ? next : -1;
   if (lane == 0) p.n_accepted[b] = n;
@@ -646,7 +434,7 @@ __global__ void __launch_bounds__(256) verify_tree_kernel(VerifyParams p) {
     const Pair* pr = p.pairs + row * p.pieces;
     const float u = p.u[row];
     const Total t = row_total(pr, first_pairs(pr, p.pieces, lane), p.pieces, lane, it, powers);
-    const int x = pick_row(Row<T>(p.logits, row, p.V), pr, p.pieces, lane, t, it, u, powers);
+    const int x = pick_row(Row<T>(p.logits, row * p.V, p.V), pr, p.pieces, lane, t, it, u, powers);
     if (lane == 0) __hip_atomic_store(sampled + i, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
   if (!last_to_arrive(p.counters + b, gridDim.y, &shared_last) || wave != 0) return;

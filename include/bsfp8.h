@@ -462,6 +462,105 @@ BSFP8_API int bsfp8_verify_tree(const void* logits, int dtype, int64_t B, int64_
                                 size_t ws_bytes, int32_t* out_tokens, int32_t* path, int32_t* n_accepted,
                                 void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * The serving step around the cache, the attention and the GEMM (per call, asynchronous, no allocation): the norms and
+ * the gated residual between two blocks, page tables and slots from request lengths, attention over the pages that
+ * bounds of their keys select, and sampling.
+ * ------------------------------------------------------------------------------------------ */
+
+/* The norms before and after a block with its gate and residual scale, in fp32 from the inputs:
+ *   z  = y * 1/sqrt(mean(y^2) + eps) * post_weight   (post_weight NULL: z = y)
+ *   h' = h + scale * gate * z                        (gate NULL: 1; y NULL: h' = h)
+ *   x  = h' * 1/sqrt(mean(h'^2) + eps) * weight      (weight NULL: 1), of h' before it is rounded
+ *   h, h_out : [R][ldh], [R][ldo], bf16 (uint16_t) or float per h_dtype (bsfp8_out; 16-byte aligned; row strides >= W, whole
+ *              16 bytes). h_out may be NULL, or h itself with the same stride (in place).
+ *   y, gate  : bf16 [R][ldy], [R][ldg] (16-byte aligned, strides multiples of 8), NULL as above (a gate or a post_weight
+ *              needs y); ldg = 0: one row of gates for all.
+ *   post_weight, weight : bf16 [W] (16-byte aligned), nullable. eps >= 0 and finite, scale finite.
+ *   x_out    : bf16 [R][W] (contiguous, 16-byte aligned), nullable.
+ *   xq, xs   : e4m3 codes [R][W] (16-byte aligned) and scale bytes [R][W/32], the rule of bsfp8_quantize_mx on the fp32
+ *              values; both or neither. W % 32 == 0 with them.
+ * W a multiple of 8 up to 32768; R < 2^31; at least one output. Means are sums of fp32 squares: rows of values past 2^63
+ * overflow them. The order of the sums depends on W only. */
+BSFP8_API int bsfp8_residual_norm(const void* h, int64_t ldh, int h_dtype, const uint16_t* y, int64_t ldy,
+                                  const uint16_t* gate, int64_t ldg, const uint16_t* post_weight, const uint16_t* weight,
+                                  float scale, float eps, int64_t R, int64_t W, void* h_out, int64_t ldo, uint16_t* x_out,
+                                  uint8_t* xq, uint8_t* xs, void* stream);
+
+/* Page tables, slots and positions of a step's tokens from the requests' lengths, and the stack of free pages.
+ * Request b holds lens[b] tokens in its first had = ceil(lens[b] / page) pages and will hold new_lens[b] (negative ones count
+ * as 0). Where it shrinks (drafts refused, a request ended: 0), the pages past ceil(new_lens[b] / page) go back on top of the
+ * stack, requests in order and their pages in order; where it grows (a token decoded, drafts, a prompt), the pages that
+ * it lacks are taken from the top after that, requests in order and their pages in order.
+ *   pages      : int32_t [B][ld_pages] (device, updated): entries of pages taken are written, no others. Each page belongs
+ *                to one request and stands once in tables and stack together.
+ *   free_pages : int32_t [capacity] (device, updated): the stack, its lowest n_free[0] entries. n_free_out (int32_t [1]): its
+ *                height after the call, or NULL (or n_free): n_free is updated in place, by a launch of its own.
+ *   Rows (tokens added): packed, request b's at [starts[b], starts[b + 1]); with per_seq > 0 its token t in row
+ *   b * per_seq + t (those past per_seq have none).
+ *   slots, positions : int64_t [R] (device): as bsfp8_cache_write takes them. seqs: int32_t [R]: the request. A row without a
+ *                token gets slot -1, position 0, seq -1; rows past R are not written.
+ *   starts     : int32_t [B + 1]: tokens added before each request. held: int32_t [B]: tokens that the request has pages
+ *                for: new_lens[b] unless pages ran out (or the table's width did); pass it as the next call's lens.
+ *   counts     : int32_t [4]: tokens added, pages taken, pages given back, pages lacking.
+ * A page lacking has entry -1 in the table (none past its width) and its tokens slot -1. B <= 2^20, page >= 1,
+ * B * ld_pages < 2^31, R < 2^31 - 4096; starts and counts end at 2^31 - 1. Nothing of a request's table is read but the pages of lens[b].
+ * Outputs must not overlap inputs or each other (BSFP8_EINVAL). */
+BSFP8_API int bsfp8_step_tables(const int32_t* lens, const int32_t* new_lens, int64_t B, int64_t page, int32_t* pages,
+                                int64_t ld_pages, int32_t* free_pages, int64_t capacity, int32_t* n_free,
+                                int32_t* n_free_out, int64_t R, int64_t per_seq, int64_t* slots, int64_t* positions,
+                                int32_t* seqs, int32_t* starts, int32_t* held, int32_t* counts, void* stream);
+
+/* Bounds of the keys of a cache's pages: bounds bf16 [pages][heads][2][dim] (device, 16-byte aligned), [0] the least and
+ * [1] the largest value of each key dimension over a page's tokens, exactly (as bsfp8_cache_read gives them). Where a token
+ * has a NaN, both are NaN. Computed anew, from the cache, for every page that holds one of the positions
+ * [first[b], lens[b]) of a sequence, over all of its positions below lens[b]; other pages' bounds are not touched.
+ *   pages, ld_pages, lens : as bsfp8_tree_attention (lens cut to [0, ld_pages * page]); a page outside the cache is skipped.
+ *   first   : int32_t [B] (device): the first position that is new, or NULL: 0.
+ *   max_new : a bound of lens[b] - first[b]: positions before lens[b] - max_new count as not new.
+ * A page that two sequences share has to hold the same positions of both (a whole page of a shared prefix).
+ * B * heads times the pages that max_new positions can touch < 2^26. */
+BSFP8_API int bsfp8_cache_bounds(const bsfp8_kv_cache* cache, const int32_t* pages, int64_t ld_pages, const int32_t* lens,
+                                 const int32_t* first, int64_t B, int64_t max_new, uint16_t* bounds, void* stream);
+
+/* Workspace bytes of bsfp8_select_pages for these sizes or smaller ones (0 for sizes it refuses), width = the lesser of
+ * ld_pages and max_len / page, rounded up. The contents need no clearing; one workspace must not be used by two calls that
+ * can run at the same time. */
+BSFP8_API size_t bsfp8_select_workspace_bytes(int64_t B, int64_t T, int64_t hkv, int64_t width);
+
+/* The pages that each token of a step attends to, by the bounds of their keys. Token t of sequence b sees the
+ * n = lens[b] - nodes[b] + t + 1 positions up to its own (a chain; T = 1 is plain decoding), in N = ceil(n / page) pages. For
+ * each key/value head it gets all of them if N <= count; else the first `sinks`, the last `recent` and, of the others, the
+ * count - sinks - recent with the largest score, the earlier page first among equals. A page's score is the largest, over the
+ * query heads that share the key/value head, of
+ *   sum_d max(q_d kmin_d, q_d kmax_d),
+ * at least every q . k of its keys; infinite where a query value or bound is not finite. A page outside [0, n_pages) comes
+ * after all others. Scores are summed in 64 bits. (For a negative scale of the attention, negate the queries.)
+ *   q, ldq, B, T, hq, pages, ld_pages, lens, nodes, max_len : as bsfp8_tree_attention.
+ *   bounds   : of bsfp8_cache_bounds; n_pages, heads, page, dim: the cache's.
+ *   selected : int32_t [B * T][heads][count] (device): the pages as the table names them, in the order of their positions;
+ *              -1 for a page outside the cache, and past the last one.
+ *   held     : int32_t [B * T] (device): the positions in a list that the token sees: whole pages up to its own, the last; 0
+ *              for t >= nodes[b].
+ * sinks >= 0, recent >= 1, sinks + recent <= count, count * page <= 2^31 - 2^14, B * T * heads < 2^22 and at most
+ * 65535 * 64 pages a sequence. */
+BSFP8_API int bsfp8_select_pages(const uint16_t* q, int64_t ldq, int64_t B, int64_t T, int64_t hq, const uint16_t* bounds,
+                                 int64_t n_pages, int64_t heads, int64_t page, int64_t dim, const int32_t* pages,
+                                 int64_t ld_pages, const int32_t* lens, const int32_t* nodes, int64_t max_len, int64_t count,
+                                 int64_t sinks, int64_t recent, void* ws, size_t ws_bytes, int32_t* selected, int32_t* held,
+                                 void* stream);
+
+/* Attention of R tokens, each over its own pages for each key/value head:
+ *   out[r][h] = sum_j softmax_j(scale * q[r][h] . K_j) V_j
+ * over the first held[r] positions of the pages selected[r][h / (hq / heads)] (int32_t [R][heads][count]), one after another:
+ * what bsfp8_tree_attention computes for a single token with that page table, in the same arithmetic. held is cut
+ * to [0, count * page]; a token without positions, or whose pages are all outside the cache, gets zeros.
+ *   q: bf16 [R][ldq]; out: bf16 [R][hq][dim] (contiguous). ws: bsfp8_attention_workspace_bytes(R, 1, hq, heads, dim,
+ *   count * page). Other arguments and limits as bsfp8_tree_attention. */
+BSFP8_API int bsfp8_sparse_attention(const uint16_t* q, int64_t ldq, int64_t R, int64_t hq, const bsfp8_kv_cache* cache,
+                                     const int32_t* selected, int64_t count, const int32_t* held, float scale, void* ws,
+                                     size_t ws_bytes, uint16_t* out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
