@@ -76,6 +76,8 @@ _SIGS = {
     "bsfp8_select_pages": (_I, [_P, _I64, _I64, _I64, _I64, _P, _I64, _I64, _I64, _I64, _P, _I64, _P, _P, _I64, _I64, _I64, _I64,
                                 _P, _SZ, _P, _P, _P]),
     "bsfp8_sparse_attention": (_I, [_P, _I64, _I64, _I64, _P, _P, _I64, _P, ctypes.c_float, _P, _SZ, _P, _P]),
+    "bsfp8_sample_workspace_bytes": (_SZ, [_I64] * 2),
+    "bsfp8_sample": (_I, [_P, _I64, _I, _I64, _I64, _P, _P, _P, _P, _P, _P, _SZ, _P, _P, _I64, _P]),
     "bsfp8_gemm_mxfp8_config": (_I, [_P, _I64, _I64, _I64, _I64, _I64, _P, _P, _I, _I, _P, _SZ, _P, _P, _P]),
 }
 
@@ -1087,3 +1089,37 @@ def bsfp8_sparse_attention(q, cache, selected, held, scale=None, ws=None, out=No
                                       _vec(out, torch.bfloat16, "out", (R, hq, D), dev), _stream(q))
     _check(st, "bsfp8_sparse_attention")
     return out
+
+
+def bsfp8_sample_workspace_bytes(R, V):
+    return int(lib().bsfp8_sample_workspace_bytes(R, V))
+
+
+def workspace_sample(R, V, device="cuda"):
+    """A workspace tensor for bsfp8_sample with these sizes or smaller ones (its contents need no clearing)."""
+    return torch.empty(bsfp8_sample_workspace_bytes(R, V), dtype=torch.uint8, device=device)
+
+
+def bsfp8_sample(logits, temperature, u, top_k=None, top_p=None, min_p=None, filtered=None, ws=None, tokens=None):
+    """A token of each row of logits [R, V] (fp32 or bf16, any row stride), drawn with u fp32 [R] uniform in [0, 1) after the
+    rules: temperature fp32 [R] (0: the largest), top_k int32 [R] (0: all), top_p fp32 [R] (1: all), min_p fp32 [R] (0: all),
+    each of the last three or None. filtered: [R, V] like logits (or logits itself), filled with the logits that the rules
+    keep and -inf: what the verification calls take. -> tokens int32 [R]."""
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("logits must be fp32 or bf16")
+    if logits.dim() != 2 or not logits.is_cuda:
+        raise ValueError("logits must be a GPU tensor [R, V]")
+    R, V = logits.shape
+    dev, dtype, f32, i32 = logits.device, logits.dtype, torch.float32, torch.int32
+    pl, ld = _rows(logits, dtype, "logits", R, V, dev)
+    pf, ldf = _rows(filtered, dtype, "filtered", R, V, dev) if filtered is not None else (0, 0)
+    ws = workspace_sample(R, V, device=dev) if ws is None else ws
+    tokens = torch.empty((R,), dtype=i32, device=dev) if tokens is None else tokens
+    st = lib().bsfp8_sample(
+        pl, ld, 1 if dtype is f32 else 0, R, V, _vec(temperature, f32, "temperature", (R,), dev),
+        _vec(top_k, i32, "top_k", (R,), dev) if top_k is not None else 0,
+        _vec(top_p, f32, "top_p", (R,), dev) if top_p is not None else 0,
+        _vec(min_p, f32, "min_p", (R,), dev) if min_p is not None else 0, _vec(u, f32, "u", (R,), dev),
+        _vec(ws, torch.uint8, "ws", ws.shape, dev), ws.numel(), _vec(tokens, i32, "tokens", (R,), dev), pf, ldf, _stream(logits))
+    _check(st, "bsfp8_sample")
+    return tokens

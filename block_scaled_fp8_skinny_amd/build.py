@@ -13,7 +13,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libbsfp8.so")
 SOURCES = ["api.cpp", "gemm.hip", "prep.hip", "mx.hip", "epilogue.hip", "measure.hip", "scratch.hip", "cache.hip",
-           "attention.hip", "verify.hip", "norm.hip", "tables.hip", "sparse.hip"]
+           "attention.hip", "verify.hip", "norm.hip", "tables.hip", "sparse.hip", "sample.hip"]
 ARCH = "gfx950"
 
 # Packed fp32 VALU instructions are disabled for every device pass.

@@ -863,4 +863,32 @@ int bsfp8_sparse_attention(const uint16_t* q, int64_t ldq, int64_t R, int64_t hq
   return launch_tree_attention(a, as_stream(stream));
 }
 
+size_t bsfp8_sample_workspace_bytes(int64_t R, int64_t V) {
+  return R > 0 && R < MAX_BLOCKS && V >= 1 && V <= (1 << 24) ? sample_ws_bytes(R, V) : 0;
+}
+
+int bsfp8_sample(const void* logits, int64_t ld, int dtype, int64_t R, int64_t V, const float* temperature,
+                 const int32_t* top_k, const float* top_p, const float* min_p, const float* u, void* ws, size_t ws_bytes,
+                 int32_t* tokens, void* filtered, int64_t ldf, void* stream) {
+  if (dtype != BSFP8_LOGITS_BF16 && dtype != BSFP8_LOGITS_F32) return BSFP8_EINVAL;
+  if (R < 0 || R >= MAX_BLOCKS || V < 1 || V > (1 << 24)) return BSFP8_ESHAPE;
+  if (R == 0) return BSFP8_OK;
+  if (!logits || !temperature || !u || !tokens) return BSFP8_EINVAL;
+  if (ld < V || ld >= ((int64_t)1 << 40) || !aligned16(logits)) return BSFP8_ESTRIDE;
+  if (filtered && (ldf < V || ldf >= ((int64_t)1 << 40) || !aligned16(filtered))) return BSFP8_ESTRIDE;
+  if (!ws || ws_bytes < sample_ws_bytes(R, V) || !aligned16(ws)) return BSFP8_EWORKSPACE;
+  const int f32 = dtype == BSFP8_LOGITS_F32;
+  const size_t es = f32 ? 4 : 2, r = (size_t)R * 4;
+  // filtered may be logits itself: written when all else has been read
+  const bool in_place = filtered == logits && ldf == ld;
+  const size_t span = ((size_t)(R - 1) * ld + V) * es;
+  if (outputs_alias({{filtered, filtered ? ((size_t)(R - 1) * ldf + V) * es : 0}, {tokens, r}, {ws, ws_bytes}},
+                    {{temperature, r}, {top_k, r}, {top_p, r}, {min_p, r}, {u, r}}) ||
+      outputs_alias({{tokens, r}, {ws, ws_bytes}, {in_place ? nullptr : filtered, filtered ? ((size_t)(R - 1) * ldf + V) * es : 0}},
+                    {{logits, span}}))
+    return BSFP8_EINVAL;
+  const SampleArgs a{logits, ld, f32, R, V, temperature, top_k, top_p, min_p, u, ws, tokens, filtered, ldf};
+  return launch_sample(a, as_stream(stream));
+}
+
 }  // extern "C"

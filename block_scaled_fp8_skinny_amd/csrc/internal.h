@@ -213,6 +213,23 @@ struct SelectPagesArgs {
 size_t select_ws_bytes(int64_t B, int64_t T, int64_t hkv, int64_t width);
 int launch_select_pages(const SelectPagesArgs& a, hipStream_t stream);
 
+// Sampling (sample.hip).
+struct SampleArgs {
+  const void* logits;
+  int64_t ld;
+  int f32;
+  int64_t R, V;
+  const float* temperature;
+  const int32_t* top_k;
+  const float *top_p, *min_p, *u;
+  void* ws;
+  int32_t* tokens;
+  void* filtered;
+  int64_t ldf;
+};
+size_t sample_ws_bytes(int64_t R, int64_t V);
+int launch_sample(const SampleArgs& a, hipStream_t stream);
+
 inline int hip_status(hipError_t err) { return err == hipSuccess ? BSFP8_OK : BSFP8_EHIP; }
 
 }  // namespace bsfp8

@@ -18,6 +18,10 @@ __device__ __forceinline__ double dpp(double v) {
   const uint64_t b = __builtin_bit_cast(uint64_t, v);
   return __builtin_bit_cast(double, (uint64_t)dpp<CTRL, ROWS>((uint32_t)(b >> 32)) << 32 | dpp<CTRL, ROWS>((uint32_t)b));
 }
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ uint64_t dpp(uint64_t v) {
+  return (uint64_t)dpp<CTRL, ROWS>((uint32_t)(v >> 32)) << 32 | dpp<CTRL, ROWS>((uint32_t)v);
+}
 constexpr int XOR1 = 0xB1, XOR2 = 0x4E, HALF_MIRROR = 0x141, MIRROR = 0x140, SHR = 0x110, BCAST15 = 0x142, BCAST31 = 0x143;
 
 // f over all lanes of the wave; f is associative and commutative
@@ -41,7 +45,12 @@ __device__ __forceinline__ double from_lane(double v, int lane) {        // unif
   const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)b, lane), hi = __builtin_amdgcn_readlane((uint32_t)(b >> 32), lane);
   return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
-__device__ __forceinline__ double wave_scan(double v) {                 // inclusive
+__device__ __forceinline__ uint64_t from_lane(uint64_t v, int lane) {
+  const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)v, lane), hi = __builtin_amdgcn_readlane((uint32_t)(v >> 32), lane);
+  return (uint64_t)hi << 32 | lo;
+}
+template <typename T>
+__device__ __forceinline__ T wave_scan(T v) {                           // inclusive; T: double, uint32_t or uint64_t
   v += dpp<SHR + 1>(v);
   v += dpp<SHR + 2>(v);
   v += dpp<SHR + 4>(v);
@@ -51,6 +60,7 @@ __device__ __forceinline__ double wave_scan(double v) {                 // inclu
   return v;
 }
 __device__ __forceinline__ double wave_sum(double v) { return from_lane(wave_scan(v), 63); }
+__device__ __forceinline__ uint64_t wave_sum(uint64_t v) { return from_lane(wave_scan(v), 63); }
 
 // The arrival of a workgroup at a sequence's counter: true for the last of `n`, which sees what the others
 // stored before theirs (whole workgroup). What is handed over is stored and

@@ -1,0 +1,878 @@
+// Sampling with temperature, top-k, top-p and min-p from given random numbers, for gfx950 (MI355X), and the logits that
+// these rules leave.
+//
+// With M a row's largest logit, w = exp((x - M) / t) is an element's weight, in fp64 and then rounded to a multiple of 2^-SH
+// (SH = 45 for 131072 columns): sums of these integers are exact in any order, so histograms by atomics repeat bit for
+// bit and every decision falls between sums that all launches agree on. Elements are ordered by (x descending, index
+// ascending), an integer of 56 bits; top-k keeps the first k, top-p the shortest prefix of those whose sum reaches p times
+// theirs, so what is kept is a prefix, of which min-p keeps w >= min_p. The token is the first index whose running sum of
+// kept weights passes u times their total.
+//
+// Three launches, each over all pieces of all rows (a wave a piece of 1024, as in the verification):
+//   stats   a piece's largest logits (of each 256 or 512 elements) and an fp32 estimate of its sum;
+//   bins    only rows with top-k or top-p: a histogram of the elements that can be in the prefix, in BINS equal steps of x.
+//           What cannot is cut off first: the k-th largest is at least the k-th largest of the 512 largest of parts of
+//           the row, and weights below (1 - p) S / V together are less than what top-p drops. The row's last
+//           workgroup finds the bins that hold the borders;
+//   pick    the pieces' sums of what is surely kept, and a list of the elements in the borders' bins; the row's last
+//           workgroup ranks those, which gives the borders, and walks to the token.
+// A fourth writes the filtered logits where they are wanted. A list that does not fit (many equal logits) is replaced by
+// another look at the row: slow, but the same answer.
+#include "logits.h"
+
+namespace bsfp8 {
+namespace {
+
+constexpr int BINS = 1024;
+constexpr int RANKED = 256;                         // elements that a workgroup ranks against each other
+constexpr int NEAR = 512;                           // border elements that a workgroup gathers
+constexpr uint32_t NO_INDEX = 0xFFFFFF;
+
+struct PieceStat {
+  float m[4];                                       // the largest of each vector of the piece (256 fp32 or 512 bf16 elements)
+  float s, lo;                                      // sum of exp((x - max) / t); the least logit near the largest
+  float pad[2];
+};
+
+// What the last workgroup of `bins` found out about a row, and that of `pick` (border, token).
+struct RowPlan {
+  double target_p;                                  // p
+  uint64_t before_p, before_k;                      // weights of the bins before p0, before kb
+  uint64_t sum_k;                                   // weights of the first k where kb < 0
+  uint64_t border;                                  // elements from this one on are kept, too
+  float M, scale, cut;                              // bin = (M - x) * scale; elements below cut are in none
+  int sure;                                         // bins before this one are kept
+  int p0, p1;                                       // bins that may hold the end of top-p's prefix (p0 > p1: known)
+  int kb, need;                                     // bin that holds the k-th element (-1: known), and how many of its elements are in
+};
+
+struct SampleParams {
+  const void* logits;
+  const float *temperature, *top_p, *min_p, *u;
+  const int32_t* top_k;
+  int* heads;                                       // [R][4]: workgroups arrived in bins, in pick; elements listed; the list is cut
+  PieceStat* stats;                                 // [R][pieces]
+  RowPlan* plans;                                   // [R]
+  uint32_t* counts;                                 // [R][BINS]
+  uint64_t *weights, *rest;                         // [R][BINS], [R]
+  uint64_t *sums, *list;                            // [R][pieces], [R][room]
+  int32_t* tokens;
+  void* filtered;
+  int64_t ld, ldf;
+  double one;                                       // 2^SH
+  int R, V, pieces, per, blocks, room;              // per: pieces of a wave
+};
+
+// A row's rules.
+struct Rules {
+  double it;                                        // 1 / t, or -1: greedy
+  float t;
+  double min_w, p;
+  int k;                                            // 0: no top-k
+  bool use_p, greedy;
+  __device__ __forceinline__ Rules(const SampleParams& a, int row) {
+    t = a.temperature[row];
+    it = inv_temperature(t);
+    greedy = is_greedy(it);
+    const int kk = a.top_k ? a.top_k[row] : 0;
+    k = kk > 0 && kk < a.V ? kk : 0;
+    const float pp = a.top_p ? a.top_p[row] : 1.f;
+    use_p = pp < 1.f;                               // (not NaN)
+    p = use_p ? (double)fmaxf(pp, 0.f) : 1.0;
+    const float mm = a.min_p ? a.min_p[row] : 0.f;
+    min_w = mm > 0.f ? (double)fminf(mm, 1.f) : 0.0;
+  }
+  __device__ __forceinline__ bool binned() const { return !greedy && (k > 0 || use_p); }
+};
+
+// An element's weight. Beside +inf logits, whose own (inf - inf) is undefined, the others weigh nothing.
+struct RowWeights {
+  Weights f;
+  __device__ __forceinline__ RowWeights(float M, double it, const double* powers) : f(M, it, powers) {}
+  __device__ __forceinline__ double operator()(float x) const { return f.M < -NEG_INF ? f(x) : 0.0; }
+};
+__device__ __forceinline__ uint64_t fixed(const SampleParams& p, double w) {   // w in [0, 1]
+  return __builtin_bit_cast(uint64_t, fma(w, p.one, 0x1p52)) & 0xFFFFFFFFFFFFFull;
+}
+// Logits as ordered integers, and back; -0 is 0.
+__device__ __forceinline__ uint32_t key_of(float x) {
+  const uint32_t b = __float_as_uint(x + 0.f);
+  return b ^ (b >> 31 ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ __forceinline__ float of_key(uint32_t k) { return __uint_as_float(k >> 31 ? k ^ 0x80000000u : ~k); }
+// An element's place in the order: larger is earlier.
+__device__ __forceinline__ uint64_t place(float x, int index) { return (uint64_t)key_of(x) << 24 | (NO_INDEX - (uint32_t)index); }
+__device__ __forceinline__ float place_logit(uint64_t c) { return of_key((uint32_t)(c >> 24)); }
+__device__ __forceinline__ int place_index(uint64_t c) { return (int)(NO_INDEX - ((uint32_t)c & NO_INDEX)); }
+
+// Bin of an element, BINS for none (below the cut, -inf, NaN). Falls with x.
+__device__ __forceinline__ int bin_of(float M, float scale, float cut, float x) {
+  if (!(x >= cut && x > NEG_INF)) return BINS;
+  if (x == M) return 0;
+  return M < -NEG_INF ? (int)fminf((M - x) * scale, (float)(BINS - 1)) : BINS - 1;
+}
+
+template <typename V>
+__device__ __forceinline__ V take(const V* at) { return __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+template <typename V>
+__device__ __forceinline__ void give(V* at, V v) { __hip_atomic_store(at, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+template <typename V>
+__device__ __forceinline__ V add(V* at, V v) { return __hip_atomic_fetch_add(at, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+
+// ---------------------------------------------------------------------------------------------
+// stats
+// ---------------------------------------------------------------------------------------------
+template <typename T>
+__global__ void __launch_bounds__(256) sample_stats_kernel(SampleParams p) {
+  constexpr int E = Row<T>::E, N = Row<T>::N;
+  const int lane = threadIdx.x & 63, row = blockIdx.x;
+  const int piece = blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Row<T> r(p.logits, row * p.ld, p.V);
+  Words w[N];
+  r.load(piece, lane, w);                           // (past the row's end: nothing is read)
+  const Rules rules(p, row);
+  // the row's counters and bins start at zero (where they lie depends on a call's sizes, so no call can leave them so)
+  if (blockIdx.y == 0 && threadIdx.x < 4) p.heads[row * 4 + threadIdx.x] = 0;
+  if (rules.binned()) {
+    for (int i = blockIdx.y * 256 + threadIdx.x; i < BINS; i += gridDim.y * 256) {
+      p.counts[(int64_t)row * BINS + i] = 0;
+      p.weights[(int64_t)row * BINS + i] = 0;
+    }
+    if (blockIdx.y == 0 && threadIdx.x == 0) {
+      p.rest[row] = 0;
+      p.plans[row].M = NEG_INF;                     // stays so in a row without logits
+    }
+  }
+  if (piece >= p.pieces) return;
+  float x[N][E];
+  r.get(w, piece, lane, x);
+  PieceStat st{{NEG_INF, NEG_INF, NEG_INF, NEG_INF}, 0.f, -NEG_INF, {0.f, 0.f}};
+  float m = NEG_INF;
+#pragma unroll
+  for (int v = 0; v < N; ++v) {
+    float a = NEG_INF;
+#pragma unroll
+    for (int i = 0; i < E; ++i) a = fmaxf(a, x[v][i]);
+    st.m[v] = wave_max(a);
+    m = fmaxf(m, st.m[v]);
+  }
+  if (rules.binned() && m > NEG_INF) {
+    const float c = (float)(rules.it * 1.4426950408889634), far = m - 128.f * fmaxf(rules.t, 1.f);
+    float s = 0.f, lo = m;
+#pragma unroll
+    for (int v = 0; v < N; ++v)
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const bool top = x[v][i] == m;
+        if (x[v][i] >= far && x[v][i] > NEG_INF) lo = fminf(lo, x[v][i]);
+        s += top ? 1.f : x[v][i] > NEG_INF && m < -NEG_INF ? __builtin_amdgcn_exp2f((x[v][i] - m) * c) : 0.f;
+      }
+    st.s = wave_reduce(s, [](float a, float b) { return a + b; });
+    st.lo = wave_reduce(lo, [](float a, float b) { return fminf(a, b); });
+  }
+  if (lane == 0) p.stats[(int64_t)row * p.pieces + piece] = st;
+}
+
+// A row's largest logit, the estimate of its sum, its least logit, and the largest of 512 parts of it (eight a lane).
+struct RowStat {
+  float M, S, lo, part[8];
+};
+__device__ __forceinline__ RowStat row_stat(const SampleParams& p, int row, int lane, const Rules& rules) {
+  const PieceStat* st = p.stats + (int64_t)row * p.pieces;
+  RowStat r;
+  r.lo = -NEG_INF;
+  r.S = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r.part[i] = NEG_INF;
+  for (int i0 = 0; i0 < p.pieces; i0 += 128) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = i0 + h * 64 + lane;
+      if (i >= p.pieces) continue;
+      const PieceStat a = st[i];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) r.part[h * 4 + v] = fmaxf(r.part[h * 4 + v], a.m[v]);
+      r.lo = fminf(r.lo, a.lo);
+    }
+  }
+  float m = r.part[0];
+#pragma unroll
+  for (int i = 1; i < 8; ++i) m = fmaxf(m, r.part[i]);
+  r.M = wave_max(m);
+  if (rules.use_p && rules.k == 0) {
+    const float c = (float)(rules.it * 1.4426950408889634);
+    for (int i = lane; i < p.pieces; i += 64) {
+      const PieceStat a = st[i];
+      const float am = fmaxf(fmaxf(a.m[0], a.m[1]), fmaxf(a.m[2], a.m[3]));
+      if (am > NEG_INF) r.S += a.s * (am == r.M ? 1.f : r.M < -NEG_INF ? __builtin_amdgcn_exp2f((am - r.M) * c) : 0.f);
+    }
+    r.S = wave_reduce(r.S, [](float a, float b) { return a + b; });
+  }
+  r.lo = wave_reduce(r.lo, [](float a, float b) { return fminf(a, b); });
+  return r;
+}
+
+// A logit below which no element can be in the prefix.
+__device__ __forceinline__ float cut_of(const SampleParams& p, const RowStat& st, const Rules& rules) {
+  if (rules.k > 0) {
+    // the largest integer of 16 bits that k of the parts' largest reach
+    uint32_t key[8], at = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) key[i] = st.part[i] > NEG_INF ? key_of(st.part[i]) : 0;
+    auto reach = [&](uint32_t c) {
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) n += __builtin_popcountll(__ballot(key[i] >= c));
+      return n >= rules.k;
+    };
+    if (!reach(1)) return NEG_INF;                  // fewer parts than k
+    for (uint32_t bit = 0x80000000u; bit >= 0x10000u; bit >>= 1)
+      if (reach(at | bit)) at |= bit;
+    const uint32_t lowest = 0x00800000u;            // of the finite logits
+    return of_key(at > lowest ? at : lowest);
+  }
+  // weights below (1 - p) S / V: half of that, for the estimate's sake
+  const float least = 0.5f * (float)(1.0 - rules.p) * fmaxf(st.S, 1.f) / (float)p.V;
+  return st.M < -NEG_INF ? st.M + rules.t * __logf(least) : st.M;
+}
+
+// ---------------------------------------------------------------------------------------------
+// bins
+// ---------------------------------------------------------------------------------------------
+// Sums over the workgroup's threads, exclusive, and all (256 threads; `wn`, `ww` of four).
+struct Prefix {
+  uint32_t n;
+  uint64_t w;
+};
+__device__ __forceinline__ Prefix block_scan(Prefix own, int lane, int wave, Prefix* waves, Prefix& all) {
+  const Prefix run{wave_scan(own.n), wave_scan(own.w)};
+  __syncthreads();                                  // `waves` is free
+  if (lane == 63) waves[wave] = run;
+  __syncthreads();
+  Prefix at{run.n - own.n, run.w - own.w};
+  all = Prefix{0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i < wave) at = Prefix{at.n + waves[i].n, at.w + waves[i].w};
+    all = Prefix{all.n + waves[i].n, all.w + waves[i].w};
+  }
+  return at;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) sample_bins_kernel(SampleParams p) {
+  constexpr int E = Row<T>::E, N = Row<T>::N;
+  __shared__ double powers[64];
+  __shared__ uint32_t count[BINS];
+  __shared__ uint64_t weight[BINS];
+  __shared__ Prefix waves[4];
+  __shared__ uint64_t found[4];
+  __shared__ int at[4], shared_last;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), row = blockIdx.x;
+  const Rules rules(p, row);
+  if (!rules.binned()) return;
+  load_powers(powers);
+  for (int i = threadIdx.x; i < BINS; i += 256) {
+    count[i] = 0;
+    weight[i] = 0;
+  }
+  const Row<T> r(p.logits, row * p.ld, p.V);
+  const int piece0 = (blockIdx.y * 4 + wave) * p.per;
+  Words w[N];
+  r.load(piece0, lane, w);
+  const RowStat st = row_stat(p, row, lane, rules);
+  if (!(st.M > NEG_INF) || (rules.use_p && !(st.M < -NEG_INF))) return;   // nothing is kept (for every workgroup of the row)
+  const float cut = cut_of(p, st, rules);
+  const float range = st.M - fmaxf(cut, st.lo), scale = range > 0.f ? (float)BINS / range : 0.f;
+  const RowWeights f(st.M, rules.it, powers);
+  __syncthreads();
+  uint64_t rest = 0;
+  for (int i = 0; i < p.per && piece0 + i < p.pieces; ++i) {
+    float x[N][E];
+    r.get(w, piece0 + i, lane, x);
+    if (i + 1 < p.per) r.load(piece0 + i + 1, lane, w);
+#pragma unroll
+    for (int v = 0; v < N; ++v)
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int b = bin_of(st.M, scale, cut, x[v][e]);
+        if (rules.use_p) {
+          if (rules.k == 0 || __any(b < BINS)) {
+            const uint64_t n = fixed(p, f(x[v][e]));
+            if (b < BINS) atomicAdd((unsigned long long*)&weight[b], (unsigned long long)n);
+            else rest += n;
+          }
+        }
+        if (b < BINS) atomicAdd(&count[b], 1u);
+      }
+  }
+  __syncthreads();
+  uint32_t* counts = p.counts + (int64_t)row * BINS;
+  uint64_t* weights = p.weights + (int64_t)row * BINS;
+  for (int i = threadIdx.x; i < BINS; i += 256) {
+    if (count[i]) add(counts + i, count[i]);
+    if (weight[i]) add(weights + i, weight[i]);
+  }
+  if (rules.use_p && rules.k == 0) {
+    rest = wave_sum(rest);
+    if (lane == 0 && rest) add(p.rest + row, rest);
+  }
+  if (!last_to_arrive(p.heads + row * 4, gridDim.y, &shared_last)) return;
+
+  // the row's bins: four a thread
+  Prefix own[4], sum{0, 0}, all;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    own[i] = Prefix{take(counts + threadIdx.x * 4 + i), rules.use_p ? take(weights + threadIdx.x * 4 + i) : 0};
+    sum = Prefix{sum.n + own[i].n, sum.w + own[i].w};
+  }
+  const Prefix before = block_scan(sum, lane, wave, waves, all);
+  if (threadIdx.x < 4) at[threadIdx.x] = -1;
+  __syncthreads();
+  // the first bin up to which `reach` holds
+  auto find = [&](int slot, auto reach) {
+    Prefix run = before;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const Prefix next{run.n + own[i].n, run.w + own[i].w};
+      if (own[i].n && !(run.n && reach(run)) && reach(next)) {
+        at[slot] = threadIdx.x * 4 + i;
+        found[slot] = run.w;
+        if (slot == 0) {
+          found[3] = (uint64_t)run.n << 32 | next.n;
+          found[1] = next.w;
+        }
+      }
+      run = next;
+    }
+    __syncthreads();
+  };
+  RowPlan pl{};
+  pl.M = st.M;
+  pl.scale = scale;
+  pl.cut = cut;
+  pl.target_p = rules.p;
+  pl.border = ~0ull;
+  pl.kb = -1;
+  pl.p0 = 1;
+  pl.sure = BINS;
+  uint64_t s_lo = all.w + (rules.k ? 0 : take(p.rest + row)), s_hi = s_lo;
+  if (rules.k > 0 && all.n > (uint32_t)rules.k) {
+    find(0, [&](const Prefix& a) { return a.n >= (uint32_t)rules.k; });
+    const uint32_t n0 = (uint32_t)(found[3] >> 32), n1 = (uint32_t)found[3];
+    if (n1 == (uint32_t)rules.k) {                  // the whole bin
+      pl.sure = at[0] + 1;
+      s_lo = s_hi = found[1];
+    } else {
+      pl.sure = pl.kb = at[0];
+      pl.need = rules.k - n0;
+      pl.before_k = s_lo = found[0];
+      s_hi = found[1];
+    }
+    __syncthreads();
+  }
+  pl.sum_k = s_lo;
+  if (rules.use_p) {
+    const double lo = rules.p * (double)s_lo, hi = rules.p * (double)s_hi;
+    find(2, [&](const Prefix& a) { return (double)a.w >= lo; });
+    // (a sum that rounding leaves short of its own p-th part: the last bin)
+    pl.p0 = at[2] < 0 ? BINS - 1 : at[2];
+    pl.before_p = at[2] < 0 ? all.w : found[2];
+    __syncthreads();
+    if (threadIdx.x == 0) at[2] = -1;
+    __syncthreads();
+    find(2, [&](const Prefix& a) { return (double)a.w >= hi; });
+    pl.p1 = at[2] < 0 ? BINS - 1 : at[2];
+    if (pl.kb >= 0) pl.p1 = min(pl.p1, pl.kb);
+    pl.sure = pl.p0;
+    if (pl.p0 == pl.p1 && take(counts + pl.p0) == 1) {   // a single element: no border inside the bin
+      pl.sure = pl.p0 + 1;
+      pl.kb = -1;
+      pl.p0 = 1;
+      pl.p1 = 0;
+    }
+  }
+  if (threadIdx.x == 0) p.plans[row] = pl;
+}
+
+// ---------------------------------------------------------------------------------------------
+// pick
+// ---------------------------------------------------------------------------------------------
+// Elements in question: the row's list, or the row itself where the list has no room. each(f): f(place, bin) of the
+// thread's share of those in bins b0 .. b1 (and kb).
+template <typename T>
+struct Near {
+  const SampleParams& p;
+  const RowPlan& pl;
+  int row, n;
+  bool listed;
+  template <typename F>
+  __device__ __forceinline__ void each(int b0, int b1, F f) const {
+    if (listed) {
+      for (int i = threadIdx.x; i < n; i += 256) {
+        const uint64_t c = take(p.list + (int64_t)row * p.room + i);
+        const int b = bin_of(pl.M, pl.scale, pl.cut, place_logit(c));
+        if (b >= b0 && b <= b1) f(c);
+      }
+    } else {
+      for (int i = threadIdx.x; i < p.V; i += 256) {
+        const float x = element<T>(p.logits, row * p.ld + i);
+        const int b = bin_of(pl.M, pl.scale, pl.cut, x);
+        if (b >= b0 && b <= b1) f(place(x, i));
+      }
+    }
+  }
+};
+
+struct FindShared {
+  uint64_t place[RANKED], w[RANKED];
+  uint32_t count[BINS];
+  uint64_t weight[BINS];
+  Prefix waves[4];
+  uint64_t lo[4], hi[4], result[2];
+  int n, at;
+};
+
+// The last element of the shortest prefix, by place, of those with place >= from in bins b0 .. b1 that reach(n, w) holds
+// for (n elements of weight w); w = the prefix's weight. Whole workgroup. reach holds for all of them at the latest.
+template <typename T, typename Reach>
+__device__ uint64_t find_border(const Near<T>& near, int b0, int b1, uint64_t from, const RowWeights& f, FindShared& s, uint64_t& w,
+                                Reach reach) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const SampleParams& p = near.p;
+  uint64_t lo = from, hi = ~0ull;
+  Prefix before{0, 0};
+  bool fits = near.listed && near.n <= RANKED;
+  while (!fits) {
+    // the range that they span
+    uint64_t a = ~0ull, z = 0;
+    uint32_t n = 0;
+    near.each(b0, b1, [&](uint64_t c) {
+      if (c < lo || c > hi) return;
+      a = min(a, c);
+      z = max(z, c);
+      ++n;
+    });
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      a = min(a, (uint64_t)__shfl_xor((unsigned long long)a, o));
+      z = max(z, (uint64_t)__shfl_xor((unsigned long long)z, o));
+    }
+    __syncthreads();
+    if (lane == 0) {
+      s.lo[wave] = a;
+      s.hi[wave] = z;
+    }
+    Prefix all;
+    (void)block_scan(Prefix{n, 0}, lane, wave, s.waves, all);
+    lo = min(min(s.lo[0], s.lo[1]), min(s.lo[2], s.lo[3]));
+    hi = max(max(s.hi[0], s.hi[1]), max(s.hi[2], s.hi[3]));
+    fits = all.n <= RANKED;
+    if (fits) break;
+    // (places differ: lo < hi, and every round leaves a shorter range)
+    const int shift = max(64 - __builtin_clzll(hi - lo) - 10, 0);
+    for (int i = threadIdx.x; i < BINS; i += 256) {
+      s.count[i] = 0;
+      s.weight[i] = 0;
+    }
+    __syncthreads();
+    near.each(b0, b1, [&](uint64_t c) {
+      if (c < lo || c > hi) return;
+      const int b = (int)((hi - c) >> shift);
+      atomicAdd(&s.count[b], 1u);
+      atomicAdd((unsigned long long*)&s.weight[b], (unsigned long long)fixed(p, f(place_logit(c))));
+    });
+    __syncthreads();
+    Prefix own[4], sum{0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      own[i] = Prefix{s.count[threadIdx.x * 4 + i], s.weight[threadIdx.x * 4 + i]};
+      sum = Prefix{sum.n + own[i].n, sum.w + own[i].w};
+    }
+    Prefix run = block_scan(sum, lane, wave, s.waves, all);
+    run = Prefix{run.n + before.n, run.w + before.w};
+    all = Prefix{all.n + before.n, all.w + before.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const Prefix next{run.n + own[i].n, run.w + own[i].w};
+      // (should rounding keep reach from holding at all: the last)
+      if (own[i].n && !(run.n && reach(run.n, run.w)) && (reach(next.n, next.w) || next.n == all.n)) {
+        s.at = threadIdx.x * 4 + i;
+        s.result[0] = run.n;
+        s.result[1] = run.w;
+      }
+      run = next;
+    }
+    __syncthreads();
+    before = Prefix{(uint32_t)s.result[0], s.result[1]};
+    const uint64_t top = hi - ((uint64_t)s.at << shift), part = (1ull << shift) - 1;
+    hi = top;
+    lo = top - lo > part ? top - part : lo;
+    __syncthreads();
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) s.n = 0;
+  __syncthreads();
+  near.each(b0, b1, [&](uint64_t c) {
+    if (c < lo || c > hi) return;
+    const int i = atomicAdd(&s.n, 1);
+    s.place[i] = c;
+    s.w[i] = fixed(p, f(place_logit(c)));
+  });
+  __syncthreads();
+  const int n = s.n;
+  if ((int)threadIdx.x < n) {
+    const uint64_t c = s.place[threadIdx.x], mine = s.w[threadIdx.x];
+    Prefix run = before;
+    int later = 0;
+    for (int i = 0; i < n; ++i) {
+      const bool ahead = s.place[i] > c;
+      run.n += ahead ? 1 : 0;
+      run.w += ahead ? s.w[i] : 0;
+      later += s.place[i] < c ? 1 : 0;
+    }
+    const bool was = run.n && reach(run.n, run.w), is = reach(run.n + 1, run.w + mine);
+    if (!was && (is || later == 0)) {
+      s.result[0] = c;
+      s.result[1] = run.w + mine;
+    }
+  }
+  __syncthreads();
+  w = s.result[1];
+  return s.result[0];
+}
+
+// The first piece whose running sum passes `target` (whole wave), the last with a sum if none does; `before` = the sum
+// before it.
+__device__ __forceinline__ int pick_piece(const uint64_t* sums, int pieces, int lane, double target, uint64_t& before) {
+  uint64_t base = 0, last_before = 0;
+  int last = 0;
+  for (int i0 = 0; i0 < pieces; i0 += 64) {
+    const uint64_t v = i0 + lane < pieces ? take(sums + i0 + lane) : 0;
+    const uint64_t run = wave_scan(v);
+    const uint64_t past = __ballot(v > 0 && (double)(base + run) > target);
+    const uint64_t some = __ballot(v > 0);
+    const int at = past ? __builtin_ctzll(past) : some ? 63 - __builtin_clzll(some) : -1;
+    if (at >= 0) {
+      last = i0 + at;
+      last_before = base + from_lane(run - v, at);
+    }
+    if (past) break;
+    base += from_lane(run, 63);
+  }
+  before = last_before;
+  return last;
+}
+
+// Whether an element is kept, but for min-p.
+__device__ __forceinline__ bool in_prefix(const RowPlan& pl, float x, int index) {
+  const int b = bin_of(pl.M, pl.scale, pl.cut, x);
+  return x < -NEG_INF && (b < pl.sure || (b < BINS && place(x, index) >= pl.border));
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256) sample_pick_kernel(SampleParams p) {
+  constexpr int E = Row<T>::E, N = Row<T>::N;
+  __shared__ double powers[64];
+  __shared__ FindShared fs;
+  __shared__ uint64_t mine[NEAR];
+  __shared__ int n_mine, base, shared_last;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), row = blockIdx.x;
+  const Rules rules(p, row);
+  if (rules.greedy && blockIdx.y > 0) return;
+  const Row<T> r(p.logits, row * p.ld, p.V);
+  const int piece0 = (blockIdx.y * 4 + wave) * p.per;
+  Words w[N];
+  r.load(piece0, lane, w);
+  load_powers(powers);
+  if (threadIdx.x == 0) n_mine = 0;
+  RowPlan pl{};
+  if (rules.binned()) {
+    pl = p.plans[row];
+  } else {
+    pl.M = row_stat(p, row, lane, rules).M;
+    pl.border = ~0ull;
+    pl.cut = NEG_INF;
+    pl.kb = -1;
+    pl.p0 = 1;
+    pl.sure = BINS;
+  }
+  if (!(pl.M > NEG_INF) || (!(pl.M < -NEG_INF) && (rules.greedy || rules.min_w > 0.0))) {   // nothing is kept
+    pl.M = NEG_INF;
+    pl.cut = -NEG_INF;
+    pl.scale = 0.f;
+    pl.sure = 0;
+    pl.border = ~0ull;
+  }
+  __syncthreads();
+  uint64_t* sums = p.sums + (int64_t)row * p.pieces;
+
+  if (rules.greedy || !(pl.M > NEG_INF)) {          // the lowest index of the largest; 0 for none
+    if (blockIdx.y > 0 || wave > 0) return;
+    int found = 0;
+    if (pl.M > NEG_INF) {
+      for (int i0 = 0, hit = -1; hit < 0; i0 += 64) {   // (some piece holds it)
+        bool is = false;
+        if (i0 + lane < p.pieces) {
+          const PieceStat a = p.stats[(int64_t)row * p.pieces + i0 + lane];
+          is = a.m[0] == pl.M || a.m[1] == pl.M || a.m[2] == pl.M || a.m[3] == pl.M;
+        }
+        const uint64_t has = __ballot(is);
+        if (!has) {
+          if (i0 + 64 >= p.pieces) break;
+          continue;
+        }
+        hit = i0 + __builtin_ctzll(has);
+        r.load(hit, lane, w);
+        float x[N][E];
+        r.get(w, hit, lane, x);
+        bool done = false;
+        for (int v = 0; v < N && !done; ++v) {
+          int e = E;
+#pragma unroll
+          for (int i = E - 1; i >= 0; --i) e = x[v][i] == pl.M ? i : e;
+          const uint64_t at = __ballot(e < E);
+          if (at) {
+            const int l = __builtin_ctzll(at);
+            found = r.index(hit, l, v, 0) + __builtin_amdgcn_readlane(e, l);
+            done = true;
+          }
+        }
+      }
+      pl.border = place(pl.M, found);
+    }
+    pl.sure = 0;
+    if (lane == 0) {
+      p.tokens[row] = found;
+      p.plans[row] = pl;
+    }
+    return;
+  }
+
+  const RowWeights f(pl.M, rules.it, powers);
+  // what is surely kept, by piece; what lies in the borders' bins, gathered
+  for (int i = 0; i < p.per && piece0 + i < p.pieces; ++i) {
+    float x[N][E];
+    const int piece = piece0 + i;
+    r.get(w, piece, lane, x);
+    if (i + 1 < p.per) r.load(piece + 1, lane, w);
+    uint64_t sum = 0;
+#pragma unroll
+    for (int v = 0; v < N; ++v)
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int b = bin_of(pl.M, pl.scale, pl.cut, x[v][e]);
+        if (__any(b < pl.sure)) {
+          const double y = f(x[v][e]);
+          if (b < pl.sure && y >= rules.min_w) sum += fixed(p, y);
+        }
+        if ((b >= pl.p0 && b <= pl.p1) || b == pl.kb) {
+          const int k = atomicAdd(&n_mine, 1);
+          if (k < NEAR) mine[k] = place(x[v][e], r.index(piece, lane, v, e));
+        }
+      }
+    sum = wave_sum(sum);
+    if (lane == 0) give(sums + piece, sum);
+  }
+  __syncthreads();
+  const int n = n_mine;
+  if (n > 0) {
+    if (threadIdx.x == 0) {
+      if (n > NEAR) give(p.heads + row * 4 + 3, 1);
+      base = add(p.heads + row * 4 + 2, n);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < min(n, NEAR); i += 256)
+      if (base + i < p.room) give(p.list + (int64_t)row * p.room + base + i, mine[i]);
+  }
+  if (!last_to_arrive(p.heads + row * 4 + 1, gridDim.y, &shared_last)) return;
+
+  // the borders
+  const int listed = take(p.heads + row * 4 + 2);
+  if (listed != 0) {
+    const Near<T> near{p, pl, row, listed, listed <= p.room && take(p.heads + row * 4 + 3) == 0};
+    uint64_t from = 0, total = pl.sum_k, unused;
+    if (pl.kb >= 0) {
+      uint64_t in = 0;
+      from = find_border(near, pl.kb, pl.kb, 0, f, fs, in, [&](uint32_t m, uint64_t) { return m >= (uint32_t)pl.need; });
+      total = pl.before_k + in;
+    }
+    pl.border = from;
+    if (pl.p0 <= pl.p1) {
+      const double target = pl.target_p * (double)total;
+      pl.border = find_border(near, pl.p0, pl.p1, from, f, fs, unused,
+                              [&](uint32_t, uint64_t x) { return (double)(pl.before_p + x) >= target; });
+    }
+    const int b0 = pl.p0 <= pl.p1 ? pl.p0 : pl.kb, b1 = pl.p0 <= pl.p1 ? pl.p1 : pl.kb;
+    near.each(b0, b1, [&](uint64_t c) {
+      if (c < pl.border) return;
+      const double y = f(place_logit(c));
+      if (y >= rules.min_w) add(sums + place_index(c) / PIECE, fixed(p, y));
+    });
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) p.plans[row] = pl;
+  if (wave != 0) return;
+  uint64_t total = 0;
+  for (int i = lane; i < p.pieces; i += 64) total += take(sums + i);
+  total = wave_sum(total);
+  const double target = (double)p.u[row] * (double)total;
+  uint64_t before;
+  const int piece = pick_piece(sums, p.pieces, lane, target, before);
+  r.load(piece, lane, w);
+  float x[N][E];
+  r.get(w, piece, lane, x);
+  int found = -1, last = 0;
+#pragma unroll 1
+  for (int v = 0; v < N; ++v) {
+    uint64_t own[E], sum = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const double y = f(x[v][e]);
+      own[e] = y >= rules.min_w && in_prefix(pl, x[v][e], r.index(piece, lane, v, e)) ? fixed(p, y) : 0;
+      sum += own[e];
+    }
+    const uint64_t run = wave_scan(sum);
+    uint64_t c = before + (run - sum);
+    int hit = -1, pos = -1;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      c += own[e];
+      pos = own[e] > 0 ? e : pos;
+      hit = hit < 0 && own[e] > 0 && (double)c > target ? e : hit;
+    }
+    const uint64_t hits = __ballot(hit >= 0), some = __ballot(pos >= 0);
+    if (found < 0 && hits) {
+      const int l = __builtin_ctzll(hits);
+      found = r.index(piece, l, v, 0) + __builtin_amdgcn_readlane(hit, l);
+    }
+    if (some) {
+      const int l = 63 - __builtin_clzll(some);
+      last = r.index(piece, l, v, 0) + __builtin_amdgcn_readlane(pos, l);
+    }
+    before += from_lane(run, 63);
+  }
+  if (lane == 0) p.tokens[row] = found >= 0 ? found : last;
+}
+
+// ---------------------------------------------------------------------------------------------
+// the filtered logits
+// ---------------------------------------------------------------------------------------------
+template <typename T>
+__global__ void __launch_bounds__(256) sample_filter_kernel(SampleParams p) {
+  constexpr int E = Row<T>::E, N = Row<T>::N;
+  __shared__ double powers[64];
+  const int lane = threadIdx.x & 63, row = blockIdx.x;
+  const int piece = blockIdx.y * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Row<T> r(p.logits, row * p.ld, p.V);
+  Words w[N];
+  r.load(piece, lane, w);
+  const Rules rules(p, row);
+  const RowPlan pl = p.plans[row];
+  load_powers(powers);
+  __syncthreads();
+  if (piece >= p.pieces) return;
+  float x[N][E];
+  r.get(w, piece, lane, x);
+  const RowWeights f(pl.M, rules.it, powers);
+  T* out = reinterpret_cast<T*>(p.filtered) + row * p.ldf;
+  const bool whole = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+#pragma unroll
+  for (int v = 0; v < N; ++v) {
+    const int at = r.index(piece, lane, v, 0);
+    if (at >= p.V) continue;
+    uint32_t o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      bool keep = in_prefix(pl, x[v][e], at + e);
+      if (rules.min_w > 0.0 && !rules.greedy) keep = keep && f(x[v][e]) >= rules.min_w;
+      o[e] = __float_as_uint(keep ? x[v][e] : NEG_INF);
+    }
+    if (whole && at + E <= p.V) {
+      u32x4_t b;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b[i] = sizeof(T) == 4 ? o[i] : o[2 * i % E] >> 16 | (o[(2 * i + 1) % E] & 0xFFFF0000u);
+      *reinterpret_cast<u32x4_t*>(out + at) = b;
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        if (at + e >= p.V) break;
+        if constexpr (sizeof(T) == 4) out[at + e] = __uint_as_float(o[e]);
+        else out[at + e] = (T)(o[e] >> 16);
+      }
+    }
+  }
+}
+
+inline int64_t pieces_of(int64_t V) { return (V + PIECE - 1) / PIECE; }
+inline int64_t room_of(int64_t V) { return V / 16 > 4096 ? V / 16 : 4096; }
+inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+}  // namespace
+
+size_t sample_ws_bytes(int64_t R, int64_t V) {
+  const size_t r = (size_t)R, pieces = (size_t)pieces_of(V);
+  return align256(r * 16) + align256(r * pieces * sizeof(PieceStat)) + align256(r * sizeof(RowPlan)) + align256(r * BINS * 4) +
+         align256(r * BINS * 8) + align256(r * 8) + align256(r * pieces * 8) + r * (size_t)room_of(V) * 8;
+}
+
+int launch_sample(const SampleArgs& a, hipStream_t stream) {
+  SampleParams p{};
+  p.logits = a.logits;
+  p.temperature = a.temperature;
+  p.top_k = a.top_k;
+  p.top_p = a.top_p;
+  p.min_p = a.min_p;
+  p.u = a.u;
+  p.tokens = a.tokens;
+  p.filtered = a.filtered;
+  p.ld = a.ld;
+  p.ldf = a.ldf;
+  p.R = (int)a.R;
+  p.V = (int)a.V;
+  p.pieces = (int)pieces_of(a.V);
+  p.room = (int)room_of(a.V);
+  int bits = 0;
+  while (((int64_t)1 << bits) < a.V) ++bits;
+  const int sh = 62 - bits < 51 ? 62 - bits : 51;   // a row's sum stays below 2^63, a weight below 2^52
+  p.one = (double)((int64_t)1 << sh);
+  const size_t r = (size_t)a.R, pieces = (size_t)p.pieces;
+  char* ws = reinterpret_cast<char*>(a.ws);
+  auto next = [&](size_t n) {
+    char* at = ws;
+    ws += align256(n);
+    return at;
+  };
+  p.heads = reinterpret_cast<int*>(next(r * 16));
+  p.stats = reinterpret_cast<PieceStat*>(next(r * pieces * sizeof(PieceStat)));
+  p.plans = reinterpret_cast<RowPlan*>(next(r * sizeof(RowPlan)));
+  p.counts = reinterpret_cast<uint32_t*>(next(r * BINS * 4));
+  p.weights = reinterpret_cast<uint64_t*>(next(r * BINS * 8));
+  p.rest = reinterpret_cast<uint64_t*>(next(r * 8));
+  p.sums = reinterpret_cast<uint64_t*>(next(r * pieces * 8));
+  p.list = reinterpret_cast<uint64_t*>(ws);
+  const int64_t all = a.R * ((p.pieces + 3) / 4);
+  p.per = all > 8192 ? 4 : all > 4096 ? 2 : 1;
+  const unsigned blocks = (unsigned)((p.pieces + 3) / 4), shares = (unsigned)((p.pieces + 4 * p.per - 1) / (4 * p.per));
+  const dim3 grid((unsigned)a.R, blocks), fewer((unsigned)a.R, shares);
+  const bool rules = a.top_k || a.top_p;
+  if (a.f32) hipLaunchKernelGGL(sample_stats_kernel<float>, grid, dim3(256), 0, stream, p);
+  else hipLaunchKernelGGL(sample_stats_kernel<uint16_t>, grid, dim3(256), 0, stream, p);
+  if (hipGetLastError() != hipSuccess) return BSFP8_EHIP;
+  if (rules) {
+    if (a.f32) hipLaunchKernelGGL(sample_bins_kernel<float>, fewer, dim3(256), 0, stream, p);
+    else hipLaunchKernelGGL(sample_bins_kernel<uint16_t>, fewer, dim3(256), 0, stream, p);
+    if (hipGetLastError() != hipSuccess) return BSFP8_EHIP;
+  }
+  if (a.f32) hipLaunchKernelGGL(sample_pick_kernel<float>, fewer, dim3(256), 0, stream, p);
+  else hipLaunchKernelGGL(sample_pick_kernel<uint16_t>, fewer, dim3(256), 0, stream, p);
+  if (hipGetLastError() != hipSuccess) return BSFP8_EHIP;
+  if (a.filtered) {
+    if (a.f32) hipLaunchKernelGGL(sample_filter_kernel<float>, grid, dim3(256), 0, stream, p);
+    else hipLaunchKernelGGL(sample_filter_kernel<uint16_t>, grid, dim3(256), 0, stream, p);
+  }
+  return hip_status(hipGetLastError());
+}
+
+}  // namespace bsfp8

@@ -561,6 +561,32 @@ BSFP8_API int bsfp8_sparse_attention(const uint16_t* q, int64_t ldq, int64_t R, 
                                      const int32_t* selected, int64_t count, const int32_t* held, float scale, void* ws,
                                      size_t ws_bytes, uint16_t* out, void* stream);
 
+/* Workspace bytes of bsfp8_sample (0 for sizes it refuses; never more for smaller sizes). The contents need no clearing:
+ * calls of any sizes may use it one after another. Not for two calls that can run at the same time. */
+BSFP8_API size_t bsfp8_sample_workspace_bytes(int64_t R, int64_t V);
+
+/* One token of each of R rows of logits, with u[r] uniform in [0, 1), by these rules in this order (w = exp((x - M) / t), M the
+ * row's largest logit, t = temperature[r]; elements ordered by falling logit, equal ones by rising index):
+ *   top-k   the first top_k[r] elements (<= 0 or >= V: all);
+ *   top-p   the shortest prefix of those, at least one, whose weights sum to top_p[r] times theirs (>= 1 or NaN: all);
+ *   min-p   of those, the ones with w >= min_p[r] (<= 0 or NaN: all; above 1 as 1).
+ * The token is the first index whose running sum of the weights kept passes u[r] times their total. t = 0 (also t < 0 or
+ * NaN): the lowest index of the largest logit, whatever the rules. An infinite t weighs all logits but -inf alike. -inf
+ * and NaN logits are never kept; a row of nothing else gives index 0. So does a row with a +inf logit, whose weights are
+ * not defined (inf - inf), at every t: comparisons with them fail, so nothing of it is kept under top-p, min-p or t = 0, and
+ * else what top-k leaves but the +inf ones.
+ *   logits : [R][ld] of `dtype` (bsfp8_logits; 16-byte aligned, any ld >= V).
+ *   temperature, top_k, top_p, min_p, u : [R] (device), the rules' nullable.
+ *   tokens : int32_t [R].
+ *   filtered : NULL, or [R][ldf] of `dtype` (16-byte aligned; logits itself with the same ld: in place): the logits that are
+ *              kept, -inf for the others: what bsfp8_verify_chain and bsfp8_verify_tree take for target and draft so
+ *              that the drafts are verified under the same rules.
+ * Weights are computed in 64 bits and rounded to 2^-45 of the largest (131072 columns; 2^-38 for 2^24, 2^-51 up to 2048), sums of them
+ * are exact: a weight below half of that is never drawn. 1 <= V <= 2^24, R < 2^24. */
+BSFP8_API int bsfp8_sample(const void* logits, int64_t ld, int dtype, int64_t R, int64_t V, const float* temperature,
+                           const int32_t* top_k, const float* top_p, const float* min_p, const float* u, void* ws,
+                           size_t ws_bytes, int32_t* tokens, void* filtered, int64_t ldf, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
