@@ -1,0 +1,118 @@
+"""A serving step's operators, in float64 and plain loops from the definitions: norms and gated residual, page tables and
+slots, bounds of a page's keys, the pages that they select, and sampling under top-k, top-p and min-p.
+
+TEST INFRASTRUCTURE ONLY (see the package docstring). Written from the formulas in the library's header; shares no code
+with the HIP library.
+"""
+import math
+
+import numpy as np
+
+
+def norm(x, weight=None, eps=1e-6):
+    y = x / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
+    return y if weight is None else y * weight
+
+
+def residual_norm(h, y=None, weight=None, post_weight=None, gate=None, scale=1.0, eps=1e-6):
+    """-> (h', x, |h| + |scale * gate * z|)."""
+    if y is None:
+        return h, norm(h, weight, eps), np.abs(h)
+    z = y if post_weight is None else norm(y, post_weight, eps)
+    z = scale * (z if gate is None else z * gate)
+    return h + z, norm(h + z, weight, eps), np.abs(h) + np.abs(z)
+
+
+def step_tables(pages, lens, new_lens, stack, page, rows, per_seq=0, capacity=None):
+    """pages: [B][W] list of lists and stack: list of free pages, both updated in place.
+    -> slots, positions, seqs, starts, held, [tokens, taken, given, lacking]."""
+    B, W = len(lens), len(pages[0]) if len(lens) else 0
+    old, new = [max(0, int(x)) for x in lens], [max(0, int(x)) for x in new_lens]
+    need = lambda n: -(-n // page)
+    given = taken = lacking = 0
+    for b in range(B):
+        for j in range(need(new[b]), min(need(old[b]), W)):
+            stack.append(pages[b][j])
+            given += 1
+    held, starts = [], [0]
+    for b in range(B):
+        last = old[b]
+        got = min(need(old[b]), W)
+        for j in range(need(old[b]), need(new[b])):
+            if j < W and stack:
+                pages[b][j] = stack.pop()
+                got += 1
+                taken += 1
+            else:
+                if j < W:
+                    pages[b][j] = -1
+                lacking += 1
+        held.append(min(new[b], got * page) if new[b] > last else new[b])
+        starts.append(starts[-1] + max(0, new[b] - last))
+    if capacity is not None:
+        del stack[capacity:]
+    slots, positions, seqs = [-1] * rows, [0] * rows, [-1] * rows
+    for b in range(B):
+        for t in range(max(0, new[b] - old[b])):
+            r = b * per_seq + t if per_seq else starts[b] + t
+            if r >= rows or (per_seq and t >= per_seq):
+                break
+            pos = old[b] + t
+            entry = pages[b][pos // page] if pos // page < W else -1
+            slots[r] = entry * page + pos % page if entry >= 0 else -1
+            positions[r], seqs[r] = pos, b
+    return slots, positions, seqs, starts, held, [starts[-1], taken, given, lacking]
+
+
+def key_bounds(K):
+    """K [tokens, heads, dim] -> [heads, 2, dim]: least and largest, NaN for both where there is one."""
+    return np.stack([K.min(0), K.max(0)], 1)
+
+
+def page_scores(q, bounds):
+    """q [g, dim] of the heads that share a key head, bounds [pages, 2, dim] -> [pages]."""
+    with np.errstate(invalid="ignore", over="ignore"):
+        u = np.maximum(q[:, None] * bounds[None, :, 0], q[:, None] * bounds[None, :, 1]).sum(-1).max(0)
+    bad = ~np.isfinite(bounds).all((1, 2)) | ~np.isfinite(q).all()
+    return np.where(bad, np.inf, u)
+
+
+def select(scores, there, N, count, sinks, recent):
+    """scores, there [N] -> the page indices of the list, ascending."""
+    if N <= count:
+        return list(range(N))
+    forced = set(range(sinks)) | set(range(N - recent, N))
+    rest = sorted((j for j in range(N) if j not in forced), key=lambda j: (not there[j], -scores[j] if there[j] else 0, j))
+    return sorted(list(forced) + rest[: count - len(forced)])
+
+
+def sample(x, t, k=0, p=1.0, m=0.0, u=0.5):
+    """One row -> (token, kept [V] bool)."""
+    V = len(x)
+    x = np.where(np.isnan(x), -np.inf, np.asarray(x, np.float64))
+    kept = np.zeros(V, bool)
+    top = x.max()
+    if top == -np.inf:
+        return 0, kept
+    order = [i for i in np.argsort(-x, kind="stable") if x[i] > -np.inf]
+    if top == np.inf:
+        if t > 0 and not p < 1 and not m > 0:
+            kept[[i for i in order[: k if 0 < k < V else V] if x[i] < np.inf]] = True
+        return 0, kept
+    if not t > 0:
+        kept[order[0]] = True
+        return int(order[0]), kept
+    with np.errstate(over="ignore", under="ignore"):
+        w = np.where(x > -np.inf, np.exp((x - top) / t), 0.0)
+    order = order[: k if 0 < k < V else V]
+    if p < 1:
+        run, goal = 0.0, max(p, 0.0) * math.fsum(w[order])
+        for n, i in enumerate(order):
+            run = math.fsum((run, w[i]))
+            if run >= goal:
+                order = order[: n + 1]
+                break
+    kept[[i for i in order if w[i] >= (min(m, 1.0) if m > 0 else 0.0)]] = True
+    c = np.cumsum(np.where(kept, w, 0.0))
+    past = np.nonzero((c > u * c[-1]) & kept & (w > 0))[0]
+    return int(past[0]) if len(past) else int(np.nonzero(kept & (w > 0))[0][-1]), kept
