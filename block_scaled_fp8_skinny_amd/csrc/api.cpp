@@ -770,7 +770,7 @@ int bsfp8_step_tables(const int32_t* lens, const int32_t* new_lens, int64_t B, i
                       int64_t* slots, int64_t* positions, int32_t* seqs, int32_t* starts, int32_t* held, int32_t* counts,
                       void* stream) {
   const int64_t lim = (int64_t)1 << 31;
-  if (B < 0 || B > (1 << 20) || page < 1 || page >= lim || ld_pages < 0 || ld_pages >= lim || capacity < 0 || capacity >= lim)
+  if (B < 0 || B > (1 << 16) || page < 1 || page >= lim || ld_pages < 0 || ld_pages >= lim || capacity < 0 || capacity >= lim)
     return BSFP8_ESHAPE;
   if (R < 0 || R >= lim - 4096 || per_seq < 0 || per_seq >= lim || B * ld_pages >= lim) return BSFP8_ESHAPE;
   if (!n_free || !starts || !counts || (B > 0 && (!lens || !new_lens || !held || (ld_pages > 0 && !pages)))) return BSFP8_EINVAL;

@@ -24,18 +24,35 @@ __device__ __forceinline__ uint64_t dpp(uint64_t v) {
 }
 constexpr int XOR1 = 0xB1, XOR2 = 0x4E, HALF_MIRROR = 0x141, MIRROR = 0x140, SHR = 0x110, BCAST15 = 0x142, BCAST31 = 0x143;
 
-// f over all lanes of the wave; f is associative and commutative
-template <typename F>
+// f over all lanes of the wave, or of each LANES neighbours; f is associative and commutative
+template <int LANES = 64, typename F>
 __device__ __forceinline__ float wave_reduce(float v, F f) {
   auto step = [&](uint32_t o) { v = f(v, __uint_as_float(o)); };
   step(dpp<XOR1>(__float_as_uint(v)));
   step(dpp<XOR2>(__float_as_uint(v)));
-  step(dpp<HALF_MIRROR>(__float_as_uint(v)));
-  step(dpp<MIRROR>(__float_as_uint(v)));
-  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = f(__uint_as_float(r[0]), __uint_as_float(r[1]));
-  r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return f(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  if constexpr (LANES >= 8) step(dpp<HALF_MIRROR>(__float_as_uint(v)));
+  if constexpr (LANES >= 16) step(dpp<MIRROR>(__float_as_uint(v)));
+  if constexpr (LANES >= 32) {
+    auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = f(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  }
+  if constexpr (LANES >= 64) {
+    auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = f(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  }
+  return v;
+}
+// the same of integers (whole wave)
+template <typename F>
+__device__ __forceinline__ uint32_t wave_reduce(uint32_t v, F f) {
+  v = f(v, dpp<XOR1>(v));
+  v = f(v, dpp<XOR2>(v));
+  v = f(v, dpp<HALF_MIRROR>(v));
+  v = f(v, dpp<MIRROR>(v));
+  auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = f((uint32_t)r[0], (uint32_t)r[1]);
+  r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return f((uint32_t)r[0], (uint32_t)r[1]);
 }
 __device__ __forceinline__ float wave_max(float v) {
   return wave_reduce(v, [](float a, float b) { return fmaxf(a, b); });

@@ -5,8 +5,9 @@
 // in fp32, rounded once where it is stored: x is the norm of h' before its rounding.
 //
 // A row is held in registers by a workgroup (or by one wave, if it is short), so every value is read and written once; the
-// two means are the only exchanges. HBM bounds many rows, the latency of one chain (load, two sums, store) few. A
-// workgroup keeps the weights of its columns for all its rows and asks for the next row before it computes this one.
+// two means are the only exchanges. HBM bounds many rows (8191 of 5120: 86 us with an fp32 residual and MXFP8 out, 5.4 TB/s;
+// 63 us in bf16, 5.3), the latency of one chain (load, two sums, store) few: 4 us for 6 rows. A workgroup keeps the weights of
+// its columns for all its rows and, but for the widest rows, asks for the next row before it computes this one.
 
 #include "lanes.h"
 
@@ -38,15 +39,19 @@ struct Held {
   u32x4_t h[F32 ? 2 : 1], y, g;
 };
 
-// V groups of eight values a thread; SHARED: the workgroup is one row's (else each wave has its own).
-template <bool F32, int V, bool SHARED>
-__global__ void __launch_bounds__(SHARED ? 1024 : 256) residual_norm_kernel(NormParams p) {
+// V groups of eight values a thread. LANES: those of a row (8 to 64 of a wave, several rows in it; 0: the workgroup is one
+// row's). AHEAD: the next row's loads and the weights stay in registers; without it (rows too wide for that) the block's
+// output is read again, from L2, after its norm is known.
+template <bool F32, int V, int LANES, int THREADS, bool AHEAD>
+__global__ void __launch_bounds__(THREADS) residual_norm_kernel(NormParams p) {
   __shared__ float sums[2][16];
+  constexpr bool SHARED = LANES == 0;
+  constexpr int ROWS = SHARED ? 1 : THREADS / (LANES > 0 ? LANES : 1);   // of a workgroup
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int waves = SHARED ? blockDim.x >> 6 : 1, threads = SHARED ? blockDim.x : 64;
-  const int t = SHARED ? threadIdx.x : lane;
-  int64_t r = SHARED ? blockIdx.x : (int64_t)blockIdx.x * 4 + wave;
-  const int64_t step = SHARED ? gridDim.x : (int64_t)gridDim.x * 4;
+  const int waves = SHARED ? blockDim.x >> 6 : 1, threads = SHARED ? blockDim.x : LANES;
+  const int t = SHARED ? threadIdx.x : threadIdx.x % (LANES > 0 ? LANES : 1);
+  int64_t r = SHARED ? blockIdx.x : (int64_t)blockIdx.x * ROWS + threadIdx.x / (LANES > 0 ? LANES : 1);
+  const int64_t step = (int64_t)gridDim.x * ROWS;
   int col[V];
   bool on[V];
 #pragma unroll
@@ -57,25 +62,22 @@ __global__ void __launch_bounds__(SHARED ? 1024 : 256) residual_norm_kernel(Norm
   const u32x4_t none = {0, 0, 0, 0};
   auto load8 = [&](const uint16_t* src, int v) { return on[v] ? *reinterpret_cast<const u32x4_t*>(src + col[v]) : none; };
   const bool gates = p.gate != nullptr && p.ldg != 0;   // a row of gates for each row
-  auto load = [&](int64_t row, Held<F32> (&d)[V]) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if constexpr (F32) {
-        const float* src = reinterpret_cast<const float*>(p.h) + row * p.ldh + col[v];
-        d[v].h[0] = on[v] ? *reinterpret_cast<const u32x4_t*>(src) : none;
-        d[v].h[1] = on[v] ? *reinterpret_cast<const u32x4_t*>(src + 4) : none;
-      } else {
-        d[v].h[0] = load8(reinterpret_cast<const uint16_t*>(p.h) + row * p.ldh, v);
-      }
-      d[v].y = p.y ? load8(p.y + row * p.ldy, v) : none;
-      d[v].g = gates ? load8(p.gate + row * p.ldg, v) : none;
+  auto load = [&](int64_t row, int v, Held<F32>& d) {
+    if constexpr (F32) {
+      const float* src = reinterpret_cast<const float*>(p.h) + row * p.ldh + col[v];
+      d.h[0] = on[v] ? *reinterpret_cast<const u32x4_t*>(src) : none;
+      d.h[1] = on[v] ? *reinterpret_cast<const u32x4_t*>(src + 4) : none;
+    } else {
+      d.h[0] = load8(reinterpret_cast<const uint16_t*>(p.h) + row * p.ldh, v);
     }
+    d.y = p.y ? load8(p.y + row * p.ldy, v) : none;
+    d.g = gates ? load8(p.gate + row * p.ldg, v) : none;
   };
   // the sum over the row; a call's slot is free again two calls later, with a barrier of the next one between
   int turn = 0;
   auto total = [&](float s) {
-    s = wave_reduce(s, [](float a, float b) { return a + b; });
-    if (!SHARED || waves == 1) return s;
+    s = wave_reduce<SHARED ? 64 : LANES>(s, [](float a, float b) { return a + b; });
+    if (!SHARED) return s;
     turn ^= 1;
     if (lane == 0) sums[turn][wave] = s;
     __syncthreads();
@@ -84,60 +86,77 @@ __global__ void __launch_bounds__(SHARED ? 1024 : 256) residual_norm_kernel(Norm
     return s;
   };
 
-  Held<F32> now[V];
-  if (r < p.R) load(r, now);
+  Held<F32> now[AHEAD ? V : 1];
   u32x4_t wv[V], pv[V], gv[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    wv[v] = p.weight ? load8(p.weight, v) : none;
-    pv[v] = p.post ? load8(p.post, v) : none;
-    gv[v] = p.gate && !gates ? load8(p.gate, v) : none;
-  }
-  for (; r < p.R; r += step) {
-    float h[V][8], z[V][8];
+  if constexpr (AHEAD) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
+      if (r < p.R) load(r, v, now[v]);
+      wv[v] = p.weight ? load8(p.weight, v) : none;
+      pv[v] = p.post ? load8(p.post, v) : none;
+      gv[v] = p.gate && !gates ? load8(p.gate, v) : none;
+    }
+  }
+  for (; r < p.R; r += step) {
+    float h[V][8], z[AHEAD ? V : 1][8];
+    auto unpack = [&](const Held<F32>& d, float (&hv)[8], float (&zv)[8]) {
       if constexpr (F32) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[v][i] = __uint_as_float(now[v].h[i >> 2][i & 3]);
+        for (int i = 0; i < 8; ++i) hv[i] = __uint_as_float(d.h[i >> 2][i & 3]);
       } else {
-        unpack8(now[v].h[0], h[v]);
+        unpack8(d.h[0], hv);
       }
-      unpack8(now[v].y, z[v]);
+      unpack8(d.y, zv);
+    };
+    float inv = 1.f;
+    if constexpr (AHEAD) {
+      u32x4_t gate[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        unpack(now[v], h[v], z[v]);
+        gate[v] = gates ? now[v].g : gv[v];
+      }
+      if (r + step < p.R) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) load(r + step, v, now[v]);
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) gv[v] = gate[v];
     }
-    u32x4_t gate[V];
+    if (p.post) {
+      float s = 0.f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) gate[v] = gates ? now[v].g : gv[v];
-    if (r + step < p.R) load(r + step, now);
-    if (p.y) {
+      for (int v = 0; v < V; ++v) {
+        if constexpr (!AHEAD) unpack8(load8(p.y + r * p.ldy, v), z[0]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += z[AHEAD ? v : 0][i] * z[AHEAD ? v : 0][i];
+      }
+      inv = rsqrtf(total(s) * p.inv_w + p.eps);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float (&zv)[8] = z[AHEAD ? v : 0];
+      if constexpr (!AHEAD) {
+        load(r, v, now[0]);
+        unpack(now[0], h[v], zv);
+        gv[v] = gates ? now[0].g : p.gate ? load8(p.gate, v) : none;
+        pv[v] = p.post ? load8(p.post, v) : none;
+      }
+      if (!p.y) continue;                           // uniform
       if (p.post) {
-        float s = 0.f;
+        float w[8];
+        unpack8(pv[v], w);
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) s += z[v][i] * z[v][i];
-        const float inv = rsqrtf(total(s) * p.inv_w + p.eps);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          float w[8];
-          unpack8(pv[v], w);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) z[v][i] = z[v][i] * inv * w[i];
-        }
+        for (int i = 0; i < 8; ++i) zv[i] = zv[i] * inv * w[i];
       }
       if (p.gate) {
+        float g[8];
+        unpack8(gv[v], g);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          float g[8];
-          unpack8(gate[v], g);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) z[v][i] *= g[i];
-        }
+        for (int i = 0; i < 8; ++i) zv[i] *= g[i];
       }
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[v][i] = on[v] ? fmaf(p.scale, z[v][i], h[v][i]) : 0.f;
+      for (int i = 0; i < 8; ++i) h[v][i] = on[v] ? fmaf(p.scale, zv[i], h[v][i]) : 0.f;
     }
     if (p.h_out) {
 #pragma unroll
@@ -160,10 +179,11 @@ __global__ void __launch_bounds__(SHARED ? 1024 : 256) residual_norm_kernel(Norm
     for (int v = 0; v < V; ++v)
 #pragma unroll
       for (int i = 0; i < 8; ++i) s += h[v][i] * h[v][i];
-    const float inv = rsqrtf(total(s) * p.inv_w + p.eps);
+    inv = rsqrtf(total(s) * p.inv_w + p.eps);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       float w[8];
+      if constexpr (!AHEAD) wv[v] = p.weight ? load8(p.weight, v) : none;
       unpack8(wv[v], w);
       float x[8];
 #pragma unroll
@@ -202,21 +222,27 @@ __global__ void __launch_bounds__(SHARED ? 1024 : 256) residual_norm_kernel(Norm
 template <bool F32>
 int launch(const NormParams& p, hipStream_t stream) {
   const int groups = p.W / 8;
-  if (groups <= 128) {                              // a wave holds the row: four rows a workgroup
-    const int64_t want = (p.R + 3) / 4;
+  if (groups <= 128) {                              // a wave or less holds the row
+    const int lanes = groups <= 8 ? 8 : groups <= 16 ? 16 : groups <= 32 ? 32 : 64, rows = 256 / lanes;
+    const int64_t want = (p.R + rows - 1) / rows;
     const dim3 grid((unsigned)(want < 2048 ? want : 2048));
-    if (groups <= 64) hipLaunchKernelGGL((residual_norm_kernel<F32, 1, false>), grid, dim3(256), 0, stream, p);
-    else hipLaunchKernelGGL((residual_norm_kernel<F32, 2, false>), grid, dim3(256), 0, stream, p);
+    if (lanes == 8) hipLaunchKernelGGL((residual_norm_kernel<F32, 1, 8, 256, true>), grid, dim3(256), 0, stream, p);
+    else if (lanes == 16) hipLaunchKernelGGL((residual_norm_kernel<F32, 1, 16, 256, true>), grid, dim3(256), 0, stream, p);
+    else if (lanes == 32) hipLaunchKernelGGL((residual_norm_kernel<F32, 1, 32, 256, true>), grid, dim3(256), 0, stream, p);
+    else if (groups <= 64) hipLaunchKernelGGL((residual_norm_kernel<F32, 1, 64, 256, true>), grid, dim3(256), 0, stream, p);
+    else hipLaunchKernelGGL((residual_norm_kernel<F32, 2, 64, 256, true>), grid, dim3(256), 0, stream, p);
     return hip_status(hipGetLastError());
   }
-  const int v = groups <= 256 ? 1 : groups <= 2048 ? 2 : 4;
+  // One group a thread while 1024 threads hold the row (8191 rows of 5120, fp32 in, MXFP8 out: 88 us; two groups 91 to 96,
+  // four 104 to 112), and no more workgroups than the GPU holds at once (20 waves a CU), each with the next row on its way (a
+  // workgroup for each row 117, without the next row's loads 96). Wider rows leave no registers for these.
+  const int v = groups <= 1024 ? 1 : groups <= 2048 ? 2 : 4;
   const int threads = ((groups + v - 1) / v + 63) / 64 * 64;
-  // as many workgroups as the GPU holds at once (2048 threads a CU, 128 registers each)
-  const int64_t most = 256 * (1024 / threads > 0 ? 1024 / threads : 1);
+  const int64_t held = 256 * (1280 / threads > 0 ? 1280 / threads : 1), most = v == 1 ? held : 1 << 20;
   const dim3 grid((unsigned)(p.R < most ? p.R : most));
-  if (v == 1) hipLaunchKernelGGL((residual_norm_kernel<F32, 1, true>), grid, dim3(threads), 0, stream, p);
-  else if (v == 2) hipLaunchKernelGGL((residual_norm_kernel<F32, 2, true>), grid, dim3(threads), 0, stream, p);
-  else hipLaunchKernelGGL((residual_norm_kernel<F32, 4, true>), grid, dim3(threads), 0, stream, p);
+  if (v == 1) hipLaunchKernelGGL((residual_norm_kernel<F32, 1, 0, 1024, true>), grid, dim3(threads), 0, stream, p);
+  else if (v == 2) hipLaunchKernelGGL((residual_norm_kernel<F32, 2, 0, 1024, false>), grid, dim3(threads), 0, stream, p);
+  else hipLaunchKernelGGL((residual_norm_kernel<F32, 4, 0, 1024, false>), grid, dim3(threads), 0, stream, p);
   return hip_status(hipGetLastError());
 }
 

@@ -221,22 +221,26 @@ __global__ void __launch_bounds__(256) select_score_kernel(SelectParams p) {
 // ---------------------------------------------------------------------------------------------
 // the pages with the largest scores
 // ---------------------------------------------------------------------------------------------
-constexpr int PICK_BINS = 2048, PICK_LIST = 256;
+constexpr int PICK_LIST = 64;                       // keys that one wave ranks against each other
+constexpr int PICK_HELD = 8;                        // keys of a thread, where they are held
 
 // The list of one token and head (a workgroup): the first `sinks` and the last `recent` of its N pages and, of the others,
 // those with the largest keys, the lower index first among equals. The least key that is taken is found by histograms of
-// the keys still in question, over the range that they span: each splits it into up to 2048 parts, keeps the one that holds
-// the border, and usually leaves a handful after the first; up to 256 are ranked against each other. What is in the
-// list is then counted off in the order of the pages.
-template <int THREADS>
+// the keys still in question, over the range that they span: each splits it into up to 4 * THREADS parts, keeps the one that
+// holds the border, and usually leaves a handful after the first, which one wave ranks against each other. What is in the
+// list is then counted off in the order of the pages. HELD: the keys stay in registers, PICK_HELD a thread (else they
+// are read again in each round).
+template <int THREADS, bool HELD>
 __global__ void __launch_bounds__(THREADS) select_pick_kernel(SelectParams p) {
-  constexpr int WAVES = THREADS / 64;
-  __shared__ int bins[PICK_BINS];
+  constexpr int WAVES = THREADS / 64, BINS = THREADS * 4, BIN_BITS = THREADS == 256 ? 10 : 12;
+  static_assert(BINS == 1 << BIN_BITS, "bins");
+  __shared__ __align__(16) int bins[BINS];
   __shared__ uint64_t list[PICK_LIST];
   __shared__ int list_at[PICK_LIST];
-  __shared__ uint64_t range[2][WAVES];
-  __shared__ int sums[WAVES], found[4];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __shared__ uint32_t lows[WAVES], highs[WAVES];
+  __shared__ int sums[HELD ? PICK_HELD * WAVES : WAVES], found[3], n_list, last_at;
+  __shared__ uint64_t last_key;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = blockIdx.x / p.heads, h = blockIdx.x - r * p.heads, b = r / p.T;
   const int n = positions_seen(p, b, r - b * p.T), N = pages_for(p, n);
   int32_t* out = p.selected + ((int64_t)r * p.heads + h) * p.count;
@@ -255,87 +259,118 @@ __global__ void __launch_bounds__(THREADS) select_pick_kernel(SelectParams p) {
   // in question: pages sinks .. N - recent - 1 (more than are needed, so N - recent > sinks)
   const uint64_t* keys = p.keys + ((int64_t)r * p.heads + h) * p.width;
   const int j0 = p.sinks, j1 = N - p.recent;
+  uint64_t held[HELD ? PICK_HELD : 1];
+  if constexpr (HELD) {
+#pragma unroll
+    for (int k = 0; k < PICK_HELD; ++k) {
+      const int j = k * THREADS + tid;
+      held[k] = j < N ? keys[j] : 0;
+    }
+  }
+  // f(page, key) of the thread's pages in question
+  auto each = [&](auto f) {
+    if constexpr (HELD) {
+#pragma unroll
+      for (int k = 0; k < PICK_HELD; ++k) {
+        const int j = k * THREADS + tid;
+        if (k * THREADS >= N) break;                // uniform
+        if (j >= j0 && j < j1) f(j, held[k]);
+      }
+    } else {
+      for (int j = j0 + tid; j < j1; j += THREADS) f(j, keys[j]);
+    }
+  };
+  auto clear = [&] { *reinterpret_cast<int4*>(bins + tid * 4) = make_int4(0, 0, 0, 0); };
   int need = p.count - p.sinks - p.recent;
   // taken: keys above `edge`, and of those equal to it the ones up to page `last`
   uint64_t edge = ~0ull;
   int last = -1;
   if (need > 0) {
-    uint64_t lo = ~0ull, hi = 0;
-    for (int j = j0 + tid; j < j1; j += THREADS) {
-      const uint64_t k = keys[j];
-      lo = min(lo, k);
-      hi = max(hi, k);
-    }
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      lo = min(lo, (uint64_t)__shfl_xor((unsigned long long)lo, o));
-      hi = max(hi, (uint64_t)__shfl_xor((unsigned long long)hi, o));
-    }
+    uint32_t low = ~0u, high = 0;                   // of the keys' upper halves
+    each([&](int, uint64_t k) {
+      low = min(low, (uint32_t)(k >> 32));
+      high = max(high, (uint32_t)(k >> 32));
+    });
+    low = wave_reduce(low, [](uint32_t x, uint32_t y) { return min(x, y); });
+    high = wave_reduce(high, [](uint32_t x, uint32_t y) { return max(x, y); });
     if (lane == 0) {
-      range[0][wave] = lo;
-      range[1][wave] = hi;
+      lows[wave] = low;
+      highs[wave] = high;
     }
+    if (tid == 0) n_list = 0;
+    clear();
     __syncthreads();
+#pragma unroll
     for (int w = 0; w < WAVES; ++w) {
-      lo = min(lo, range[0][w]);
-      hi = max(hi, range[1][w]);
+      low = min(low, lows[w]);
+      high = max(high, highs[w]);
     }
+    uint64_t lo = (uint64_t)low << 32, hi = (uint64_t)high << 32 | 0xFFFFFFFFull;
     int left = j1 - j0;                             // keys in [lo, hi]
-    // each round leaves fewer parts of the range: at most six for 64 bits
+    // each round leaves a shorter range: at most seven for 64 bits
     while (left > PICK_LIST && lo < hi) {
-      const int bits = 64 - __builtin_clzll(hi - lo), shift = max(bits - 11, 0);
+      const int shift = max(64 - __builtin_clzll(hi - lo) - BIN_BITS, 0);
+      each([&](int, uint64_t k) {
+        if (k >= lo && k <= hi) atomicAdd(&bins[(int)((hi - k) >> shift)], 1);
+      });
       __syncthreads();
-      for (int i = tid; i < PICK_BINS; i += THREADS) bins[i] = 0;
-      __syncthreads();
-      for (int j = j0 + tid; j < j1; j += THREADS) {
-        const uint64_t k = keys[j];
-        if (k >= lo && k <= hi) atomicAdd(&bins[(int)((k - lo) >> shift)], 1);
-      }
-      __syncthreads();
-      // from the top: thread i takes the bins PER * i .. of the reversed order
-      constexpr int PER = PICK_BINS / THREADS;
-      int own[PER], sum = 0;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        own[i] = bins[PICK_BINS - 1 - (tid * PER + i)];
-        sum += own[i];
-      }
-      int run = sum;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int up = __shfl_up(run, o);
-        if (lane >= o) run += up;
-      }
+      const int4 own4 = *reinterpret_cast<const int4*>(bins + tid * 4);
+      const int own[4] = {own4.x, own4.y, own4.z, own4.w}, sum = own[0] + own[1] + own[2] + own[3];
+      const int run = (int)wave_scan((uint32_t)sum);
       if (lane == 63) sums[wave] = run;
+      clear();
       __syncthreads();
       int before = run - sum;
-      for (int w = 0; w < wave; ++w) before += sums[w];
-      if (before < need && before + sum >= need) {  // one thread's: left >= need
-        int i = 0;
 #pragma unroll
-        for (int k = 0; k < PER; ++k)
-          if (i == k && before + own[k] < need) {
+      for (int w = 0; w < WAVES; ++w) before += w < wave ? sums[w] : 0;
+      if (before < need && before + sum >= need) {  // one thread's: left >= need
+        int bin = tid * 4;
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          if (bin == tid * 4 + k && before + own[k] < need) {
             before += own[k];
-            i = k + 1;
+            ++bin;
           }
-        found[0] = PICK_BINS - 1 - (tid * PER + i);
+        found[0] = bin;
         found[1] = before;
-        found[2] = bins[found[0]];
+        found[2] = own[bin - tid * 4 == 0 ? 0 : bin - tid * 4 == 1 ? 1 : bin - tid * 4 == 2 ? 2 : 3];
       }
       __syncthreads();
-      const uint64_t bin = (uint64_t)found[0];
       need -= found[1];
       left = found[2];
-      const uint64_t low = lo + (bin << shift);
-      const uint64_t part = (1ull << shift) - 1;
-      if (hi - low > part) hi = low + part;
-      lo = low;
-      __syncthreads();                              // found and bins are free
+      const uint64_t top = hi - ((uint64_t)found[0] << shift), part = (1ull << shift) - 1;
+      lo = top - lo > part ? top - part : lo;
+      hi = top;
     }
     edge = lo;
     if (left == need) {                             // all of them: keys from lo on
       last = N;
-    } else if (lo == hi && left > PICK_LIST) {      // equal keys: the first `need` of them
+    } else if (left <= PICK_LIST) {
+      each([&](int j, uint64_t k) {
+        if (k >= lo && k <= hi) {
+          const int i = atomicAdd(&n_list, 1);
+          list[i] = k;
+          list_at[i] = j;
+        }
+      });
+      __syncthreads();
+      if (wave == 0) {
+        const uint64_t k = lane < left ? list[lane] : 0;
+        const int j = lane < left ? list_at[lane] : 0;
+        int rank = 0;
+        for (int i = 0; i < left; ++i) {            // (uniform)
+          const uint64_t o = from_lane(k, i);
+          rank += o > k || (o == k && __builtin_amdgcn_readlane(j, i) < j) ? 1 : 0;
+        }
+        if (lane < left && rank == need - 1) {
+          last_key = k;
+          last_at = j;
+        }
+      }
+      __syncthreads();
+      edge = last_key;
+      last = last_at;
+    } else {                                        // equal keys: the first `need` of them
       int seen = 0;
       for (int i0 = j0; i0 < j1; i0 += THREADS) {
         const int j = i0 + tid;
@@ -349,60 +384,53 @@ __global__ void __launch_bounds__(THREADS) select_pick_kernel(SelectParams p) {
           if (w < wave) at += sums[w];
           seen += sums[w];
         }
-        if (is && at == need - 1) found[3] = j;
+        if (is && at == need - 1) last_at = j;
         if (seen >= need) break;                    // uniform
       }
       __syncthreads();
-      last = found[3];
-    } else {
-      if (tid == 0) found[0] = 0;
-      __syncthreads();
-      for (int j = j0 + tid; j < j1; j += THREADS) {
-        const uint64_t k = keys[j];
-        if (k >= lo && k <= hi) {
-          const int at = atomicAdd(&found[0], 1);
-          list[at] = k;
-          list_at[at] = j;
-        }
-      }
-      __syncthreads();
-      for (int i = tid; i < left; i += THREADS) {
-        const uint64_t k = list[i];
-        const int j = list_at[i];
-        int rank = 0;
-        for (int o = 0; o < left; ++o) rank += list[o] > k || (list[o] == k && list_at[o] < j) ? 1 : 0;
-        if (rank == need - 1) {
-          range[0][0] = k;
-          found[3] = j;
-        }
-      }
-      __syncthreads();
-      edge = range[0][0];
-      last = found[3];
+      last = last_at;
     }
   }
   // in the order of the pages
-  int base = 0;
-  for (int i0 = 0; i0 < N; i0 += THREADS) {
-    const int j = i0 + tid;
-    bool in = false;
-    if (j < N) {
-      in = j < j0 || j >= j1;
-      if (!in) {
-        const uint64_t k = keys[j];
-        in = k > edge || (k == edge && j <= last);
+  auto in = [&](int j, uint64_t k) { return j < N && (j < j0 || j >= j1 || k > edge || (k == edge && j <= last)); };
+  const uint64_t below = (1ull << lane) - 1;
+  if constexpr (HELD) {
+    uint64_t mask[PICK_HELD];
+    __syncthreads();                                // `sums` is free
+#pragma unroll
+    for (int k = 0; k < PICK_HELD; ++k) {
+      mask[k] = __ballot(in(k * THREADS + tid, held[k]));
+      if (lane == 0) sums[k * WAVES + wave] = __builtin_popcountll(mask[k]);
+    }
+    __syncthreads();
+    int base = 0;
+#pragma unroll
+    for (int k = 0; k < PICK_HELD; ++k) {
+      if (k * THREADS >= N) break;                  // uniform
+      int at = base;
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) {
+        at += w < wave ? sums[k * WAVES + w] : 0;
+        base += sums[k * WAVES + w];
       }
+      if (mask[k] >> lane & 1) out[at + __builtin_popcountll(mask[k] & below)] = entry(k * THREADS + tid);
     }
-    const uint64_t mask = __ballot(in);
-    __syncthreads();
-    if (lane == 0) sums[wave] = __builtin_popcountll(mask);
-    __syncthreads();
-    int at = base + __builtin_popcountll(mask & ((1ull << lane) - 1));
-    for (int w = 0; w < WAVES; ++w) {
-      if (w < wave) at += sums[w];
-      base += sums[w];
+  } else {
+    int base = 0;
+    for (int i0 = 0; i0 < N; i0 += THREADS) {
+      const int j = i0 + tid;
+      const bool is = j < N && in(j, keys[j]);
+      const uint64_t mask = __ballot(is);
+      __syncthreads();
+      if (lane == 0) sums[wave] = __builtin_popcountll(mask);
+      __syncthreads();
+      int at = base + __builtin_popcountll(mask & below);
+      for (int w = 0; w < WAVES; ++w) {
+        if (w < wave) at += sums[w];
+        base += sums[w];
+      }
+      if (is) out[at] = entry(j);
     }
-    if (in) out[at] = entry(j);
   }
 }
 
@@ -485,8 +513,9 @@ int launch_select_pages(const SelectPagesArgs& a, hipStream_t stream) {
     if (hipGetLastError() != hipSuccess) return BSFP8_EHIP;
   }
   const dim3 grid((unsigned)(a.B * a.T * a.heads));
-  if (p.width <= 2048) hipLaunchKernelGGL(select_pick_kernel<256>, grid, dim3(256), 0, stream, p);
-  else hipLaunchKernelGGL(select_pick_kernel<1024>, grid, dim3(1024), 0, stream, p);
+  if (p.width <= 256 * PICK_HELD) hipLaunchKernelGGL((select_pick_kernel<256, true>), grid, dim3(256), 0, stream, p);
+  else if (p.width <= 1024 * PICK_HELD) hipLaunchKernelGGL((select_pick_kernel<1024, true>), grid, dim3(1024), 0, stream, p);
+  else hipLaunchKernelGGL((select_pick_kernel<1024, false>), grid, dim3(1024), 0, stream, p);
   return hip_status(hipGetLastError());
 }
 

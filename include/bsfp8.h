@@ -503,7 +503,7 @@ BSFP8_API int bsfp8_residual_norm(const void* h, int64_t ldh, int h_dtype, const
  *   starts     : int32_t [B + 1]: tokens added before each request. held: int32_t [B]: tokens that the request has pages
  *                for: new_lens[b] unless pages ran out (or the table's width did); pass it as the next call's lens.
  *   counts     : int32_t [4]: tokens added, pages taken, pages given back, pages lacking.
- * A page lacking has entry -1 in the table (none past its width) and its tokens slot -1. B <= 2^20, page >= 1,
+ * A page lacking has entry -1 in the table (none past its width) and its tokens slot -1. B <= 2^16, page >= 1,
  * B * ld_pages < 2^31, R < 2^31 - 4096; starts and counts end at 2^31 - 1. Nothing of a request's table is read but the pages of lens[b].
  * Outputs must not overlap inputs or each other (BSFP8_EINVAL). */
 BSFP8_API int bsfp8_step_tables(const int32_t* lens, const int32_t* new_lens, int64_t B, int64_t page, int32_t* pages,

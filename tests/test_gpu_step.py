@@ -109,6 +109,18 @@ def test_norm(case):
     assert torch.equal(mine, out) and torch.equal(x3, x) and (wide[:, W:] == 7).all()
 
 
+@pytest.mark.parametrize("W", [8, 72, 96, 128, 136, 256, 264, 288, 8192, 8200, 24000])
+@pytest.mark.parametrize("f32", [False, True])
+def test_norm_of_every_layout(W, f32):
+    """Several rows in a wave, rows of a workgroup of one, two and four groups a thread; more rows than fit at once."""
+    case = (33 if W > 512 else 9001, W, f32, "row", True, W % 32 == 0)
+    h, y, w, p, g = norm_inputs(case)
+    out, x = B.bsfp8_residual_norm(h, y, weight=w, post_weight=p, gate=g, scale=-0.7)
+    check_norm(h, y, w, p, g, -0.7, out, x, None)
+    out, x = B.bsfp8_residual_norm(h, y, weight=w, scale=2.0, mx=case[5])
+    check_norm(h, y, w, None, None, 2.0, out, None if case[5] else x, x if case[5] else None)
+
+
 @pytest.mark.parametrize("W", [64, 2560])
 def test_norm_without_a_block(W):
     h = norm_inputs((6, W, True, None, False, False))[0]
@@ -546,3 +558,21 @@ def test_a_selection_workspace_serves_smaller_calls():
         a = B.bsfp8_select_pages(q, bounds, pages, lens, 20, 16, ws=ws)
         b = B.bsfp8_select_pages(q, bounds, pages, lens, 20, 16)
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("pages", [8192, 8193, 20000])
+def test_selection_of_very_many_pages(pages):
+    """Keys that are held and keys that are read again in every round; equal ones among them."""
+    choose(270, 1, 2, 1, 64, 16, [pages * 16 - 3], 50, attend=False)
+
+    def few(qt, q, bounds, table, n):
+        bounds.copy_(torch.randint(-2, 3, (n, 1, 1, 1), generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).expand_as(bounds))
+        qt[:], q[:] = 1, 1
+    for count in (7, pages // 5, pages - 9):
+        choose(271, 1, 2, 1, 64, 16, [pages * 16 - 3], count, change=few, attend=False)
+
+
+@pytest.mark.parametrize("left", [63, 64, 65, 66, 67, 68])
+def test_selection_about_the_ranked_number(left):
+    for count in (4, 33, left - 1):
+        choose(280 + left, 1, 2, 1, 64, 16, [(left + 3) * 16], count, attend=False)
