@@ -5,8 +5,10 @@
 //   u = sum_d max(q_d kmin_d, q_d kmax_d)
 // is at least q . k for every key of the page; a page's score for one token and key/value head is the largest u of the
 // query heads that share the head. Bounds are the cache's own values (e4m3 codes times scales, exact in bf16), so they are
-// exact and do not depend on an order. Scores are sums of products of bf16 values in fp64, where they are exact but for
-// queries and keys of extreme range: which page is the last to be taken is a decision between neighbours.
+// exact and do not depend on an order. Which page is the last to be taken is a decision between neighbours, made on scores in
+// fp64, where sums of products of bf16 values are exact but for queries and keys of extreme range; they are found in
+// fp32 with a bound of their error, and only the pages that this leaves undecided are scored again (by fp64 matrix products
+// all of them took 7.9 us for 8 heads of 2048 pages, 17 for 16 sequences of 4 tokens over up to 256).
 
 #include "lanes.h"
 
@@ -25,12 +27,17 @@ struct BoundsParams {
   FastDiv dpage, dheads, dper;
 };
 
+// bf16 pairs as ordered 16-bit integers, and back (the same operation): NaN above infinity or, negative, below minus infinity.
+__device__ __forceinline__ s16x2_t ordered(s16x2_t v) { return v ^ ((v >> 15) & (short)0x7FFF); }
+__device__ __forceinline__ s16x2_t pair_of(uint32_t v) { return __builtin_bit_cast(s16x2_t, v); }
+
 // A wave for each page and head. A token's codes lie on D/16 lanes (16 each; 12 of 16 lanes used for 192), the wave takes
-// 64 / LPT tokens at a time, BATCH such loads in flight; a token past the sequence's end repeats the last one, which
-// changes neither bound. Bound by HBM for a prompt.
+// 64 / LPT tokens at a time, BATCH such loads computed while the next BATCH are on their way; a token past the sequence's
+// end repeats the last one, which changes neither bound. Values are rebuilt as bf16 and compared as ordered integers, two
+// an instruction. Bound by HBM for a prompt, by latency and the code's own fetch for a step's pages.
 template <int D>
 __global__ void __launch_bounds__(256) cache_bounds_kernel(BoundsParams p) {
-  constexpr int LPT = D == 64 ? 4 : D == 128 ? 8 : 16, TOKENS = 64 / LPT, BATCH = 8;
+  constexpr int LPT = D == 64 ? 4 : D == 128 ? 8 : 16, TOKENS = 64 / LPT, BATCH = 4;
   const int lane = threadIdx.x & 63;
   const int64_t item = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (item >= p.items) return;
@@ -51,66 +58,63 @@ __global__ void __launch_bounds__(256) cache_bounds_kernel(BoundsParams p) {
   const int64_t row0 = ((int64_t)id * p.heads + h) * p.page;
   const uint8_t* codes = p.kq + row0 * D + (on ? sub * 16 : 0);
   const uint8_t* scales = p.ks + row0 * (D / 32) + (on ? sub / 2 : 0);
-  float lo[16], hi[16];
+  s16x2_t lo[8], hi[8];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    lo[i] = __builtin_inff();
-    hi[i] = -__builtin_inff();
+  for (int i = 0; i < 8; ++i) {
+    lo[i] = 0x7FFF;
+    hi[i] = -0x8000;
   }
-  uint32_t nan = 0;                                 // bit i: a NaN among value i
-  for (int s0 = 0; s0 < tokens; s0 += TOKENS * BATCH) {
-    u32x4_t w[BATCH];
-    uint32_t e[BATCH];
+  u32x4_t w[BATCH];
+  uint32_t e[BATCH];
+  auto load = [&](int s0) {
 #pragma unroll
     for (int n = 0; n < BATCH; ++n) {
       const int at = min(s0 + n * TOKENS + tok, tokens - 1);
       w[n] = *reinterpret_cast<const u32x4_t*>(codes + (int64_t)at * D);
       e[n] = scales[(int64_t)at * (D / 32)];
     }
+  };
+  load(0);
+#pragma unroll 1
+  for (int s0 = 0; s0 < tokens; s0 += TOKENS * BATCH) {
+    u32x4_t c[BATCH];
+    float f[BATCH];
 #pragma unroll
     for (int n = 0; n < BATCH; ++n) {
-      if (s0 + n * TOKENS >= tokens) break;         // uniform
-      const float f = block_scale(e[n]);
-      const bf16x8_t a = dequant8(w[n][0], w[n][1], f), c = dequant8(w[n][2], w[n][3], f);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float x = (float)a[i], y = (float)c[i];
-        lo[i] = fminf(lo[i], x);
-        hi[i] = fmaxf(hi[i], x);
-        lo[8 + i] = fminf(lo[8 + i], y);
-        hi[8 + i] = fmaxf(hi[8 + i], y);
-      }
-      uint32_t code = 0;                            // a NaN code is all ones but its sign
-#pragma unroll
-      for (int i = 0; i < 4; ++i) code |= ((w[n][i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-      if (__any(code != 0 || e[n] == 255)) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) nan |= ((float)a[i] != (float)a[i] ? 1u : 0u) << i | ((float)c[i] != (float)c[i] ? 1u : 0u) << (8 + i);
-      }
+      c[n] = w[n];
+      f[n] = block_scale(e[n]);
     }
+    if (s0 + TOKENS * BATCH < tokens) load(s0 + TOKENS * BATCH);
+#pragma unroll
+    for (int n = 0; n < BATCH; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const s16x2_t x = ordered(pair_of(bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[n][i], f[n], false))));
+        const s16x2_t y = ordered(pair_of(bits_of(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[n][i], f[n], true))));
+        lo[2 * i] = __builtin_elementwise_min(lo[2 * i], x);
+        hi[2 * i] = __builtin_elementwise_max(hi[2 * i], x);
+        lo[2 * i + 1] = __builtin_elementwise_min(lo[2 * i + 1], y);
+        hi[2 * i + 1] = __builtin_elementwise_max(hi[2 * i + 1], y);
+      }
   }
+#pragma unroll 1
+  for (int o = LPT; o < 64; o <<= 1)
 #pragma unroll
-  for (int o = LPT; o < 64; o <<= 1) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      lo[i] = fminf(lo[i], __shfl_xor(lo[i], o));
-      hi[i] = fmaxf(hi[i], __shfl_xor(hi[i], o));
+    for (int i = 0; i < 8; ++i) {
+      lo[i] = __builtin_elementwise_min(lo[i], pair_of((uint32_t)__shfl_xor((int)__builtin_bit_cast(uint32_t, lo[i]), o)));
+      hi[i] = __builtin_elementwise_max(hi[i], pair_of((uint32_t)__shfl_xor((int)__builtin_bit_cast(uint32_t, hi[i]), o)));
     }
-    nan |= (uint32_t)__shfl_xor((int)nan, o);
-  }
-  if (nan) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (nan >> i & 1) lo[i] = hi[i] = __uint_as_float(0x7FC00000u);
-  }
   if (tok < 2 && on) {                              // lane group 0 stores the least values, 1 the largest
-    uint16_t* dst = p.bounds + (((int64_t)id * p.heads + h) * 2 + tok) * D + sub * 16;
     u32x4_t o[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      o[i >> 2][i & 3] = tok ? pack_bf16x2(hi[2 * i], hi[2 * i + 1]) : pack_bf16x2(lo[2 * i], lo[2 * i + 1]);
-    reinterpret_cast<u32x4_t*>(dst)[0] = o[0];
-    reinterpret_cast<u32x4_t*>(dst)[1] = o[1];
+    for (int i = 0; i < 8; ++i) {
+      const s16x2_t nan = (hi[i] > (short)0x7F80) | (lo[i] < (short)-0x7F81);   // (-0x7F81: minus infinity, ordered)
+      const s16x2_t v = ordered(tok ? hi[i] : lo[i]);
+      o[i >> 2][i & 3] = __builtin_bit_cast(uint32_t, (v & ~nan) | (nan & (short)0x7FC0));
+    }
+    u32x4_t* dst = reinterpret_cast<u32x4_t*>(p.bounds + (((int64_t)id * p.heads + h) * 2 + tok) * D + sub * 16);
+    dst[0] = o[0];
+    dst[1] = o[1];
   }
 }
 
@@ -120,10 +124,11 @@ __global__ void __launch_bounds__(256) cache_bounds_kernel(BoundsParams p) {
 struct SelectParams {
   const uint16_t *q, *bounds;
   const int32_t *pages, *lens, *nodes;
-  uint64_t* keys;                                   // [B * T][heads][width]
+  float2* scores;                                   // [B * T][heads][width]: a page's score in fp32, and how far it may be off
+  uint64_t* keys;                                   // [B * T][heads][width]: exact ones, where they are needed
   int32_t *selected, *held;
   int64_t ldq, ld_pages, n_pages;
-  int B, T, hq, heads, g, page, max_len, width, count, sinks, recent;
+  int B, T, hq, heads, g, dim, page, max_len, width, count, sinks, recent;
   int gp, tokens, blocks;                           // see select_score_kernel
   FastDiv dpage;
 };
@@ -135,21 +140,20 @@ __device__ __forceinline__ int positions_seen(const SelectParams& p, int b, int 
 }
 __device__ __forceinline__ int pages_for(const SelectParams& p, int n) { return n > 0 ? fdiv(n - 1, p.dpage) + 1 : 0; }
 
-// Scores ordered as integers: a page that does not exist 0, else above it; infinite for bounds or queries that are not finite.
-__device__ __forceinline__ uint64_t score_key(double u) {
-  u += 0.0;                                         // -0 is 0
-  const uint64_t b = __builtin_bit_cast(uint64_t, u);
-  return b >> 63 ? ~b : b | 0x8000000000000000ull;
-}
+// How far an fp32 score may be off, as a share of the sum of its terms' magnitudes. The sum is at most 16 matrix products of
+// 32 values with fp32 accumulation; measured over random, cancelling and wide-ranged values its error is below 2^-20.7 of
+// that, and neither inputs nor results are flushed. 2^-18 for the sum, as much again for the rounding of what is
+// compared with it.
+constexpr float SCORE_ERROR = 0x1p-17f;
+constexpr float SCORE_TINY = 0x1p-126f;             // what fp32 cannot hold
 
-typedef double f64x4_t __attribute__((ext_vector_type(4)));
+typedef short s16x8_t __attribute__((ext_vector_type(8)));
 
-// One wave scores 16 pages of a sequence and head for all of its tokens, by fp64 matrix products of 16 rows x 16 pages x 4
-// values: the row's positive part times the largest values plus its negative part times the least. A lane loads eight
-// neighbouring values of its page (lane % 16) and row at a time; which of them meet in one product is free as long as
-// both sides agree. Rows: the g query heads of a token are filled up to gp = 1, 2, 4, 8 or 16 by repeating the last one
-// (or take several blocks of 16), so that a token's maximum is taken over whole registers and lane groups; `tokens` of
-// them in a block of rows. Element r of a lane's result is row 4 r + lane / 16 of its page.
+// One wave scores 16 pages of a sequence and head for all of its tokens in bf16 matrix products of 16 rows x 16 pages: the
+// rows' positive parts times the largest values plus their negative parts times the least; and the magnitudes' product,
+// for the error. Rows: the g query heads of a token are filled up to gp = 1, 2, 4, 8 or 16 by repeating the last one (or take
+// several blocks of 16), so that a token's maximum is taken over whole registers and lane groups; `tokens` of them in
+// a block of rows. Element r of a lane's result is row 4 * (lane / 16) + r of page lane % 16.
 template <int D>
 __global__ void __launch_bounds__(256) select_score_kernel(SelectParams p) {
   constexpr int STEPS = D / 32;
@@ -162,84 +166,235 @@ __global__ void __launch_bounds__(256) select_score_kernel(SelectParams p) {
   const int id = j < most ? p.pages[(int64_t)b * p.ld_pages + j] : -1;
   const bool there = id >= 0 && id < p.n_pages;
   const uint16_t* at = p.bounds + ((int64_t)(there ? id : 0) * p.heads + h) * 2 * D + q4 * 8;
-  u32x4_t lo[STEPS], hi[STEPS];
+  s16x8_t lo[STEPS], hi[STEPS], big[STEPS];
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) {
-    lo[s] = *reinterpret_cast<const u32x4_t*>(at + s * 32);
-    hi[s] = *reinterpret_cast<const u32x4_t*>(at + D + s * 32);
+    lo[s] = *reinterpret_cast<const s16x8_t*>(at + s * 32);
+    hi[s] = *reinterpret_cast<const s16x8_t*>(at + D + s * 32);
   }
-  for (int rb = 0; rb * p.tokens < p.T; ++rb) {
-    double best[4];                                 // largest so far: by register, over a token's blocks of heads
+  auto as_bf16 = [](s16x8_t v) { return __builtin_bit_cast(bf16x8_t, v); };
+  const s16x8_t zero = 0, no_sign = 0x7FFF;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) best[r] = -__builtin_inf();
-    const int t = rb * p.tokens + (p.blocks > 1 ? 0 : r16 / p.gp);
+  for (int s = 0; s < STEPS; ++s) big[s] = __builtin_elementwise_max(lo[s] & no_sign, hi[s] & no_sign);
+  const int gp = p.blocks > 1 ? 16 : p.gp;
+  for (int rb = 0; rb * p.tokens < p.T; ++rb) {
+    float best[4], off[4];                          // largest so far: by register, over a token's blocks of heads
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      best[r] = -__builtin_inff();
+      off[r] = 0.f;
+    }
+    const int t = rb * p.tokens + (p.blocks > 1 ? 0 : r16 / gp);
     for (int blk = 0; blk < p.blocks; ++blk) {
-      const int head = min(blk * 16 + (p.blocks > 1 ? r16 : r16 % p.gp), p.g - 1);
+      const int head = min(blk * 16 + (p.blocks > 1 ? r16 : r16 % gp), p.g - 1);
       const uint16_t* qr = p.q + ((int64_t)b * p.T + min(t, p.T - 1)) * p.ldq + ((int64_t)h * p.g + head) * D + q4 * 8;
-      f64x4_t acc = {0, 0, 0, 0};
+      f32x4_t sum = {0.f, 0.f, 0.f, 0.f}, size = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int s = 0; s < STEPS; ++s) {
-        const u32x4_t w = *reinterpret_cast<const u32x4_t*>(qr + s * 32);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t shift = i & 1 ? 0 : 16;
-          const float x = __uint_as_float((w[i / 2] << shift) & 0xFFFF0000u);
-          const float l = __uint_as_float((lo[s][i / 2] << shift) & 0xFFFF0000u);
-          const float m = __uint_as_float((hi[s][i / 2] << shift) & 0xFFFF0000u);
-          // (NaN passes to both)
-          acc = __builtin_amdgcn_mfma_f64_16x16x4f64((double)(x <= 0.f ? 0.f : x), (double)m, acc, 0, 0, 0);
-          acc = __builtin_amdgcn_mfma_f64_16x16x4f64((double)(x >= 0.f ? 0.f : x), (double)l, acc, 0, 0, 0);
-        }
+        const s16x8_t x = *reinterpret_cast<const s16x8_t*>(qr + s * 32);
+        // (bf16 compare with 0 as integers do; a NaN stays in one of them)
+        sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(__builtin_elementwise_max(x, zero)), as_bf16(hi[s]), sum, 0, 0, 0);
+        sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(__builtin_elementwise_min(x, zero)), as_bf16(lo[s]), sum, 0, 0, 0);
+        size = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16(x & no_sign), as_bf16(big[s]), size, 0, 0, 0);
       }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const double u = __builtin_fabs(acc[r]) < __builtin_inf() ? acc[r] : __builtin_inf();
-        best[r] = fmax(best[r], u);
+      for (int r = 0; r < 4; ++r) {                 // (magnitudes that are not finite: nothing is known)
+        const bool fine = size[r] < __builtin_inff();
+        best[r] = fmaxf(best[r], fine ? sum[r] : 0.f);
+        off[r] = fmaxf(off[r], fine ? size[r] : __builtin_inff());
       }
     }
     // over the rows of a token: 16 / gp tokens in the block
-    const int gp = p.blocks > 1 ? 16 : p.gp;
+    auto join = [&](int r, int o) {
+      best[r] = fmaxf(best[r], best[o]);
+      off[r] = fmaxf(off[r], off[o]);
+    };
+    if (gp >= 2) {
+      join(0, 1);
+      join(2, 3);
+    }
+    if (gp >= 4) join(0, 2);
+#pragma unroll
+    for (int r = 0; r < 4; r += 2) {
+      if (gp >= 8) {
+        best[r] = fmaxf(best[r], __shfl_xor(best[r], 16));
+        off[r] = fmaxf(off[r], __shfl_xor(off[r], 16));
+      }
+      if (gp >= 16) {
+        best[r] = fmaxf(best[r], __shfl_xor(best[r], 32));
+        off[r] = fmaxf(off[r], __shfl_xor(off[r], 32));
+      }
+    }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      if (gp >= 2) best[r] = fmax(best[r], __shfl_xor(best[r], 16));
-      if (gp >= 4) best[r] = fmax(best[r], __shfl_xor(best[r], 32));
-    }
-    if (gp >= 8) {
-      best[0] = fmax(best[0], best[1]);
-      best[2] = fmax(best[2], best[3]);
-    }
-    if (gp >= 16) best[0] = fmax(best[0], best[2]);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 4 * r + q4, tt = rb * p.tokens + row / gp;
+      const int row = 4 * q4 + r, tt = rb * p.tokens + row / gp;
       if (row % gp == 0 && tt < p.T && j < most)
-        p.keys[(((int64_t)b * p.T + tt) * p.heads + h) * p.width + j] = there ? score_key(best[r]) : 0ull;
+        p.scores[(((int64_t)b * p.T + tt) * p.heads + h) * p.width + j] =
+            there ? make_float2(best[r], off[r] * SCORE_ERROR + SCORE_TINY) : make_float2(-__builtin_inff(), 0.f);
     }
   }
+}
+
+// Scores as ordered integers (-0 is 0).
+__device__ __forceinline__ uint32_t score_key(float u) {
+  const uint32_t b = __float_as_uint(u + 0.f);
+  return b ^ (b >> 31 ? ~0u : 0x80000000u);
+}
+__device__ __forceinline__ uint64_t score_key(double u) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, u + 0.0);
+  return b ^ (b >> 63 ? ~0ull : 0x8000000000000000ull);
+}
+
+// The score of one page in 64 bits, by a wave: products of bf16 values are exact there, and so are sums of values of a common
+// range. Infinite where something is not finite. Eight lanes a head, eight heads at a time.
+__device__ __forceinline__ double exact_score(const SelectParams& p, const uint16_t* q, const uint16_t* bound, int lane) {
+  double best = -__builtin_inf();
+#pragma unroll 1
+  for (int h0 = 0; h0 < p.g; h0 += 8) {
+    const uint16_t* x = q + min(h0 + (lane >> 3), p.g - 1) * p.dim;
+    double a = 0;
+#pragma unroll 2
+    for (int d = (lane & 7) * 8; d < p.dim; d += 64) {
+      const u32x4_t xv = *reinterpret_cast<const u32x4_t*>(x + d), lv = *reinterpret_cast<const u32x4_t*>(bound + d),
+                    hv = *reinterpret_cast<const u32x4_t*>(bound + p.dim + d);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t shift = i & 1 ? 0 : 16;
+        const float v = __uint_as_float((xv[i / 2] << shift) & 0xFFFF0000u), l = __uint_as_float((lv[i / 2] << shift) & 0xFFFF0000u),
+                    m = __uint_as_float((hv[i / 2] << shift) & 0xFFFF0000u);
+        a = fma((double)(v <= 0.f ? 0.f : v), (double)m, fma((double)(v >= 0.f ? 0.f : v), (double)l, a));
+      }
+    }
+    a += dpp<XOR1>(a);
+    a += dpp<XOR2>(a);
+    a += dpp<HALF_MIRROR>(a);
+    best = fmax(best, __builtin_fabs(a) < __builtin_inf() ? a : __builtin_inf());
+  }
+  for (int o = 8; o < 64; o <<= 1) best = fmax(best, __shfl_xor(best, o));
+  return best;
 }
 
 // ---------------------------------------------------------------------------------------------
 // the pages with the largest scores
 // ---------------------------------------------------------------------------------------------
 constexpr int PICK_LIST = 64;                       // keys that one wave ranks against each other
-constexpr int PICK_HELD = 8;                        // keys of a thread, where they are held
+
+template <int THREADS>
+struct PickShared {
+  static constexpr int WAVES = THREADS / 64, BINS = THREADS * 4;
+  __align__(16) int bins[BINS];
+  uint64_t list[PICK_LIST], open[PICK_LIST];
+  int list_at[PICK_LIST], sums[8 * WAVES], found[3], n_list, last_at;
+  uint32_t low[WAVES], high[WAVES], off[WAVES];
+};
+
+// The `need`-th largest of `left` keys in [lo, hi], the lower index first among equals: keys above `edge` are before it, and
+// of those equal to it the ones up to index `last`. By histograms over the range in question: each splits it into
+// 4 * THREADS parts and keeps the one that holds the border; what is left then, usually a handful, one wave ranks.
+// each(f): f(index, key) of the thread's keys; at(i): key i, or one outside [lo, hi], of the thread of i % THREADS;
+// VALUE: only `edge` is wanted. Whole workgroup; bins and n_list hold zeros, before and after.
+template <int THREADS, bool VALUE, typename K, typename Each, typename At>
+__device__ __forceinline__ void find_border(PickShared<THREADS>& s, Each each, At at, int end, int left, int need, K lo, K hi, K& edge,
+                                            int& last) {
+  using S = PickShared<THREADS>;
+  constexpr int BIN_BITS = THREADS == 256 ? 10 : 12, KEY_BITS = sizeof(K) * 8;
+  static_assert(S::BINS == 1 << BIN_BITS, "bins");
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  while (left > PICK_LIST && lo < hi) {             // each round leaves a shorter range: at most seven
+    const int bits = KEY_BITS == 64 ? 64 - __builtin_clzll((uint64_t)(hi - lo)) : 32 - __builtin_clz((uint32_t)(hi - lo));
+    const int shift = max(bits - BIN_BITS, 0);
+    each([&](int, K k) {
+      if (k >= lo && k <= hi) atomicAdd(&s.bins[(int)((hi - k) >> shift)], 1);
+    });
+    __syncthreads();
+    const int4 own4 = *reinterpret_cast<const int4*>(s.bins + tid * 4);
+    const int own[4] = {own4.x, own4.y, own4.z, own4.w}, sum = own[0] + own[1] + own[2] + own[3];
+    const int run = (int)wave_scan((uint32_t)sum);
+    if (lane == 63) s.sums[wave] = run;
+    *reinterpret_cast<int4*>(s.bins + tid * 4) = make_int4(0, 0, 0, 0);
+    __syncthreads();
+    int before = run - sum;
+#pragma unroll
+    for (int w = 0; w < S::WAVES; ++w) before += w < wave ? s.sums[w] : 0;
+    if (before < need && before + sum >= need) {    // one thread's: left >= need
+      int bin = 0, count = own[0];
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        if (bin == k && before + own[k] < need) {
+          before += own[k];
+          bin = k + 1;
+          count = own[k + 1];
+        }
+      s.found[0] = tid * 4 + bin;
+      s.found[1] = before;
+      s.found[2] = count;
+    }
+    __syncthreads();
+    need -= s.found[1];
+    left = s.found[2];
+    const K top = hi - ((K)s.found[0] << shift), part = ((K)1 << shift) - 1;
+    lo = top - lo > part ? top - part : lo;
+    hi = top;
+  }
+  edge = lo;
+  last = end;
+  if (left == need && !VALUE) return;               // all of them: keys from lo on
+  if (left <= PICK_LIST) {
+    each([&](int j, K k) {
+      if (k >= lo && k <= hi) {
+        const int i = atomicAdd(&s.n_list, 1);
+        s.list[i] = k;
+        s.list_at[i] = j;
+      }
+    });
+    __syncthreads();
+    // (every wave does, which saves a barrier)
+    const uint64_t k = lane < left ? s.list[lane] : 0;
+    const int j = lane < left ? s.list_at[lane] : 0;
+    int rank = 0;
+    for (int i = 0; i < left; ++i) {                // (uniform)
+      const uint64_t o = from_lane(k, i);
+      rank += o > k || (o == k && __builtin_amdgcn_readlane(j, i) < j) ? 1 : 0;
+    }
+    const uint64_t is = __ballot(lane < left && rank == need - 1);
+    if (is) {                                       // (always)
+      edge = (K)from_lane(k, __builtin_ctzll(is));
+      last = __builtin_amdgcn_readlane(j, __builtin_ctzll(is));
+    }
+    if (tid == 0) s.n_list = 0;
+  } else if (!VALUE) {                              // equal keys: the first `need` of them
+    int seen = 0;
+    for (int i0 = 0; i0 < end; i0 += THREADS) {
+      const bool is = i0 + tid < end && at(i0 + tid) == lo;
+      const uint64_t mask = __ballot(is);
+      __syncthreads();
+      if (lane == 0) s.sums[wave] = __builtin_popcountll(mask);
+      __syncthreads();
+      int place = seen + __builtin_popcountll(mask & ((1ull << lane) - 1));
+      for (int w = 0; w < S::WAVES; ++w) {
+        if (w < wave) place += s.sums[w];
+        seen += s.sums[w];
+      }
+      if (is && place == need - 1) s.last_at = i0 + tid;
+      if (seen >= need) break;                      // uniform
+    }
+    __syncthreads();
+    last = s.last_at;
+  }
+}
 
 // The list of one token and head (a workgroup): the first `sinks` and the last `recent` of its N pages and, of the others,
-// those with the largest keys, the lower index first among equals. The least key that is taken is found by histograms of
-// the keys still in question, over the range that they span: each splits it into up to 4 * THREADS parts, keeps the one that
-// holds the border, and usually leaves a handful after the first, which one wave ranks against each other. What is in the
-// list is then counted off in the order of the pages. HELD: the keys stay in registers, PICK_HELD a thread (else they
-// are read again in each round).
-template <int THREADS, bool HELD>
+// those with the largest scores, the earlier page first among equals.
+//
+// With v the border among the fp32 scores and d the largest distance that one of them may be off, the border among the
+// exact scores is within d of v (the k-th largest moves no further than the values do). So a page whose score is above v + d
+// by more than it may be off itself is taken, one as far below v - d is not, and only the few between, often just the
+// border's own page, are scored again in 64 bits, by the waves that hold them, and ranked by that.
+// HELD: scores that a thread holds in registers (0: they are read again in each round).
+template <int THREADS, int HELD>
 __global__ void __launch_bounds__(THREADS) select_pick_kernel(SelectParams p) {
-  constexpr int WAVES = THREADS / 64, BINS = THREADS * 4, BIN_BITS = THREADS == 256 ? 10 : 12;
-  static_assert(BINS == 1 << BIN_BITS, "bins");
-  __shared__ __align__(16) int bins[BINS];
-  __shared__ uint64_t list[PICK_LIST];
-  __shared__ int list_at[PICK_LIST];
-  __shared__ uint32_t lows[WAVES], highs[WAVES];
-  __shared__ int sums[HELD ? PICK_HELD * WAVES : WAVES], found[3], n_list, last_at;
-  __shared__ uint64_t last_key;
+  constexpr int WAVES = THREADS / 64;
+  __shared__ PickShared<THREADS> s;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = blockIdx.x / p.heads, h = blockIdx.x - r * p.heads, b = r / p.T;
   const int n = positions_seen(p, b, r - b * p.T), N = pages_for(p, n);
@@ -257,177 +412,202 @@ __global__ void __launch_bounds__(THREADS) select_pick_kernel(SelectParams p) {
     return;
   }
   // in question: pages sinks .. N - recent - 1 (more than are needed, so N - recent > sinks)
-  const uint64_t* keys = p.keys + ((int64_t)r * p.heads + h) * p.width;
+  const float2* scores = p.scores + ((int64_t)r * p.heads + h) * p.width;
+  uint64_t* keys = p.keys + ((int64_t)r * p.heads + h) * p.width;
   const int j0 = p.sinks, j1 = N - p.recent;
-  uint64_t held[HELD ? PICK_HELD : 1];
-  if constexpr (HELD) {
+  float2 held[HELD > 0 ? HELD : 1];
+  int ids[HELD > 0 ? HELD : 1];
+  if constexpr (HELD > 0) {
 #pragma unroll
-    for (int k = 0; k < PICK_HELD; ++k) {
+    for (int k = 0; k < HELD; ++k) {
       const int j = k * THREADS + tid;
-      held[k] = j < N ? keys[j] : 0;
+      held[k] = j < N ? scores[j] : make_float2(0.f, 0.f);
+      ids[k] = j < N ? entry(j) : -1;
     }
   }
-  // f(page, key) of the thread's pages in question
+  // f(page, score) of the thread's pages in question: those of tid modulo THREADS
   auto each = [&](auto f) {
-    if constexpr (HELD) {
+    if constexpr (HELD > 0) {
 #pragma unroll
-      for (int k = 0; k < PICK_HELD; ++k) {
+      for (int k = 0; k < HELD; ++k) {
         const int j = k * THREADS + tid;
         if (k * THREADS >= N) break;                // uniform
         if (j >= j0 && j < j1) f(j, held[k]);
       }
     } else {
-      for (int j = j0 + tid; j < j1; j += THREADS) f(j, keys[j]);
+      for (int j = tid; j < j1; j += THREADS)
+        if (j >= j0) f(j, scores[j]);
     }
   };
-  auto clear = [&] { *reinterpret_cast<int4*>(bins + tid * 4) = make_int4(0, 0, 0, 0); };
-  int need = p.count - p.sinks - p.recent;
-  // taken: keys above `edge`, and of those equal to it the ones up to page `last`
-  uint64_t edge = ~0ull;
-  int last = -1;
+  const int need = p.count - p.sinks - p.recent;
+  float above = __builtin_inff(), below = __builtin_inff();   // scores that far out are decided
   if (need > 0) {
-    uint32_t low = ~0u, high = 0;                   // of the keys' upper halves
-    each([&](int, uint64_t k) {
-      low = min(low, (uint32_t)(k >> 32));
-      high = max(high, (uint32_t)(k >> 32));
+    uint32_t low = ~0u, high = 0;
+    float off = 0.f;
+    each([&](int, float2 k) {
+      low = min(low, score_key(k.x));
+      high = max(high, score_key(k.x));
+      off = fmaxf(off, k.y);
     });
     low = wave_reduce(low, [](uint32_t x, uint32_t y) { return min(x, y); });
     high = wave_reduce(high, [](uint32_t x, uint32_t y) { return max(x, y); });
+    off = wave_max(off);
     if (lane == 0) {
-      lows[wave] = low;
-      highs[wave] = high;
+      s.low[wave] = low;
+      s.high[wave] = high;
+      s.off[wave] = __float_as_uint(off);
     }
-    if (tid == 0) n_list = 0;
-    clear();
+    if (tid == 0) s.n_list = 0;
+    *reinterpret_cast<int4*>(s.bins + tid * 4) = make_int4(0, 0, 0, 0);
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) {
-      low = min(low, lows[w]);
-      high = max(high, highs[w]);
+      low = min(low, s.low[w]);
+      high = max(high, s.high[w]);
+      off = fmaxf(off, __uint_as_float(s.off[w]));
     }
-    uint64_t lo = (uint64_t)low << 32, hi = (uint64_t)high << 32 | 0xFFFFFFFFull;
-    int left = j1 - j0;                             // keys in [lo, hi]
-    // each round leaves a shorter range: at most seven for 64 bits
-    while (left > PICK_LIST && lo < hi) {
-      const int shift = max(64 - __builtin_clzll(hi - lo) - BIN_BITS, 0);
-      each([&](int, uint64_t k) {
-        if (k >= lo && k <= hi) atomicAdd(&bins[(int)((hi - k) >> shift)], 1);
-      });
-      __syncthreads();
-      const int4 own4 = *reinterpret_cast<const int4*>(bins + tid * 4);
-      const int own[4] = {own4.x, own4.y, own4.z, own4.w}, sum = own[0] + own[1] + own[2] + own[3];
-      const int run = (int)wave_scan((uint32_t)sum);
-      if (lane == 63) sums[wave] = run;
-      clear();
-      __syncthreads();
-      int before = run - sum;
-#pragma unroll
-      for (int w = 0; w < WAVES; ++w) before += w < wave ? sums[w] : 0;
-      if (before < need && before + sum >= need) {  // one thread's: left >= need
-        int bin = tid * 4;
-#pragma unroll
-        for (int k = 0; k < 3; ++k)
-          if (bin == tid * 4 + k && before + own[k] < need) {
-            before += own[k];
-            ++bin;
-          }
-        found[0] = bin;
-        found[1] = before;
-        found[2] = own[bin - tid * 4 == 0 ? 0 : bin - tid * 4 == 1 ? 1 : bin - tid * 4 == 2 ? 2 : 3];
-      }
-      __syncthreads();
-      need -= found[1];
-      left = found[2];
-      const uint64_t top = hi - ((uint64_t)found[0] << shift), part = (1ull << shift) - 1;
-      lo = top - lo > part ? top - part : lo;
-      hi = top;
-    }
-    edge = lo;
-    if (left == need) {                             // all of them: keys from lo on
-      last = N;
-    } else if (left <= PICK_LIST) {
-      each([&](int j, uint64_t k) {
-        if (k >= lo && k <= hi) {
-          const int i = atomicAdd(&n_list, 1);
-          list[i] = k;
-          list_at[i] = j;
-        }
-      });
-      __syncthreads();
-      if (wave == 0) {
-        const uint64_t k = lane < left ? list[lane] : 0;
-        const int j = lane < left ? list_at[lane] : 0;
-        int rank = 0;
-        for (int i = 0; i < left; ++i) {            // (uniform)
-          const uint64_t o = from_lane(k, i);
-          rank += o > k || (o == k && __builtin_amdgcn_readlane(j, i) < j) ? 1 : 0;
-        }
-        if (lane < left && rank == need - 1) {
-          last_key = k;
-          last_at = j;
-        }
-      }
-      __syncthreads();
-      edge = last_key;
-      last = last_at;
-    } else {                                        // equal keys: the first `need` of them
-      int seen = 0;
-      for (int i0 = j0; i0 < j1; i0 += THREADS) {
-        const int j = i0 + tid;
-        const bool is = j < j1 && keys[j] == lo;
-        const uint64_t mask = __ballot(is);
-        __syncthreads();
-        if (lane == 0) sums[wave] = __builtin_popcountll(mask);
-        __syncthreads();
-        int at = seen + __builtin_popcountll(mask & ((1ull << lane) - 1));
-        for (int w = 0; w < WAVES; ++w) {
-          if (w < wave) at += sums[w];
-          seen += sums[w];
-        }
-        if (is && at == need - 1) last_at = j;
-        if (seen >= need) break;                    // uniform
-      }
-      __syncthreads();
-      last = last_at;
-    }
-  }
-  // in the order of the pages
-  auto in = [&](int j, uint64_t k) { return j < N && (j < j0 || j >= j1 || k > edge || (k == edge && j <= last)); };
-  const uint64_t below = (1ull << lane) - 1;
-  if constexpr (HELD) {
-    uint64_t mask[PICK_HELD];
+    uint32_t border;
+    int unused;
+    find_border<THREADS, true, uint32_t>(
+        s, [&](auto f) { each([&](int j, float2 k) { f(j, score_key(k.x)); }); }, [](int) { return 0u; }, j1, j1 - j0, need, low, high,
+        border, unused);
+    const float v = __uint_as_float(border >> 31 ? border ^ 0x80000000u : ~border);
+    above = v + off;
+    below = v - off;
     __syncthreads();                                // `sums` is free
-#pragma unroll
-    for (int k = 0; k < PICK_HELD; ++k) {
-      mask[k] = __ballot(in(k * THREADS + tid, held[k]));
-      if (lane == 0) sums[k * WAVES + wave] = __builtin_popcountll(mask[k]);
-    }
-    __syncthreads();
-    int base = 0;
-#pragma unroll
-    for (int k = 0; k < PICK_HELD; ++k) {
-      if (k * THREADS >= N) break;                  // uniform
-      int at = base;
-#pragma unroll
-      for (int w = 0; w < WAVES; ++w) {
-        at += w < wave ? sums[k * WAVES + w] : 0;
-        base += sums[k * WAVES + w];
+  }
+  auto sure = [&](int j, float2 k) { return j < j0 || (j >= j1 && j < N) || (j < j1 && k.x - k.y > above); };
+  auto open = [&](int j, float2 k) { return need > 0 && j >= j0 && j < j1 && !(k.x - k.y > above) && !(k.x + k.y < below); };
+  const uint16_t* q = p.q + (int64_t)r * p.ldq + (int64_t)h * p.g * p.dim;
+  auto rescore = [&](int id) {                      // (uniform) a page's key in 64 bits
+    return id < 0 ? 0ull : score_key(exact_score(p, q, p.bounds + ((int64_t)id * p.heads + h) * 2 * p.dim, lane));
+  };
+  const uint64_t lower = (1ull << lane) - 1;
+  int n_open = 0, n_sure = 0;
+  uint64_t edge = ~0ull;
+  int last = -1;
+  // many open pages, or not held: their keys through memory, each written and read by its own lane, and the border among those
+  auto find_open = [&] {
+#pragma unroll 1
+    for (int i0 = 0; i0 < j1; i0 += THREADS) {
+      const int j = i0 + tid;
+      uint64_t todo = __ballot(j < j1 && open(j, scores[j]));
+      while (todo) {
+        const int l = __builtin_ctzll(todo);
+        todo &= todo - 1;
+        const uint64_t key = rescore(entry(j - lane + l));
+        if (lane == l) keys[j] = key;
       }
-      if (mask[k] >> lane & 1) out[at + __builtin_popcountll(mask[k] & below)] = entry(k * THREADS + tid);
+    }
+    find_border<THREADS, false, uint64_t>(
+        s, [&](auto f) { each([&](int j, float2 k) { if (open(j, k)) f(j, keys[j]); }); },
+        [&](int j) { return open(j, scores[j]) ? keys[j] : ~0ull; }, j1, n_open, p.count - n_sure, (uint64_t)0, (uint64_t)~0ull, edge, last);
+    __syncthreads();
+  };
+  auto beyond = [&](int j) { return keys[j] > edge || (keys[j] == edge && j <= last); };
+  if constexpr (HELD > 0) {
+    // counted off in the order of the pages: rows of 64, one after another over the waves; sure ones in the lower half of a
+    // count, open ones in the upper (every wave adds the counts up by itself, 64 at a time)
+    constexpr int WORDS = (HELD * WAVES + 63) / 64, PER = 64 / WAVES;   // (PER: rows of a word)
+    uint64_t yes[HELD], maybe[HELD];
+    uint32_t before[WORDS];
+    auto count = [&] {
+#pragma unroll
+      for (int k = 0; k < HELD; ++k)
+        if (lane == 0) s.sums[k * WAVES + wave] = __builtin_popcountll(yes[k]) | __builtin_popcountll(maybe[k]) << 16;
+      __syncthreads();
+      uint32_t base = 0;
+#pragma unroll
+      for (int w = 0; w < WORDS; ++w) {
+        const uint32_t v = w * 64 + lane < HELD * WAVES ? (uint32_t)s.sums[w * 64 + lane] : 0u, run = wave_scan(v);
+        before[w] = base + run - v;
+        base += (uint32_t)__builtin_amdgcn_readlane((int)run, 63);
+      }
+      n_sure = base & 0xFFFF;
+      n_open = base >> 16;
+    };
+    auto at_row = [&](int k) { return (uint32_t)__builtin_amdgcn_readlane((int)before[k / PER], k % PER * WAVES + wave); };
+#pragma unroll
+    for (int k = 0; k < HELD; ++k) {
+      yes[k] = __ballot(sure(k * THREADS + tid, held[k]));
+      maybe[k] = __ballot(open(k * THREADS + tid, held[k]));
+    }
+    count();
+    uint64_t taken = ~0ull;                         // open pages, in order
+    if (n_sure + n_open > p.count) {
+      if (n_open <= PICK_LIST) {
+#pragma unroll
+        for (int k = 0; k < HELD; ++k)
+          if (maybe[k] >> lane & 1) s.list_at[(at_row(k) >> 16) + __builtin_popcountll(maybe[k] & lower)] = ids[k];
+        __syncthreads();
+#pragma unroll 1
+        for (int i = wave; i < n_open; i += WAVES) {
+          const uint64_t key = rescore(__builtin_amdgcn_readfirstlane(s.list_at[i]));
+          if (lane == 0) s.open[i] = key;
+        }
+        __syncthreads();
+        const uint64_t key = lane < n_open ? s.open[lane] : 0;
+        int rank = 0;
+        for (int i = 0; i < n_open; ++i) {          // (uniform)
+          const uint64_t o = from_lane(key, i);
+          rank += o > key || (o == key && i < lane) ? 1 : 0;
+        }
+        taken = __ballot(lane < n_open && rank < p.count - n_sure);
+      } else {
+        find_open();
+#pragma unroll
+        for (int k = 0; k < HELD; ++k) {
+          const int j = k * THREADS + tid;
+          yes[k] |= __ballot((maybe[k] >> lane & 1) && beyond(j));
+          maybe[k] = 0;
+        }
+        __syncthreads();                            // `sums` is free
+        count();
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < HELD; ++k) {
+      if (k * THREADS >= N) break;                  // uniform
+      const uint32_t row = at_row(k);
+      const int place = (int)(row >> 16) + __builtin_popcountll(maybe[k] & lower);   // among the open pages
+      const bool is = (yes[k] >> lane & 1) || ((maybe[k] >> lane & 1) && (place > 63 || (taken >> place & 1)));
+      // before it: the sure ones, and the open ones that are taken
+      const uint64_t ahead = place > 63 ? taken : taken & ((1ull << place) - 1);
+      const int more = taken == ~0ull ? place : __builtin_popcountll(ahead);
+      if (is) out[(row & 0xFFFF) + __builtin_popcountll(yes[k] & lower) + more] = ids[k];
     }
   } else {
+    for (int i0 = 0; i0 < N; i0 += THREADS) {       // how many are sure, and open
+      const int j = i0 + tid;
+      const float2 k = j < N ? scores[j] : make_float2(0.f, 0.f);
+      n_sure += __builtin_popcountll(__ballot(sure(j, k)));
+      n_open += __builtin_popcountll(__ballot(open(j, k)));
+    }
+    if (lane == 0) {
+      s.low[wave] = (uint32_t)n_sure;
+      s.high[wave] = (uint32_t)n_open;
+    }
+    __syncthreads();
+    n_sure = n_open = 0;
+    for (int w = 0; w < WAVES; ++w) {
+      n_sure += (int)s.low[w];
+      n_open += (int)s.high[w];
+    }
+    const bool all = n_sure + n_open <= p.count;
+    if (!all) find_open();
     int base = 0;
     for (int i0 = 0; i0 < N; i0 += THREADS) {
       const int j = i0 + tid;
-      const bool is = j < N && in(j, keys[j]);
+      const float2 k = j < N ? scores[j] : make_float2(0.f, 0.f);
+      const bool is = sure(j, k) || (open(j, k) && (all || beyond(j)));
       const uint64_t mask = __ballot(is);
       __syncthreads();
-      if (lane == 0) sums[wave] = __builtin_popcountll(mask);
+      if (lane == 0) s.sums[wave] = __builtin_popcountll(mask);
       __syncthreads();
-      int at = base + __builtin_popcountll(mask & below);
+      int at = base + __builtin_popcountll(mask & lower);
       for (int w = 0; w < WAVES; ++w) {
-        if (w < wave) at += sums[w];
-        base += sums[w];
+        if (w < wave) at += s.sums[w];
+        base += s.sums[w];
       }
       if (is) out[at] = entry(j);
     }
@@ -471,7 +651,7 @@ int64_t bounds_pages(const CacheBoundsArgs& a) {
   return n < a.ld_pages ? n : a.ld_pages;
 }
 
-size_t select_ws_bytes(int64_t B, int64_t T, int64_t hkv, int64_t width) { return (size_t)B * T * hkv * width * 8; }
+size_t select_ws_bytes(int64_t B, int64_t T, int64_t hkv, int64_t width) { return (size_t)B * T * hkv * width * 16; }
 
 int launch_select_pages(const SelectPagesArgs& a, hipStream_t stream) {
   SelectParams p{};
@@ -480,7 +660,6 @@ int launch_select_pages(const SelectPagesArgs& a, hipStream_t stream) {
   p.pages = a.pages;
   p.lens = a.lens;
   p.nodes = a.nodes;
-  p.keys = reinterpret_cast<uint64_t*>(a.ws);
   p.selected = a.selected;
   p.held = a.held;
   p.ldq = a.ldq;
@@ -495,6 +674,9 @@ int launch_select_pages(const SelectPagesArgs& a, hipStream_t stream) {
   const int64_t held = a.ld_pages * a.page;
   p.max_len = (int)(a.n_pages == 0 ? 0 : a.max_len < held ? a.max_len : held);
   p.width = (int)((p.max_len + a.page - 1) / a.page);
+  p.scores = reinterpret_cast<float2*>(a.ws);
+  p.keys = reinterpret_cast<uint64_t*>(p.scores + a.B * a.T * a.heads * p.width);
+  p.dim = (int)a.dim;
   p.count = (int)a.count;
   p.sinks = (int)a.sinks;
   p.recent = (int)a.recent;
@@ -513,9 +695,13 @@ int launch_select_pages(const SelectPagesArgs& a, hipStream_t stream) {
     if (hipGetLastError() != hipSuccess) return BSFP8_EHIP;
   }
   const dim3 grid((unsigned)(a.B * a.T * a.heads));
-  if (p.width <= 256 * PICK_HELD) hipLaunchKernelGGL((select_pick_kernel<256, true>), grid, dim3(256), 0, stream, p);
-  else if (p.width <= 1024 * PICK_HELD) hipLaunchKernelGGL((select_pick_kernel<1024, true>), grid, dim3(1024), 0, stream, p);
-  else hipLaunchKernelGGL((select_pick_kernel<1024, false>), grid, dim3(1024), 0, stream, p);
+  // Two scores a thread while that holds all of them, then eight; beyond 8192 pages they are read again. (A launch is as
+  // short as its code, which the instruction cache fetches anew: 8 lists of 2048 pages take 10.5 us with eight of
+  // 256 threads, 7.3 with two of 1024.)
+  if (p.width <= 256 * 2) hipLaunchKernelGGL((select_pick_kernel<256, 2>), grid, dim3(256), 0, stream, p);
+  else if (p.width <= 1024 * 2) hipLaunchKernelGGL((select_pick_kernel<1024, 2>), grid, dim3(1024), 0, stream, p);
+  else if (p.width <= 1024 * 8) hipLaunchKernelGGL((select_pick_kernel<1024, 8>), grid, dim3(1024), 0, stream, p);
+  else hipLaunchKernelGGL((select_pick_kernel<1024, 0>), grid, dim3(1024), 0, stream, p);
   return hip_status(hipGetLastError());
 }
 

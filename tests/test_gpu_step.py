@@ -576,3 +576,17 @@ def test_selection_of_very_many_pages(pages):
 def test_selection_about_the_ranked_number(left):
     for count in (4, 33, left - 1):
         choose(280 + left, 1, 2, 1, 64, 16, [(left + 3) * 16], count, attend=False)
+
+
+@pytest.mark.parametrize("pages", [40, 100, 900, 3000, 17000])
+def test_scores_closer_than_fp32_tells(pages):
+    """Scores of 256 and more that differ by 2^-20: the border lies among many that fp32 cannot tell apart."""
+    def near(qt, q, bounds, table, n):
+        r = np.random.default_rng(12)
+        x = np.zeros((n, 64))
+        x[:, 0], x[:, 7] = 256, r.integers(-60, 60, n) * 2.0 ** -20
+        x[::5, 3] = r.choice([-1.0, 1.0], len(x[::5]))
+        bounds.copy_(torch.from_numpy(x).to(torch.bfloat16).cuda()[:, None, None, :].expand_as(bounds))
+        qt[:], q[:] = 1, 1
+    for count in (4, pages // 3, pages // 2, pages - 5):
+        choose(290, 1, 3, 1, 64, 16, [pages * 16 - 3], count, change=near, attend=False)
