@@ -18,14 +18,23 @@
 //           workgroup ranks those, which gives the borders, and walks to the token.
 // A fourth writes the filtered logits where they are wanted. A list that does not fit (many equal logits) is replaced by
 // another look at the row: slow, but the same answer.
+//
+// What bounds it: reading is a small part (64 rows of 131072 fp32 columns, 34 MB, are read three times: 5.5 us of HBM, then
+// cache). In few rows it is the chain of dependent steps, so the last workgroups ask for what they need all at once, counters
+// lie in cache lines of their own, vectors below every border are passed over before any exponential, and long unrolled code
+// was rolled up, which takes longer to fetch than to run. In many rows it is fp64 exponentials and atomics to LDS and memory.
+// One row of 32768: 21 us a call (kernels 3.8 + 10.3 + 10); 64 of 131072: 47 (9.5 + 20.5 + 21 in a trace); 48 bf16 rows
+// of 32768 with the filtered logits: 40 (4.1 + 13.2 + 15 + 7.8).
 #include "logits.h"
 
 namespace bsfp8 {
 namespace {
 
 constexpr int BINS = 1024;
+constexpr int LINE = 32;                            // a counter has 128 bytes of its own: atomics of one line wait for each other
 constexpr int RANKED = 256;                         // elements that a workgroup ranks against each other
 constexpr int NEAR = 512;                           // border elements that a workgroup gathers
+constexpr int HELD_SUMS = 512;                      // pieces whose sums the last workgroup holds in LDS
 constexpr uint32_t NO_INDEX = 0xFFFFFF;
 
 struct PieceStat {
@@ -41,6 +50,7 @@ struct RowPlan {
   uint64_t sum_k;                                   // weights of the first k where kb < 0
   uint64_t border;                                  // elements from this one on are kept, too
   float M, scale, cut;                              // bin = (M - x) * scale; elements below cut are in none
+  float least, safe;                                // none below `least` is kept or in a border's bin; all from `safe` on are kept
   int sure;                                         // bins before this one are kept
   int p0, p1;                                       // bins that may hold the end of top-p's prefix (p0 > p1: known)
   int kb, need;                                     // bin that holds the k-th element (-1: known), and how many of its elements are in
@@ -50,7 +60,7 @@ struct SampleParams {
   const void* logits;
   const float *temperature, *top_p, *min_p, *u;
   const int32_t* top_k;
-  int* heads;                                       // [R][4]: workgroups arrived in bins, in pick; elements listed; the list is cut
+  int* heads;                                       // [R][4 * LINE]: workgroups arrived in bins, in pick; elements listed; the list is cut
   PieceStat* stats;                                 // [R][pieces]
   RowPlan* plans;                                   // [R]
   uint32_t* counts;                                 // [R][BINS]
@@ -60,7 +70,7 @@ struct SampleParams {
   void* filtered;
   int64_t ld, ldf;
   double one;                                       // 2^SH
-  int R, V, pieces, per, blocks, room;              // per: pieces of a wave
+  int R, V, pieces, per, room;                      // per: pieces of a wave of the bins
 };
 
 // A row's rules.
@@ -90,6 +100,8 @@ struct RowWeights {
   Weights f;
   __device__ __forceinline__ RowWeights(float M, double it, const double* powers) : f(M, it, powers) {}
   __device__ __forceinline__ double operator()(float x) const { return f.M < -NEG_INF ? f(x) : 0.0; }
+  // of an element between -inf and a finite M (what is below 2^-1000 is nothing to a sum)
+  __device__ __forceinline__ double plain(float x) const { return f.some(x); }
 };
 __device__ __forceinline__ uint64_t fixed(const SampleParams& p, double w) {   // w in [0, 1]
   return __builtin_bit_cast(uint64_t, fma(w, p.one, 0x1p52)) & 0xFFFFFFFFFFFFFull;
@@ -112,6 +124,25 @@ __device__ __forceinline__ int bin_of(float M, float scale, float cut, float x) 
   return M < -NEG_INF ? (int)fminf((M - x) * scale, (float)(BINS - 1)) : BINS - 1;
 }
 
+// Vectors and elements by rotation, so that their loops stay loops: these launches last about as long as their code takes to
+// be fetched, and an exponential is 200 bytes of it.
+template <typename V, int N>
+__device__ __forceinline__ V next(V (&w)[N]) {
+  const V first = w[0];
+#pragma unroll
+  for (int i = 0; i + 1 < N; ++i) w[i] = w[i + 1];
+  return first;
+}
+
+// Whether one of the wave's elements reaches a logit.
+template <int E>
+__device__ __forceinline__ bool any_from(const float (&x)[E], float least) {
+  float top = x[0];
+#pragma unroll
+  for (int e = 1; e < E; ++e) top = fmaxf(top, x[e]);
+  return __any(top >= least);
+}
+
 template <typename V>
 __device__ __forceinline__ V take(const V* at) { return __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
 template <typename V>
@@ -132,7 +163,7 @@ __global__ void __launch_bounds__(256) sample_stats_kernel(SampleParams p) {
   r.load(piece, lane, w);                           // (past the row's end: nothing is read)
   const Rules rules(p, row);
   // the row's counters and bins start at zero (where they lie depends on a call's sizes, so no call can leave them so)
-  if (blockIdx.y == 0 && threadIdx.x < 4) p.heads[row * 4 + threadIdx.x] = 0;
+  if (blockIdx.y == 0 && threadIdx.x < 4) p.heads[((int64_t)row * 4 + threadIdx.x) * LINE] = 0;
   if (rules.binned()) {
     for (int i = blockIdx.y * 256 + threadIdx.x; i < BINS; i += gridDim.y * 256) {
       p.counts[(int64_t)row * BINS + i] = 0;
@@ -219,15 +250,25 @@ __device__ __forceinline__ float cut_of(const SampleParams& p, const RowStat& st
     uint32_t key[8], at = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) key[i] = st.part[i] > NEG_INF ? key_of(st.part[i]) : 0;
-    auto reach = [&](uint32_t c) {
+    auto search = [&](auto reach) {
+#pragma unroll 1
+      for (uint32_t bit = 0x80000000u; bit >= 0x20000u; bit >>= 1)
+        if (reach(at | bit)) at |= bit;
+    };
+    // (128 parts tell nearly as much of a small k, with a quarter of the work)
+    uint32_t two[2] = {max(max(key[0], key[1]), max(key[2], key[3])), max(max(key[4], key[5]), max(key[6], key[7]))};
+    auto reach2 = [&](uint32_t c) {
+      return __builtin_popcountll(__ballot(two[0] >= c)) + __builtin_popcountll(__ballot(two[1] >= c)) >= rules.k;
+    };
+    auto reach8 = [&](uint32_t c) {
       int n = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) n += __builtin_popcountll(__ballot(key[i] >= c));
       return n >= rules.k;
     };
-    if (!reach(1)) return NEG_INF;                  // fewer parts than k
-    for (uint32_t bit = 0x80000000u; bit >= 0x10000u; bit >>= 1)
-      if (reach(at | bit)) at |= bit;
+    if (rules.k <= 64 && reach2(1)) search(reach2);
+    else if (reach8(1)) search(reach8);
+    else return NEG_INF;                            // fewer parts than k
     const uint32_t lowest = 0x00800000u;            // of the finite logits
     return of_key(at > lowest ? at : lowest);
   }
@@ -260,14 +301,14 @@ __device__ __forceinline__ Prefix block_scan(Prefix own, int lane, int wave, Pre
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256) sample_bins_kernel(SampleParams p) {
+__global__ void __launch_bounds__(256, 6) sample_bins_kernel(SampleParams p) {
   constexpr int E = Row<T>::E, N = Row<T>::N;
   __shared__ double powers[64];
   __shared__ uint32_t count[BINS];
   __shared__ uint64_t weight[BINS];
   __shared__ Prefix waves[4];
   __shared__ uint64_t found[4];
-  __shared__ int at[4], shared_last;
+  __shared__ int at[4], held[4], shared_last;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), row = blockIdx.x;
   const Rules rules(p, row);
   if (!rules.binned()) return;
@@ -287,24 +328,32 @@ __global__ void __launch_bounds__(256) sample_bins_kernel(SampleParams p) {
   const RowWeights f(st.M, rules.it, powers);
   __syncthreads();
   uint64_t rest = 0;
+  const bool sums = rules.use_p, all_sums = rules.use_p && rules.k == 0;
+#pragma unroll 1
   for (int i = 0; i < p.per && piece0 + i < p.pieces; ++i) {
-    float x[N][E];
-    r.get(w, piece0 + i, lane, x);
-    if (i + 1 < p.per) r.load(piece0 + i + 1, lane, w);
+    Words now[N];
 #pragma unroll
-    for (int v = 0; v < N; ++v)
+    for (int v = 0; v < N; ++v) now[v] = w[v];
+    if (i + 1 < p.per) r.load(piece0 + i + 1, lane, w);
+#pragma unroll 1
+    for (int v = 0; v < N; ++v) {
+      float x[E];
+      r.get(next(now), piece0 + i, lane, v, x);
+      const bool some = any_from(x, cut);           // (with a few rows kept, most vectors hold none)
+      if (!some && !all_sums) continue;
+      uint64_t n[E];
+      if (sums) {                                   // (M is finite then; NaN and -inf give nothing)
+#pragma unroll
+        for (int e = 0; e < E; ++e) n[e] = fixed(p, f.plain(x[e]));
+      }
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const int b = bin_of(st.M, scale, cut, x[v][e]);
-        if (rules.use_p) {
-          if (rules.k == 0 || __any(b < BINS)) {
-            const uint64_t n = fixed(p, f(x[v][e]));
-            if (b < BINS) atomicAdd((unsigned long long*)&weight[b], (unsigned long long)n);
-            else rest += n;
-          }
-        }
+        const int b = bin_of(st.M, scale, cut, x[e]);
         if (b < BINS) atomicAdd(&count[b], 1u);
+        if (sums && b < BINS) atomicAdd((unsigned long long*)&weight[b], (unsigned long long)n[e]);
+        else if (sums) rest += n[e];
       }
+    }
   }
   __syncthreads();
   uint32_t* counts = p.counts + (int64_t)row * BINS;
@@ -313,11 +362,11 @@ __global__ void __launch_bounds__(256) sample_bins_kernel(SampleParams p) {
     if (count[i]) add(counts + i, count[i]);
     if (weight[i]) add(weights + i, weight[i]);
   }
-  if (rules.use_p && rules.k == 0) {
+  if (all_sums) {
     rest = wave_sum(rest);
     if (lane == 0 && rest) add(p.rest + row, rest);
   }
-  if (!last_to_arrive(p.heads + row * 4, gridDim.y, &shared_last)) return;
+  if (!last_to_arrive(p.heads + (int64_t)row * 4 * LINE, gridDim.y, &shared_last)) return;
 
   // the row's bins: four a thread
   Prefix own[4], sum{0, 0}, all;
@@ -337,6 +386,7 @@ __global__ void __launch_bounds__(256) sample_bins_kernel(SampleParams p) {
       const Prefix next{run.n + own[i].n, run.w + own[i].w};
       if (own[i].n && !(run.n && reach(run)) && reach(next)) {
         at[slot] = threadIdx.x * 4 + i;
+        held[slot] = (int)own[i].n;
         found[slot] = run.w;
         if (slot == 0) {
           found[3] = (uint64_t)run.n << 32 | next.n;
@@ -385,41 +435,43 @@ __global__ void __launch_bounds__(256) sample_bins_kernel(SampleParams p) {
     pl.p1 = at[2] < 0 ? BINS - 1 : at[2];
     if (pl.kb >= 0) pl.p1 = min(pl.p1, pl.kb);
     pl.sure = pl.p0;
-    if (pl.p0 == pl.p1 && take(counts + pl.p0) == 1) {   // a single element: no border inside the bin
+    if (pl.p0 == pl.p1 && at[2] >= 0 && held[2] == 1) {   // a single element: no border inside the bin
       pl.sure = pl.p0 + 1;
       pl.kb = -1;
       pl.p0 = 1;
       pl.p1 = 0;
     }
   }
+  // (a whole bin further down than the last that matters)
+  const int end = max(pl.sure - 1, max(pl.kb, pl.p0 <= pl.p1 ? pl.p1 : -1));
+  pl.least = fmaxf(cut, st.M - (float)(end + 2) / scale);
+  if (!(bin_of(st.M, scale, cut, pl.least) > end)) pl.least = cut;
+  pl.safe = st.M - (float)(pl.sure - 2) / scale;
+  if (!(bin_of(st.M, scale, cut, pl.safe) < pl.sure)) pl.safe = __uint_as_float(0x7FC00000u);   // (none)
   if (threadIdx.x == 0) p.plans[row] = pl;
 }
 
 // ---------------------------------------------------------------------------------------------
 // pick
 // ---------------------------------------------------------------------------------------------
-// Elements in question: the row's list, or the row itself where the list has no room. each(f): f(place, bin) of the
-// thread's share of those in bins b0 .. b1 (and kb).
+// Elements in question: the row's list (the thread's own element of one that a workgroup ranks), or the row itself where the
+// list has no room. each(f): f(place) of the thread's share of those in bins b0 .. b1.
 template <typename T>
 struct Near {
   const SampleParams& p;
   const RowPlan& pl;
   int row, n;
   bool listed;
+  uint64_t own;
   template <typename F>
   __device__ __forceinline__ void each(int b0, int b1, F f) const {
-    if (listed) {
-      for (int i = threadIdx.x; i < n; i += 256) {
-        const uint64_t c = take(p.list + (int64_t)row * p.room + i);
-        const int b = bin_of(pl.M, pl.scale, pl.cut, place_logit(c));
-        if (b >= b0 && b <= b1) f(c);
-      }
-    } else {
-      for (int i = threadIdx.x; i < p.V; i += 256) {
-        const float x = element<T>(p.logits, row * p.ld + i);
-        const int b = bin_of(pl.M, pl.scale, pl.cut, x);
-        if (b >= b0 && b <= b1) f(place(x, i));
-      }
+    const int64_t end = listed ? n : p.V;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < end; i += 256) {
+      const uint64_t c = !listed ? place(element<T>(p.logits, row * p.ld + i), i)
+                         : n <= RANKED ? own : take(p.list + (int64_t)row * p.room + i);
+      const int b = bin_of(pl.M, pl.scale, pl.cut, place_logit(c));
+      if (b >= b0 && b <= b1) f(c);
     }
   }
 };
@@ -511,7 +563,11 @@ __device__ uint64_t find_border(const Near<T>& near, int b0, int b1, uint64_t fr
     __syncthreads();
   }
   __syncthreads();
-  if (threadIdx.x == 0) s.n = 0;
+  if (threadIdx.x == 0) {
+    s.n = 0;
+    s.result[0] = ~0ull;
+    s.result[1] = before.w;
+  }
   __syncthreads();
   near.each(b0, b1, [&](uint64_t c) {
     if (c < lo || c > hi) return;
@@ -544,11 +600,12 @@ __device__ uint64_t find_border(const Near<T>& near, int b0, int b1, uint64_t fr
 
 // The first piece whose running sum passes `target` (whole wave), the last with a sum if none does; `before` = the sum
 // before it.
-__device__ __forceinline__ int pick_piece(const uint64_t* sums, int pieces, int lane, double target, uint64_t& before) {
+template <typename F>
+__device__ __forceinline__ int pick_piece(F sum, int pieces, int lane, double target, uint64_t& before) {
   uint64_t base = 0, last_before = 0;
   int last = 0;
   for (int i0 = 0; i0 < pieces; i0 += 64) {
-    const uint64_t v = i0 + lane < pieces ? take(sums + i0 + lane) : 0;
+    const uint64_t v = i0 + lane < pieces ? sum(i0 + lane) : 0;
     const uint64_t run = wave_scan(v);
     const uint64_t past = __ballot(v > 0 && (double)(base + run) > target);
     const uint64_t some = __ballot(v > 0);
@@ -571,19 +628,20 @@ __device__ __forceinline__ bool in_prefix(const RowPlan& pl, float x, int index)
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256) sample_pick_kernel(SampleParams p) {
+__global__ void __launch_bounds__(256, 5) sample_pick_kernel(SampleParams p) {
   constexpr int E = Row<T>::E, N = Row<T>::N;
   __shared__ double powers[64];
   __shared__ FindShared fs;
   __shared__ uint64_t mine[NEAR];
-  __shared__ int n_mine, base, shared_last;
+  __shared__ uint64_t piece_sums[HELD_SUMS], vector_sums[4];
+  __shared__ int n_mine, base, shared_last, first[4], final[4];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), row = blockIdx.x;
   const Rules rules(p, row);
   if (rules.greedy && blockIdx.y > 0) return;
   const Row<T> r(p.logits, row * p.ld, p.V);
-  const int piece0 = (blockIdx.y * 4 + wave) * p.per;
+  const int piece = blockIdx.y * 4 + wave;
   Words w[N];
-  r.load(piece0, lane, w);
+  r.load(piece, lane, w);
   load_powers(powers);
   if (threadIdx.x == 0) n_mine = 0;
   RowPlan pl{};
@@ -592,10 +650,16 @@ __global__ void __launch_bounds__(256) sample_pick_kernel(SampleParams p) {
   } else {
     pl.M = row_stat(p, row, lane, rules).M;
     pl.border = ~0ull;
-    pl.cut = NEG_INF;
+    pl.cut = pl.least = pl.safe = NEG_INF;
     pl.kb = -1;
     pl.p0 = 1;
     pl.sure = BINS;
+  }
+  float heavy = NEG_INF;                            // elements below it fall to min-p, with room for the arithmetic's errors
+  if (rules.min_w > 0.0) {                          // (the borders are found among all elements)
+    const float d = rules.t * __logf((float)rules.min_w);
+    heavy = fmaxf(heavy, pl.M + d - (1e-3f * rules.t + 1e-5f * (fabsf(pl.M) + fabsf(d))));
+    if (!rules.binned()) pl.least = heavy;
   }
   if (!(pl.M > NEG_INF) || (!(pl.M < -NEG_INF) && (rules.greedy || rules.min_w > 0.0))) {   // nothing is kept
     pl.M = NEG_INF;
@@ -651,26 +715,39 @@ __global__ void __launch_bounds__(256) sample_pick_kernel(SampleParams p) {
 
   const RowWeights f(pl.M, rules.it, powers);
   // what is surely kept, by piece; what lies in the borders' bins, gathered
-  for (int i = 0; i < p.per && piece0 + i < p.pieces; ++i) {
-    float x[N][E];
-    const int piece = piece0 + i;
-    r.get(w, piece, lane, x);
-    if (i + 1 < p.per) r.load(piece + 1, lane, w);
+  if (piece < p.pieces) {
     uint64_t sum = 0;
-#pragma unroll
-    for (int v = 0; v < N; ++v)
+#pragma unroll 1
+    for (int v = 0; v < N; ++v) {
+      float x[E];
+      r.get(next(w), piece, lane, v, x);
+      if (!any_from(x, pl.least)) continue;
+      uint32_t sure = 0, maybe = 0;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const int b = bin_of(pl.M, pl.scale, pl.cut, x[v][e]);
-        if (__any(b < pl.sure)) {
-          const double y = f(x[v][e]);
-          if (b < pl.sure && y >= rules.min_w) sum += fixed(p, y);
-        }
-        if ((b >= pl.p0 && b <= pl.p1) || b == pl.kb) {
-          const int k = atomicAdd(&n_mine, 1);
-          if (k < NEAR) mine[k] = place(x[v][e], r.index(piece, lane, v, e));
+        const bool in = x[e] >= pl.safe && x[e] > NEG_INF;
+        sure |= (in && x[e] >= heavy ? 1u : 0u) << e;
+        maybe |= (!in && x[e] >= pl.least ? 1u : 0u) << e;
+      }
+      if (__any(maybe != 0)) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          if (!(maybe >> e & 1)) continue;
+          const int b = bin_of(pl.M, pl.scale, pl.cut, x[e]);
+          sure |= (b < pl.sure && x[e] >= heavy ? 1u : 0u) << e;
+          if ((b >= pl.p0 && b <= pl.p1) || b == pl.kb) {
+            const int k = atomicAdd(&n_mine, 1);
+            if (k < NEAR) mine[k] = place(x[e], r.index(piece, lane, v, e));
+          }
         }
       }
+      if (!__any(sure != 0)) continue;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const double y = f.plain(x[e]);
+        sum += (sure >> e & 1) && y >= rules.min_w ? fixed(p, y) : 0;
+      }
+    }
     sum = wave_sum(sum);
     if (lane == 0) give(sums + piece, sum);
   }
@@ -678,82 +755,100 @@ __global__ void __launch_bounds__(256) sample_pick_kernel(SampleParams p) {
   const int n = n_mine;
   if (n > 0) {
     if (threadIdx.x == 0) {
-      if (n > NEAR) give(p.heads + row * 4 + 3, 1);
-      base = add(p.heads + row * 4 + 2, n);
+      if (n > NEAR) give(p.heads + ((int64_t)row * 4 + 3) * LINE, 1);
+      base = add(p.heads + ((int64_t)row * 4 + 2) * LINE, n);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < min(n, NEAR); i += 256)
       if (base + i < p.room) give(p.list + (int64_t)row * p.room + base + i, mine[i]);
   }
-  if (!last_to_arrive(p.heads + row * 4 + 1, gridDim.y, &shared_last)) return;
+  if (!last_to_arrive(p.heads + ((int64_t)row * 4 + 1) * LINE, gridDim.y, &shared_last)) return;
 
-  // the borders
-  const int listed = take(p.heads + row * 4 + 2);
+  // the borders: list, its length and the pieces' sums asked for together
+  const uint64_t own = take(p.list + (int64_t)row * p.room + threadIdx.x);   // (there is room for more than 256)
+  const int listed = take(p.heads + ((int64_t)row * 4 + 2) * LINE);
+  const bool cut = take(p.heads + ((int64_t)row * 4 + 3) * LINE) != 0, in_lds = p.pieces <= HELD_SUMS;
+  if (in_lds)
+    for (int i = threadIdx.x; i < p.pieces; i += 256) piece_sums[i] = take(sums + i);
   if (listed != 0) {
-    const Near<T> near{p, pl, row, listed, listed <= p.room && take(p.heads + row * 4 + 3) == 0};
-    uint64_t from = 0, total = pl.sum_k, unused;
-    if (pl.kb >= 0) {
-      uint64_t in = 0;
-      from = find_border(near, pl.kb, pl.kb, 0, f, fs, in, [&](uint32_t m, uint64_t) { return m >= (uint32_t)pl.need; });
-      total = pl.before_k + in;
+    const Near<T> near{p, pl, row, listed, !cut && listed <= p.room, own};
+    uint64_t from = 0, total = pl.sum_k;
+#pragma unroll 1
+    for (int turn = 0; turn < 2; ++turn) {          // top-k's, then top-p's
+      const int b0 = turn ? pl.p0 : pl.kb, b1 = turn ? pl.p1 : pl.kb;
+      if (b0 < 0 || b0 > b1) continue;
+      const double target = pl.target_p * (double)total;
+      uint64_t in;
+      from = find_border(near, b0, b1, from, f, fs, in, [&](uint32_t m, uint64_t x) {
+        return turn ? (double)(pl.before_p + x) >= target : m >= (uint32_t)pl.need;
+      });
+      if (!turn) total = pl.before_k + in;
     }
     pl.border = from;
-    if (pl.p0 <= pl.p1) {
-      const double target = pl.target_p * (double)total;
-      pl.border = find_border(near, pl.p0, pl.p1, from, f, fs, unused,
-                              [&](uint32_t, uint64_t x) { return (double)(pl.before_p + x) >= target; });
-    }
     const int b0 = pl.p0 <= pl.p1 ? pl.p0 : pl.kb, b1 = pl.p0 <= pl.p1 ? pl.p1 : pl.kb;
+    __syncthreads();                                // (the sums are in LDS)
     near.each(b0, b1, [&](uint64_t c) {
       if (c < pl.border) return;
       const double y = f(place_logit(c));
-      if (y >= rules.min_w) add(sums + place_index(c) / PIECE, fixed(p, y));
+      if (!(y >= rules.min_w)) return;
+      const int piece = place_index(c) / PIECE;
+      if (in_lds) atomicAdd((unsigned long long*)&piece_sums[piece], (unsigned long long)fixed(p, y));
+      else add(sums + piece, fixed(p, y));
     });
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
   }
   if (threadIdx.x == 0) p.plans[row] = pl;
-  if (wave != 0) return;
+  __syncthreads();
+  // the token: its piece (every wave finds it), then a wave for each vector of that
+  auto sum_of = [&](int i) { return in_lds ? piece_sums[i] : take(sums + i); };
   uint64_t total = 0;
-  for (int i = lane; i < p.pieces; i += 64) total += take(sums + i);
+  for (int i = lane; i < p.pieces; i += 64) total += sum_of(i);
   total = wave_sum(total);
   const double target = (double)p.u[row] * (double)total;
   uint64_t before;
-  const int piece = pick_piece(sums, p.pieces, lane, target, before);
-  r.load(piece, lane, w);
-  float x[N][E];
-  r.get(w, piece, lane, x);
-  int found = -1, last = 0;
+  const int its = pick_piece(sum_of, p.pieces, lane, target, before);
+  uint64_t own_w[E], sum = 0;
+#pragma unroll
+  for (int e = 0; e < E; ++e) own_w[e] = 0;
+  if (wave < N) {
+    float x[E];
+    r.get(r.load(its, lane, wave), its, lane, wave, x);
 #pragma unroll 1
-  for (int v = 0; v < N; ++v) {
-    uint64_t own[E], sum = 0;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const double y = f(x[v][e]);
-      own[e] = y >= rules.min_w && in_prefix(pl, x[v][e], r.index(piece, lane, v, e)) ? fixed(p, y) : 0;
-      sum += own[e];
+    for (int e = 0; e < E; ++e) {                   // (own_w fills from its end, one place a round)
+      const float a = next(x);
+      const double y = f(a);
+      (void)next(own_w);
+      own_w[E - 1] = y >= rules.min_w && in_prefix(pl, a, r.index(its, lane, wave, e)) ? fixed(p, y) : 0;
+      sum += own_w[E - 1];
     }
-    const uint64_t run = wave_scan(sum);
-    uint64_t c = before + (run - sum);
-    int hit = -1, pos = -1;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      c += own[e];
-      pos = own[e] > 0 ? e : pos;
-      hit = hit < 0 && own[e] > 0 && (double)c > target ? e : hit;
-    }
-    const uint64_t hits = __ballot(hit >= 0), some = __ballot(pos >= 0);
-    if (found < 0 && hits) {
-      const int l = __builtin_ctzll(hits);
-      found = r.index(piece, l, v, 0) + __builtin_amdgcn_readlane(hit, l);
-    }
-    if (some) {
-      const int l = 63 - __builtin_clzll(some);
-      last = r.index(piece, l, v, 0) + __builtin_amdgcn_readlane(pos, l);
-    }
-    before += from_lane(run, 63);
   }
-  if (lane == 0) p.tokens[row] = found >= 0 ? found : last;
+  const uint64_t run = wave_scan(sum);
+  if (lane == 63) vector_sums[wave] = run;
+  __syncthreads();
+  for (int v = 0; v < wave; ++v) before += vector_sums[v];
+  uint64_t c = before + (run - sum);
+  int hit = -1, pos = -1;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    c += own_w[e];
+    pos = own_w[e] > 0 ? e : pos;
+    hit = hit < 0 && own_w[e] > 0 && (double)c > target ? e : hit;
+  }
+  const uint64_t hits = __ballot(hit >= 0), some = __ballot(pos >= 0);
+  const int hl = hits ? __builtin_ctzll(hits) : 0, pl_ = some ? 63 - __builtin_clzll(some) : 0;
+  if (lane == 0) {
+    first[wave] = hits ? r.index(its, hl, wave, 0) + __builtin_amdgcn_readlane(hit, hl) : -1;
+    final[wave] = some ? r.index(its, pl_, wave, 0) + __builtin_amdgcn_readlane(pos, pl_) : -1;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int token = -1, end = 0;
+    for (int v = 0; v < 4; ++v) {
+      token = token < 0 ? first[v] : token;
+      end = final[v] >= 0 ? final[v] : end;
+    }
+    p.tokens[row] = token >= 0 ? token : end;
+  }
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -773,22 +868,34 @@ __global__ void __launch_bounds__(256) sample_filter_kernel(SampleParams p) {
   load_powers(powers);
   __syncthreads();
   if (piece >= p.pieces) return;
-  float x[N][E];
-  r.get(w, piece, lane, x);
   const RowWeights f(pl.M, rules.it, powers);
   T* out = reinterpret_cast<T*>(p.filtered) + row * p.ldf;
   const bool whole = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
-#pragma unroll
+#pragma unroll 1
   for (int v = 0; v < N; ++v) {
     const int at = r.index(piece, lane, v, 0);
+    float x[E];
+    r.get(next(w), piece, lane, v, x);
+    uint32_t keep = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) keep |= (in_prefix(pl, x[e], at + e) ? 1u : 0u) << e;
+    if (rules.min_w > 0.0 && !rules.greedy) {
+      uint32_t drop = 0, ask = keep;
+#pragma unroll 1
+      while (__any(ask != 0)) {
+        const int e = __builtin_ctz(ask | 1u << 31);
+        float y = x[0];
+#pragma unroll
+        for (int o = 1; o < E; ++o) y = e == o ? x[o] : y;
+        if (ask && !(f(y) >= rules.min_w)) drop |= 1u << e;
+        ask &= ask - 1;
+      }
+      keep &= ~drop;
+    }
     if (at >= p.V) continue;
     uint32_t o[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      bool keep = in_prefix(pl, x[v][e], at + e);
-      if (rules.min_w > 0.0 && !rules.greedy) keep = keep && f(x[v][e]) >= rules.min_w;
-      o[e] = __float_as_uint(keep ? x[v][e] : NEG_INF);
-    }
+    for (int e = 0; e < E; ++e) o[e] = __float_as_uint(keep >> e & 1 ? x[e] : NEG_INF);
     if (whole && at + E <= p.V) {
       u32x4_t b;
 #pragma unroll
@@ -813,7 +920,7 @@ inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 size_t sample_ws_bytes(int64_t R, int64_t V) {
   const size_t r = (size_t)R, pieces = (size_t)pieces_of(V);
-  return align256(r * 16) + align256(r * pieces * sizeof(PieceStat)) + align256(r * sizeof(RowPlan)) + align256(r * BINS * 4) +
+  return align256(r * 16 * LINE) + align256(r * pieces * sizeof(PieceStat)) + align256(r * sizeof(RowPlan)) + align256(r * BINS * 4) +
          align256(r * BINS * 8) + align256(r * 8) + align256(r * pieces * 8) + r * (size_t)room_of(V) * 8;
 }
 
@@ -844,7 +951,7 @@ int launch_sample(const SampleArgs& a, hipStream_t stream) {
     ws += align256(n);
     return at;
   };
-  p.heads = reinterpret_cast<int*>(next(r * 16));
+  p.heads = reinterpret_cast<int*>(next(r * 16 * LINE));
   p.stats = reinterpret_cast<PieceStat*>(next(r * pieces * sizeof(PieceStat)));
   p.plans = reinterpret_cast<RowPlan*>(next(r * sizeof(RowPlan)));
   p.counts = reinterpret_cast<uint32_t*>(next(r * BINS * 4));
@@ -852,21 +959,26 @@ int launch_sample(const SampleArgs& a, hipStream_t stream) {
   p.rest = reinterpret_cast<uint64_t*>(next(r * 8));
   p.sums = reinterpret_cast<uint64_t*>(next(r * pieces * 8));
   p.list = reinterpret_cast<uint64_t*>(ws);
-  const int64_t all = a.R * ((p.pieces + 3) / 4);
-  p.per = all > 8192 ? 4 : all > 4096 ? 2 : 1;
-  const unsigned blocks = (unsigned)((p.pieces + 3) / 4), shares = (unsigned)((p.pieces + 4 * p.per - 1) / (4 * p.per));
-  const dim3 grid((unsigned)a.R, blocks), fewer((unsigned)a.R, shares);
+  const unsigned blocks = (unsigned)((p.pieces + 3) / 4);
+  const dim3 grid((unsigned)a.R, blocks);
   const bool rules = a.top_k || a.top_p;
   if (a.f32) hipLaunchKernelGGL(sample_stats_kernel<float>, grid, dim3(256), 0, stream, p);
   else hipLaunchKernelGGL(sample_stats_kernel<uint16_t>, grid, dim3(256), 0, stream, p);
   if (hipGetLastError() != hipSuccess) return BSFP8_EHIP;
   if (rules) {
-    if (a.f32) hipLaunchKernelGGL(sample_bins_kernel<float>, fewer, dim3(256), 0, stream, p);
-    else hipLaunchKernelGGL(sample_bins_kernel<uint16_t>, fewer, dim3(256), 0, stream, p);
+    // A workgroup of the bins adds up to 2048 sums to the row's, so more of them than the GPU holds at once take more of a row
+    // each. By one, two and four pieces a wave: 64 rows of 131072 fp32 columns (2048 workgroups by one) 26.0, 20.6 and 22.4
+    // us; 256 rows 53.4, 43.9 and 44.9; 1024 rows 190, 142 and 122.
+    const int64_t all = a.R * blocks;
+    SampleParams b = p;
+    b.per = all > 8192 ? 4 : all > 1024 ? 2 : 1;
+    const dim3 bins((unsigned)a.R, (unsigned)((p.pieces + 4 * b.per - 1) / (4 * b.per)));
+    if (a.f32) hipLaunchKernelGGL(sample_bins_kernel<float>, bins, dim3(256), 0, stream, b);
+    else hipLaunchKernelGGL(sample_bins_kernel<uint16_t>, bins, dim3(256), 0, stream, b);
     if (hipGetLastError() != hipSuccess) return BSFP8_EHIP;
   }
-  if (a.f32) hipLaunchKernelGGL(sample_pick_kernel<float>, fewer, dim3(256), 0, stream, p);
-  else hipLaunchKernelGGL(sample_pick_kernel<uint16_t>, fewer, dim3(256), 0, stream, p);
+  if (a.f32) hipLaunchKernelGGL(sample_pick_kernel<float>, grid, dim3(256), 0, stream, p);
+  else hipLaunchKernelGGL(sample_pick_kernel<uint16_t>, grid, dim3(256), 0, stream, p);
   if (hipGetLastError() != hipSuccess) return BSFP8_EHIP;
   if (a.filtered) {
     if (a.f32) hipLaunchKernelGGL(sample_filter_kernel<float>, grid, dim3(256), 0, stream, p);
