@@ -1,0 +1,131 @@
+"""Continuous batching of a small random model on one GPU, every step of it through the library.
+
+    python examples/serving.py [--places B] [--requests N] [--pages C] [--dense]
+
+The decoder of speculative.py behind a pool of cache pages. Requests come and go: a step gives each place of the batch up to
+CHUNK tokens of its prompt, or the token that it generated last, and takes pages from the pool as it needs them; a request
+that has ended gives its pages back. The lengths are all that the host decides (a request is let in once the pool holds
+its longest length), so nothing waits for the GPU before the end. Prompts attend to all of their tokens. Tokens that are
+generated attend to C pages for each key/value head: the first, the latest and those whose keys' bounds allow the largest
+scores (--dense: to all). Each request has its own sampling rules.
+"""
+import argparse
+import os
+import sys
+from collections import deque, namedtuple
+
+import torch
+
+sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
+from speculative import DIM, HKV, HQ, L, LAYERS, Model, PAGE, VOCAB, WIDTH  # noqa: E402
+
+CHUNK = 16
+Request = namedtuple("Request", "prompt new temperature top_k top_p min_p", defaults=(0.0, 0, 1.0, 0.0))
+
+
+class Server:
+    """Places for `places` requests of up to `longest` tokens over a pool of `pool` pages."""
+
+    def __init__(self, model, places, longest, pool, count=8, dense=False, seed=0):
+        self.model, self.places, self.count, self.dense = model, places, count, dense
+        dev = self.dev = model.device
+        width = (longest + PAGE - 1) // PAGE
+        zeros = lambda *s: torch.zeros(s, dtype=torch.int32, device=dev)
+        self.caches = [L.KVCache.empty(pool, HKV, PAGE, DIM, device=dev) for _ in range(LAYERS)]
+        self.bounds = [torch.zeros(pool, HKV, 2, DIM, dtype=torch.bfloat16, device=dev) for _ in range(LAYERS)]
+        self.pages = zeros(places, width) - 1
+        self.free = torch.arange(pool, dtype=torch.int32, device=dev)
+        self.n_free = zeros(1) + pool
+        self.lens, self.last = zeros(places), zeros(places)
+        self.norm_weight = torch.ones(WIDTH, dtype=torch.bfloat16, device=dev)
+        self.ws_select = L.workspace_select(places, 1, HKV, width, device=dev)
+        self.ws_attention = L.workspace_attention(places, 1, HQ, HKV, DIM, min(count, width) * PAGE, device=dev)
+        self.ws_sample = L.workspace_sample(places, VOCAB, device=dev)
+        self.g = torch.Generator(device=dev)
+        self.g.manual_seed(seed)
+
+    def attend(self, i, q, held, nodes):
+        """q bf16 [B, T, HQ, DIM] -> [B, T, HQ, DIM]"""
+        if q.shape[1] > 1 or self.dense:
+            return L.bsfp8_tree_attention(q, self.caches[i], self.pages, held, nodes=nodes)
+        count = min(self.count, self.pages.shape[1])
+        selected, n = L.bsfp8_select_pages(q, self.bounds[i], self.pages, held, count, PAGE, nodes=nodes, ws=self.ws_select)
+        return L.bsfp8_sparse_attention(q[:, 0], self.caches[i], selected, n, ws=self.ws_attention).unsqueeze(1)
+
+    def step(self, tokens, given, nodes, new_lens, rules):
+        """A step of T tokens a place. tokens int32 [B, T] from prompts where `given` [B, 1], else the last one generated;
+        nodes int32 [B]: how many of them count; new_lens int32 [B]: the lengths after it (0: the request has ended)."""
+        m, (B, T) = self.model, tokens.shape
+        t = L.bsfp8_step_tables(self.pages, self.lens, new_lens, self.free, self.n_free, PAGE, B * T, T)
+        ids = torch.where(given, tokens, self.last[:, None])
+        h, x = L.bsfp8_residual_norm(m.embed[ids.flatten().long()].float(), weight=self.norm_weight)
+        for i in range(LAYERS):
+            q, k, v = L.bsfp8_gemm(x, *m.qkv[i]).squeeze(1).split([HQ * DIM, HKV * DIM, HKV * DIM], 1)
+            q = L.bsfp8_cache_write(self.caches[i], t.slots, k, v, q=q, q_weight=m.weight, k_weight=m.weight, cos_sin=m.cos_sin,
+                                    positions=t.positions)
+            L.bsfp8_cache_bounds(self.caches[i], self.pages, t.held, self.bounds[i], first=self.lens, max_new=T)
+            y = self.attend(i, q.view(B, T, HQ, DIM), t.held, nodes)
+            o = L.bsfp8_gemm(y.reshape(B * T, HQ * DIM), *m.o[i]).squeeze(1)
+            h, x = L.bsfp8_residual_norm(h, o, weight=self.norm_weight, h_out=h)
+        at = torch.arange(B, device=self.dev) * T + (nodes.long() - 1).clamp(min=0)
+        logits = L.bsfp8_gemm(x[at], *m.head, out_dtype="f32").squeeze(1)
+        u = torch.rand(B, generator=self.g, device=self.dev)
+        self.last = L.bsfp8_sample(logits, rules[0], u, rules[1], rules[2], rules[3], ws=self.ws_sample)
+        self.lens = t.held
+        return self.last
+
+    def serve(self, requests):
+        """The tokens that each request generated, in the requests' order."""
+        B, dev, pool = self.places, self.dev, self.free.numel()
+        need = [(len(r.prompt) + r.new + PAGE - 1) // PAGE for r in requests]
+        if any(n > min(pool, self.pages.shape[1]) for n in need):
+            raise ValueError("a request is longer than the pool or the table")
+        waiting, at, done, taken = deque(range(len(requests))), [None] * B, [0] * B, 0
+        made, where, idle = [], [], Request([], 0)
+        while waiting or any(a is not None for a in at) or any(done):
+            ended = [False] * B
+            for b in range(B):
+                if at[b] is not None and done[b] == len(requests[at[b]].prompt) + requests[at[b]].new - 1:
+                    taken -= need[at[b]]
+                    at[b], done[b], ended[b] = None, 0, True
+            for b in range(B):                           # (a place that ends gives its pages back first)
+                if at[b] is None and not ended[b] and waiting and taken + need[waiting[0]] <= pool:
+                    at[b] = waiting.popleft()
+                    taken += need[at[b]]
+            run = [requests[a] if a is not None else idle for a in at]
+            n = [min(CHUNK, len(r.prompt) - d) if d < len(r.prompt) else int(a is not None) for r, d, a in zip(run, done, at)]
+            T = CHUNK if max(n) > 1 else 1
+            piece = [(list(r.prompt[d:d + k]) + [0] * T)[:T] for r, d, k in zip(run, done, n)]
+            given = [[d < len(r.prompt)] for r, d in zip(run, done)]
+            done = [d + k for d, k in zip(done, n)]
+            on = lambda x, dtype: torch.tensor(x, dtype=dtype).pin_memory().to(dev, non_blocking=True)
+            rules = [on([getattr(r, f) for r in run], torch.int32 if f == "top_k" else torch.float32) for f in Request._fields[2:]]
+            made.append(self.step(on(piece, torch.int32), on(given, torch.bool), on(n, torch.int32), on(done, torch.int32), rules))
+            where.append([a if a is not None and d >= len(requests[a].prompt) else None for a, d in zip(at, done)])
+        out = [[] for _ in requests]
+        for step, places in zip(torch.stack(made).tolist() if made else [], where):
+            for token, a in zip(step, places):
+                if a is not None:
+                    out[a].append(token)
+        return out
+
+
+def main():
+    ap = argparse.ArgumentParser()
+    ap.add_argument("--places", type=int, default=8)
+    ap.add_argument("--requests", type=int, default=20)
+    ap.add_argument("--pages", type=int, default=8, help="that a generated token attends to, for each key/value head")
+    ap.add_argument("--dense", action="store_true")
+    a = ap.parse_args()
+    g = torch.Generator().manual_seed(1)
+    draw = lambda lo, hi: int(torch.randint(lo, hi, (1,), generator=g))
+    rules = [dict(), dict(temperature=0.8, top_k=40), dict(temperature=1.0, top_p=0.9), dict(temperature=0.7, min_p=0.05)]
+    requests = [Request(torch.randint(0, VOCAB, (draw(1, 300),), generator=g).tolist(), draw(1, 100), **rules[i % 4])
+                for i in range(a.requests)]
+    server = Server(Model(), a.places, 400, a.places * 20, a.pages, a.dense)
+    for r, text in zip(requests, server.serve(requests)):
+        print(len(r.prompt), text)
+
+
+if __name__ == "__main__":
+    main()

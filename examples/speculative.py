@@ -1,13 +1,15 @@
 """Speculative decoding of a small random model on one GPU, every step of it through the library.
 
     python examples/speculative.py [--mode chain|tree|plain] [--temperature T] [--rounds N]
+                                     [--top-k K] [--top-p P] [--min-p P]
 
 A two-layer decoder with MXFP8 key/value caches and e4m3 twin weights. The drafter is the same model left after its
 first layer, so both share that layer's cache. A round drafts a chain of five tokens (or a tree of seven nodes: two
 guesses after the root and after each of them), runs root and drafts through the whole model in one pass, verifies them
 against the target's logits, and keeps what was accepted: a tree's accepted nodes are moved to the sequence's end by
 reading their cache rows and writing them back, which reproduces codes and scales bit for bit. Nothing waits for the GPU
-inside a round. At temperature 0 the tokens are those of plain decoding.
+inside a round. At temperature 0 the tokens are those of plain decoding. Rules (top-k, top-p, min-p) filter drafts' and
+target's logits alike, so what stands is distributed as the filtered target.
 """
 import argparse
 import os
@@ -75,7 +77,7 @@ PARENTS, DEPTH = [-1, 0, 0, 1, 1, 2, 2], [0, 1, 1, 2, 2, 2, 2]
 MASKS = [1 << i | (1 << p | 1 if p >= 0 else 0) for i, p in enumerate(PARENTS)]
 
 
-def generate(model, prompt, rounds, mode="chain", temperature=0.0, seed=0, drafts=5):
+def generate(model, prompt, rounds, mode="chain", temperature=0.0, seed=0, drafts=5, top_k=0, top_p=1.0, min_p=0.0):
     """prompt int32 [B, P] -> the tokens that each sequence generated in `rounds` rounds, and how many drafts a round
     were accepted on the average."""
     dev, (B, P) = model.device, prompt.shape
@@ -89,7 +91,15 @@ def generate(model, prompt, rounds, mode="chain", temperature=0.0, seed=0, draft
     rand = lambda *s: torch.rand(*s, generator=g, device=dev)
     i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=dev).expand(B, -1).contiguous()
 
-    def sample(logits):                                  # [B, n, VOCAB] -> int32 [B, n]
+    rules = temperature > 0 and (top_k > 0 or top_p < 1 or min_p > 0)
+
+    def sample(logits):                                  # [B, n, VOCAB], filtered by the rules -> int32 [B, n]
+        if rules:
+            R = logits.shape[0] * logits.shape[1]
+            every = lambda x, dtype: torch.full((R,), x, dtype=dtype, device=dev)
+            rows = logits.view(R, VOCAB)
+            return L.bsfp8_sample(rows, every(temperature, torch.float32), rand(R), every(top_k, torch.int32),
+                                  every(top_p, torch.float32), every(min_p, torch.float32), filtered=rows).view(logits.shape[:2])
         if temperature == 0:
             return logits.argmax(-1).to(torch.int32)
         p = torch.softmax(logits / temperature, -1)
@@ -98,7 +108,7 @@ def generate(model, prompt, rounds, mode="chain", temperature=0.0, seed=0, draft
     lens = torch.zeros(B, dtype=torch.int32, device=dev)
     logits = model.forward(caches, pages, prompt, lens, torch.arange(P, device=dev).expand(B, P))
     lens = lens + P
-    out, accepted = [sample(logits[:, -1:])], []
+    out, accepted = [sample(logits[:, -1:].contiguous())], []
     root = out[0]
     ws = L.workspace_verify(B, T, VOCAB, device=dev)
     parents, masks = i32(PARENTS), torch.tensor(MASKS, device=dev).expand(B, -1).contiguous()
@@ -114,6 +124,8 @@ def generate(model, prompt, rounds, mode="chain", temperature=0.0, seed=0, draft
                 best = lg[:, n // 2:].topk(2, -1).indices.flatten(1)
                 tokens = torch.cat([tokens, best.to(torch.int32)], 1)
             logits = model.forward(caches, pages, tokens, lens, first + depth, mask=masks)
+            if rules:
+                sample(logits)
             got, path, n = L.bsfp8_verify_tree(logits, tokens, parents, t, rand(B, T), ws=ws)
             # the accepted nodes' rows, one after another from the sequence's end
             src = slots_of(pages, torch.where(path >= 0, first + path, -1)).flatten()
@@ -128,6 +140,8 @@ def generate(model, prompt, rounds, mode="chain", temperature=0.0, seed=0, draft
             draft = torch.cat(draft, 1) if draft else torch.empty(B, 0, VOCAB, device=dev)
             tokens = torch.cat(tokens, 1)
             logits = model.forward(caches, pages, tokens, lens, first + row)
+            if rules:
+                sample(logits)
             got, n = L.bsfp8_verify_chain(logits, draft, tokens[:, 1:].contiguous(), t, rand(B, T - 1), rand(B), ws=ws)
         lens = lens + n + 1
         root = got.gather(1, n[:, None].long())
@@ -141,11 +155,14 @@ def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--mode", choices=("plain", "chain", "tree"), default="chain")
     ap.add_argument("--temperature", type=float, default=0.0)
+    ap.add_argument("--top-k", type=int, default=0, help="0: all")
+    ap.add_argument("--top-p", type=float, default=1.0, help="1: all")
+    ap.add_argument("--min-p", type=float, default=0.0, help="0: all")
     ap.add_argument("--rounds", type=int, default=24, help="each gives at least one token a sequence")
     a = ap.parse_args()
     model = Model()
     prompt = torch.randint(0, VOCAB, (2, 12), generator=torch.Generator().manual_seed(1)).to(torch.int32).cuda()
-    text, mean = generate(model, prompt, a.rounds, a.mode, a.temperature)
+    text, mean = generate(model, prompt, a.rounds, a.mode, a.temperature, top_k=a.top_k, top_p=a.top_p, min_p=a.min_p)
     for s in text:
         print(s)
     print(f"{mean:.2f} drafts accepted a round")
