@@ -745,8 +745,8 @@ int bsfp8_residual_norm(const void* h, int64_t ldh, int h_dtype, const uint16_t*
   if (R < 0 || R >= ((int64_t)1 << 31) || W < 8 || W % 8 || W > 32768) return BSFP8_ESHAPE;
   if ((xq || xs) && W % 32) return BSFP8_ESHAPE;
   if (!(eps >= 0.f) || eps > 3.4e38f || !(scale - scale == 0.f)) return BSFP8_EINVAL;
-  if ((xq != nullptr) != (xs != nullptr) || (!h_out && !x_out && !xq) || (!y && (gate || post_weight))) return BSFP8_EINVAL;
   if (R == 0) return BSFP8_OK;
+  if ((xq != nullptr) != (xs != nullptr) || (!h_out && !x_out && !xq) || (!y && (gate || post_weight))) return BSFP8_EINVAL;
   if (!h) return BSFP8_EINVAL;
   const int f32 = h_dtype == BSFP8_OUT_F32;
   const int64_t size = f32 ? 4 : 2, unit = 16 / size;
