@@ -5,7 +5,7 @@
 // in fp32, rounded once where it is stored: x is the norm of h' before its rounding.
 //
 // A row is held in registers by a workgroup (or by one wave, if it is short), so every value is read and written once; the
-// two means are the only exchanges. HBM bounds many rows (8191 of 5120: 86 us with an fp32 residual and MXFP8 out, 5.4 TB/s;
+// two means are the only exchanges. HBM bounds many rows (8191 of 5120: 88 us with an fp32 residual and MXFP8 out, 5.2 TB/s;
 // 63 us in bf16, 5.3), the latency of one chain (load, two sums, store) few: 4 us for 6 rows. A workgroup keeps the weights of
 // its columns for all its rows and, but for the widest rows, asks for the next row before it computes this one.
 

@@ -23,8 +23,9 @@
 // cache). In few rows it is the chain of dependent steps, so the last workgroups ask for what they need all at once, counters
 // lie in cache lines of their own, vectors below every border are passed over before any exponential, and long unrolled code
 // was rolled up, which takes longer to fetch than to run. In many rows it is fp64 exponentials and atomics to LDS and memory.
-// One row of 32768: 21 us a call (kernels 3.8 + 10.3 + 10); 64 of 131072: 47 (9.5 + 20.5 + 21 in a trace); 48 bf16 rows
-// of 32768 with the filtered logits: 40 (4.1 + 13.2 + 15 + 7.8).
+// One row of 32768: 22 us a call (kernels 3.9 + 10.6 + 10.6 in a trace); 64 of 131072: 47 to 53 (9.8 + 20.3 + 19.6); 48 bf16
+// rows of 32768 with the filtered logits: 40 (4.3 + 12.7 + 15 + 7.9). One workgroup for all of a row of up to 32768 columns,
+// which saves the hand-overs, is no faster: its CU's fp64 rate and 64-bit LDS atomics take 27 us for the one row, 53 for the 48.
 #include "logits.h"
 
 namespace bsfp8 {
