@@ -78,6 +78,8 @@ class Server:
         """The tokens that each request generated, in the requests' order."""
         B, dev, pool = self.places, self.dev, self.free.numel()
         need = [(len(r.prompt) + r.new + PAGE - 1) // PAGE for r in requests]
+        if any(not r.prompt or r.new < 1 for r in requests):
+            raise ValueError("a request needs a prompt and a token to generate")
         if any(n > min(pool, self.pages.shape[1]) for n in need):
             raise ValueError("a request is longer than the pool or the table")
         waiting, at, done, taken = deque(range(len(requests))), [None] * B, [0] * B, 0

@@ -90,6 +90,12 @@ def test_what_cannot_be_served(ex, model):
         ex.Server(model, 2, 64, 30).serve([ex.Request([1] * 60, 20)])
 
 
+def test_requests_of_nothing_are_refused(ex, model):
+    for r in (ex.Request([], 5), ex.Request([1, 2], 0), ex.Request([3], -1)):
+        with pytest.raises(ValueError):
+            ex.Server(model, 2, 64, 8).serve([ex.Request([1], 1), r])
+
+
 @pytest.mark.parametrize("mode", ["plain", "chain", "tree"])
 def test_the_largest_logit_alone_is_greedy(ex, model, mode):
     import speculative
